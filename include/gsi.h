@@ -276,6 +276,92 @@ size_t gsi_calibrate_status_offset(void);
  * initial contents except a zero status word. */
 gsi_status gsi_calibrate(const gsi_calib *c, void *ws, size_t ws_bytes, void *stream);
 
+/* ---- plain linear maps: weights in 4 bits, weights of many experts ----
+ * The maps of a transformer that carry no basis: y = W x with W dense, or
+ * with W in 4 bits (a quarter of the bytes that a decode step reads), for
+ * one map or for the n maps of a mixture of experts.
+ *
+ * Conventions of these entry points, beside those above
+ *   - No workspace and no state: calls on different streams never meet.
+ *   - x and y are given with row strides ldx and ldy in elements, multiples
+ *     of 16 bytes; only the d (d_out) leading elements of a row are touched.
+ *   - y must not overlap any input.
+ *   - A token with Inf or NaN gives outputs that are not finite; the other
+ *     tokens are unaffected.
+ *
+ * Weights.  bits = 0: W [n][d_out][d] in `dtype`, map i starting i * stride
+ * elements after W (stride >= d_out * d).  bits = 4: w = scale (code - zero):
+ *   W      : codes [n][d_out][d / 2], one byte for two columns, the even one
+ *            in the low nibble
+ *   scales : [n][d_out][ceil(d / group)] in `dtype`
+ *   zeros  : [n][d_out][ceil(d / group)] bytes, 0..15 (only the low four bits
+ *            are read), or NULL for 8 everywhere
+ *   group  : 32, 64 or 128 columns of a row per scale; the last group of a
+ *            row may be shorter
+ * d is a multiple of 8 (bits = 0) or 32 (bits = 4), at most 2^20; d_out a
+ * multiple of 8, at most 2^24; W 16-byte aligned, stride a multiple of 16
+ * bytes.  Products accumulate in fp32: codes and bf16 values multiply
+ * exactly, a group's scale multiplies the group's fp32 sum, and y is
+ * rounded once.  With 4-bit weights and |x| near the largest fp32 value the
+ * sum 32 sum |x| of a group must itself stay finite. */
+typedef struct gsi_weights {
+  int32_t d;
+  int32_t d_out;
+  int32_t n;       /* maps (experts); 1 for a single map                     */
+  int32_t dtype;   /* gsi_dtype of x, y, and of W (bits 0) or scales (bits 4) */
+  int32_t bits;    /* 0 or 4                                                 */
+  int32_t group;   /* bits = 4: 32, 64 or 128; otherwise 0                   */
+  int64_t stride;  /* bits = 0: elements between maps; otherwise 0           */
+  const void *W;
+  const void *scales;
+  const uint8_t *zeros;
+} gsi_weights;
+
+/* y = W x for T tokens through one map in 4 bits (n = 1, bits = 4).
+ * x [T] rows, y [T] rows; T == 0 is a no-op. */
+gsi_status gsi_q4_linear(const gsi_weights *w, const void *x, int64_t ldx, void *y, int64_t ldy,
+                         int32_t T, void *stream);
+
+/* The maps of many experts on rows ordered by expert: for every expert e and
+ * every r in [offsets[e], offsets[e + 1]), y row r = W_e x row rows[r].
+ *   offsets : [n + 1] int32 (device), nondecreasing within [0, R]
+ *   rows    : [R] int32 (device), the x row of each y row, or NULL for r
+ *             itself; an entry outside [0, T) gives a y row of zeros
+ *   T       : rows of x;  R : rows of y (and of `rows`)
+ * Rows of y outside [offsets[0], offsets[n]) are left as they were.  The
+ * offsets are read on the device: nothing waits for them on the host, and
+ * entries outside [0, R] are clamped to it.  R == 0 is a no-op. */
+gsi_status gsi_grouped_linear(const gsi_weights *w, const void *x, int64_t ldx, int32_t T,
+                              const int32_t *offsets, const int32_t *rows, void *y, int64_t ldy,
+                              int32_t R, void *stream);
+
+/* Order the choices of T tokens by expert.  ids [T][top] holds expert
+ * numbers, int32 or int64 (ids_bytes 4 or 8); a number outside [0, n) drops
+ * the choice.  Choice (t, j) has the flat index t * top + j; the kept
+ * choices are ordered by expert and, within one, by flat index.
+ *   offsets : [n + 1] int32, the first grouped row of each expert and, last,
+ *             the number of kept choices
+ *   rows    : [T * top] int32, the token t of each grouped row; -1 behind
+ *             the last kept one
+ *   pos     : [T * top] int32, the grouped row of each choice, -1 if dropped
+ * n in 1..1024, T * top <= 2^26.  T == 0 writes the offsets only. */
+gsi_status gsi_group_rows(const void *ids, int32_t ids_bytes, int32_t T, int32_t top, int32_t n,
+                          int32_t *offsets, int32_t *rows, int32_t *pos, void *stream);
+
+/* Each token's weighted sum over its choices, the inverse of the grouping:
+ *   out[t] = base[t] + sum_j weights[t][j] y[pos[t][j]]
+ * summed in fp32 in the order of j and rounded once.
+ *   y       : R rows of d elements, row stride ldy
+ *   pos     : [T][top] int32; an entry outside [0, R) adds nothing
+ *   weights : [T][top] fp32, or NULL for 1
+ *   base    : T rows, row stride ldb, or NULL for 0
+ *   out     : T rows, row stride ldo; may be base itself (same stride)
+ * d a multiple of 8, top in 1..64. */
+gsi_status gsi_group_combine(const void *y, int64_t ldy, int32_t R, const int32_t *pos,
+                             const float *weights, const void *base, int64_t ldb, void *out,
+                             int64_t ldo, int32_t T, int32_t top, int32_t d, int32_t dtype,
+                             void *stream);
+
 #ifdef __cplusplus
 }
 #endif

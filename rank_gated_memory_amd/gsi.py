@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_float, c_int32, c_size_t, c_uint8, c_void_p
+from ctypes import POINTER, c_float, c_int32, c_int64, c_size_t, c_uint8, c_void_p
 
 import torch
 
@@ -44,6 +44,12 @@ class GsiCalibStruct(ctypes.Structure):
     _fields_ = [("n", c_int32), ("d", c_int32), ("k", c_int32), ("dtype", c_int32),
                 ("A", c_void_p), ("V0", c_void_p), ("V", c_void_p), ("iters", c_int32),
                 ("reserved", c_int32)]
+
+
+class GsiWeightsStruct(ctypes.Structure):
+    _fields_ = [("d", c_int32), ("d_out", c_int32), ("n", c_int32), ("dtype", c_int32),
+                ("bits", c_int32), ("group", c_int32), ("stride", c_int64),
+                ("W", c_void_p), ("scales", c_void_p), ("zeros", c_void_p)]
 
 
 _lib = None
@@ -94,6 +100,18 @@ def lib() -> ctypes.CDLL:
         L.gsi_stack_phase.restype = c_int32
         L.gsi_stack_phase.argtypes = [c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_size_t,
                                       c_void_p]
+        L.gsi_q4_linear.restype = c_int32
+        L.gsi_q4_linear.argtypes = [POINTER(GsiWeightsStruct), c_void_p, c_int64, c_void_p, c_int64,
+                                    c_int32, c_void_p]
+        L.gsi_grouped_linear.restype = c_int32
+        L.gsi_grouped_linear.argtypes = [POINTER(GsiWeightsStruct), c_void_p, c_int64, c_int32, c_void_p,
+                                         c_void_p, c_void_p, c_int64, c_int32, c_void_p]
+        L.gsi_group_rows.restype = c_int32
+        L.gsi_group_rows.argtypes = [c_void_p, c_int32, c_int32, c_int32, c_int32, c_void_p, c_void_p,
+                                     c_void_p, c_void_p]
+        L.gsi_group_combine.restype = c_int32
+        L.gsi_group_combine.argtypes = [c_void_p, c_int64, c_int32, c_void_p, c_void_p, c_void_p, c_int64,
+                                        c_void_p, c_int64, c_int32, c_int32, c_int32, c_int32, c_void_p]
         _lib = L
     return _lib
 
@@ -341,3 +359,162 @@ def gsi_calibrate(A: torch.Tensor, V0: torch.Tensor, iters: int, V=None, ws=None
            "gsi_calibrate")
     o = int(lib().gsi_calibrate_status_offset())
     return V, ws[o:o + 4].view(torch.int32)
+
+
+# ---- plain linear maps: weights in 4 bits, weights of many experts ----
+
+def _call(where: str, fn, device: torch.device, stream, *args):
+    """fn(*args, stream) on `device`: its own current stream unless one is given,
+    whatever device is current."""
+    if device.type != "cuda":
+        raise ValueError(f"{where}: tensors must be on the GPU")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    raw = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+    if device.index is None or device.index == torch.cuda.current_device():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, raw)
+    if status != GSI_OK:
+        raise GsiError(status, where)
+
+
+def _rows2d(t: torch.Tensor, name: str, dtype, device, cols: int, n: int | None = None) -> int:
+    """The row stride of a [n][cols] tensor whose rows are contiguous."""
+    if t.dim() != 2 or t.shape[1] != cols or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must be [{'n' if n is None else n}][{cols}], is {tuple(t.shape)}")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} on {device}, is {t.dtype} on {t.device}")
+    if t.stride(1) != 1 and cols > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), cols)
+
+
+def _ints(t: torch.Tensor, name: str, shape, device):
+    if t.dtype != torch.int32 or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32 {tuple(shape)} on {device}, "
+                         f"is {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+class Q4:
+    """One map or the maps of n experts in 4 bits: w = scale (code - zero).
+
+    codes  : uint8 [d_out][d / 2] or [n][d_out][d / 2], the even column of a
+             pair in the low nibble
+    scales : [..][ceil(d / group)] in the dtype of x and y (bf16 or fp32)
+    zeros  : uint8 like scales, values 0..15, or None for 8 everywhere
+    The tensors are used where they lie and must stay alive as long as this."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None,
+                 group: int = 128):
+        if codes.dim() not in (2, 3) or codes.dtype != torch.uint8:
+            raise ValueError("codes must be uint8 [d_out][d / 2] or [n][d_out][d / 2]")
+        if group not in (32, 64, 128):
+            raise ValueError(f"group must be 32, 64 or 128, is {group}")
+        self.codes, self.scales, self.zeros, self.group = codes, scales, zeros, group
+        self.n = codes.shape[0] if codes.dim() == 3 else 1
+        self.d_out, self.d = codes.shape[-2], 2 * codes.shape[-1]
+        self.dtype, self.device = scales.dtype, codes.device
+        want = (*codes.shape[:-1], (self.d + group - 1) // group)
+        for t, name in ((scales, "scales"), (zeros, "zeros")):
+            if t is not None and (tuple(t.shape) != want or t.device != codes.device):
+                raise ValueError(f"{name} must be {want} on {codes.device}")
+        if zeros is not None and zeros.dtype != torch.uint8:
+            raise ValueError("zeros must be uint8")
+        if not all(t is None or t.is_contiguous() for t in (codes, scales, zeros)):
+            raise ValueError("codes, scales and zeros must be contiguous")
+        self.struct = GsiWeightsStruct(self.d, self.d_out, self.n, _dtype_code(scales), 4, group, 0,
+                                       _ptr(codes), _ptr(scales), _ptr(zeros))
+
+
+def gsi_q4_linear(w: Q4, x: torch.Tensor, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y [T][d_out] = x [T][d] through one map in 4 bits; x [d] is one token
+    and gives y [1][d_out]."""
+    if x.dim() == 1:
+        x = x[None]
+    ldx = _rows2d(x, "x", w.dtype, w.device, w.d)
+    T = x.shape[0]
+    if y is None:
+        y = torch.empty((T, w.d_out), dtype=w.dtype, device=w.device)
+    ldy = _rows2d(y, "y", w.dtype, w.device, w.d_out, T)
+    _call("gsi_q4_linear", lib().gsi_q4_linear, w.device, stream, w.struct, x.data_ptr(), ldx, y.data_ptr(), ldy, T)
+    return y
+
+
+def gsi_grouped_linear(w, x: torch.Tensor, offsets: torch.Tensor, rows: torch.Tensor | None = None,
+                       y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The rows of y ordered by expert: y[r] = W[e] x[rows[r]] for r in
+    [offsets[e], offsets[e + 1]); without rows, y[r] = W[e] x[r].  w is a
+    tensor [n][d_out][d] (each map contiguous, maps any stride apart) or a Q4
+    of n maps.  Rows of y behind the last expert's are not written."""
+    if isinstance(w, Q4):
+        struct, d, d_out, n, dtype, dev = w.struct, w.d, w.d_out, w.n, w.dtype, w.device
+    else:
+        if w.dim() != 3:
+            raise ValueError(f"W must be [n][d_out][d], is {tuple(w.shape)}")
+        n, d_out, d = w.shape
+        stride, s1, s2 = w.stride()
+        if s2 != 1 or s1 != d:
+            raise ValueError("every map of W must be contiguous")
+        dtype, dev = w.dtype, w.device
+        struct = GsiWeightsStruct(d, d_out, n, _dtype_code(w), 0, 0, stride, w.data_ptr(), None, None)
+    ldx = _rows2d(x, "x", dtype, dev, d)
+    R = x.shape[0] if rows is None else rows.shape[0]
+    _ints(offsets, "offsets", (n + 1,), dev)
+    if rows is not None:
+        _ints(rows, "rows", (R,), dev)
+    if y is None:
+        y = torch.empty((R, d_out), dtype=dtype, device=dev)
+    ldy = _rows2d(y, "y", dtype, dev, d_out, R)
+    _call("gsi_grouped_linear", lib().gsi_grouped_linear, dev, stream, struct, x.data_ptr(), ldx, x.shape[0],
+          offsets.data_ptr(), _ptr(rows), y.data_ptr(), ldy, R)
+    return y
+
+
+def gsi_group_rows(ids: torch.Tensor, n: int, offsets: torch.Tensor | None = None,
+                   rows: torch.Tensor | None = None, pos: torch.Tensor | None = None, stream=None):
+    """Order the expert numbers ids [T][top] (int32 or int64; numbers outside
+    [0, n) are dropped) by expert: (offsets [n + 1], rows [T * top], the token
+    of each grouped row, pos [T][top], the grouped row of each choice or -1)."""
+    if ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64) or not ids.is_contiguous():
+        raise ValueError("ids must be contiguous [T][top], int32 or int64")
+    T, top = ids.shape
+    dev = ids.device
+    if offsets is None and rows is None and pos is None:
+        at = T * top
+        both = torch.empty(2 * at + n + 1, dtype=torch.int32, device=dev)
+        rows, pos, offsets = both[:at], both[at:2 * at].view(T, top), both[2 * at:]
+    else:
+        offsets = torch.empty(n + 1, dtype=torch.int32, device=dev) if offsets is None else offsets
+        rows = torch.empty(T * top, dtype=torch.int32, device=dev) if rows is None else rows
+        pos = torch.empty((T, top), dtype=torch.int32, device=dev) if pos is None else pos
+        _ints(offsets, "offsets", (n + 1,), dev)
+        _ints(rows, "rows", (T * top,), dev)
+        _ints(pos, "pos", (T, top), dev)
+    _call("gsi_group_rows", lib().gsi_group_rows, dev, stream, ids.data_ptr(), ids.element_size(), T, top, n,
+          offsets.data_ptr(), rows.data_ptr(), pos.data_ptr())
+    return offsets, rows, pos
+
+
+def gsi_group_combine(y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor | None = None,
+                      base: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """out[t] = base[t] + sum_j weights[t][j] y[pos[t][j]]; a pos outside y's
+    rows adds nothing, weights None are 1, base None is 0; out may be base."""
+    if y.dim() != 2 or pos.dim() != 2:
+        raise ValueError("y must be [R][d] and pos [T][top]")
+    T, top = pos.shape
+    d, dtype, dev = y.shape[1], y.dtype, y.device
+    ldy = _rows2d(y, "y", dtype, dev, d)
+    _ints(pos, "pos", (T, top), dev)
+    if weights is not None and (weights.dtype != torch.float32 or weights.device != dev or not weights.is_contiguous()
+                                or weights.shape != pos.shape):
+        raise ValueError("weights must be contiguous fp32 like pos")
+    ldb = 0 if base is None else _rows2d(base, "base", dtype, dev, d, T)
+    if out is None:
+        out = torch.empty((T, d), dtype=dtype, device=dev)
+    ldo = _rows2d(out, "out", dtype, dev, d, T)
+    _call("gsi_group_combine", lib().gsi_group_combine, dev, stream, y.data_ptr(), ldy, y.shape[0], pos.data_ptr(),
+          _ptr(weights), _ptr(base), ldb, out.data_ptr(), ldo, T, top, d, _dtype_code(y))
+    return out
