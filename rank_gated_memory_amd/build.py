@@ -9,7 +9,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", "gsi_api.cpp"), os.path.join(PKG, "csrc", "gsi_kernels.hip"),
            os.path.join(PKG, "csrc", "gsi_batched.hip"), os.path.join(PKG, "csrc", "gsi_calib.hip"),
-           os.path.join(PKG, "csrc", "gsi_noalloc.hip"), os.path.join(PKG, "csrc", "gsi_maps.hip"),
+           os.path.join(PKG, "csrc", "gsi_noalloc.hip"), os.path.join(PKG, "csrc", "gsi_maps_api.cpp"),
+           os.path.join(PKG, "csrc", "gsi_maps_stream.hip"), os.path.join(PKG, "csrc", "gsi_maps_wide.hip"),
            os.path.join(PKG, "csrc", "gsi_rows.hip")]
 OUT = os.path.join(PKG, "libgsi.so")
 

@@ -1,0 +1,86 @@
+// Entry points of the plain linear maps: argument checks and the choice of kernel.
+#include "gsi_maps.h"
+
+namespace gsi {
+namespace {
+
+inline bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+gsi_status check_weights(const gsi_weights *w) {
+  if (!w) return GSI_E_NULL;
+  if (w->dtype != GSI_FP32 && w->dtype != GSI_BF16) return GSI_E_DTYPE;
+  if (w->bits != 0 && w->bits != 4) return GSI_E_DTYPE;
+  if (w->n < 1 || w->n > 4096 || w->d_out < 8 || w->d_out % 8 || w->d_out > (1 << 24)) return GSI_E_SHAPE;
+  if (w->d < 8 || w->d % (w->bits ? 32 : 8) || w->d > (1 << 20)) return GSI_E_SHAPE;
+  const int es = w->dtype == GSI_FP32 ? 4 : 2;
+  if (w->bits) {
+    if ((w->group != 32 && w->group != 64 && w->group != 128) || w->stride != 0) return GSI_E_SHAPE;
+  } else if (w->group != 0 || (w->n > 1 && w->stride < (int64_t)w->d_out * w->d) || w->stride > (INT64_MAX >> 16)) {
+    return GSI_E_SHAPE;
+  }
+  if (!w->W || (w->bits && !w->scales)) return GSI_E_NULL;
+  if (!aligned(w->W, 16) || (w->bits && !aligned(w->scales, es)) || (!w->bits && w->n > 1 && w->stride * es % 16))
+    return GSI_E_ALIGN;
+  return GSI_OK;
+}
+
+gsi_status run_maps(const gsi_weights *w, const void *x, int64_t ldx, int32_t T, const int32_t *offsets,
+                    const int32_t *rows, void *y, int64_t ldy, int32_t R, void *stream) {
+  const int es = w->dtype == GSI_FP32 ? 4 : 2;
+  if (ldx < w->d || ldy < w->d_out || ldx > INT64_MAX / 4 / T || ldy > INT64_MAX / 4 / R) return GSI_E_SHAPE;
+  if (!x || !y) return GSI_E_NULL;
+  if (!aligned(x, 16) || !aligned(y, 16) || ldx * es % 16 || ldy * es % 16 || !aligned(offsets, 4) || !aligned(rows, 4))
+    return GSI_E_ALIGN;
+  MArgs a{};
+  a.W = static_cast<const uint8_t *>(w->W);
+  a.scales = static_cast<const uint8_t *>(w->scales);
+  a.zeros = w->zeros;
+  a.x = static_cast<const uint8_t *>(x);
+  a.y = static_cast<uint8_t *>(y);
+  a.offsets = offsets;
+  a.rows = rows;
+  a.w_stride = w->bits ? (int64_t)w->d_out * (w->d / 2) : w->stride * es;
+  a.ldx = ldx;
+  a.ldy = ldy;
+  a.d = w->d;
+  a.d_out = w->d_out;
+  a.n = w->n;
+  a.R = R;
+  a.T = T;
+  a.groups = w->bits ? (w->d + w->group - 1) / w->group : 0;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const int per = R / (w->n < R ? w->n : R);  // rows per expert, on average
+  if (w->bits == 0 && w->dtype == GSI_BF16 && per >= 64) return launch_wide(a, st);
+  const bool f32 = w->dtype == GSI_FP32;
+  return launch_stream(a, w->bits ? (f32 ? kQ4F32 : kQ4Bf16) : (f32 ? kF32 : kBf16), w->group, st);
+}
+
+}  // namespace
+}  // namespace gsi
+
+using namespace gsi;
+
+extern "C" {
+
+gsi_status gsi_q4_linear(const gsi_weights *w, const void *x, int64_t ldx, void *y, int64_t ldy,
+                         int32_t T, void *stream) {
+  const gsi_status s = check_weights(w);
+  if (s != GSI_OK) return s;
+  if (w->bits != 4) return GSI_E_DTYPE;
+  if (w->n != 1 || T < 0) return GSI_E_SHAPE;
+  if (T == 0) return GSI_OK;
+  return run_maps(w, x, ldx, T, nullptr, nullptr, y, ldy, T, stream);
+}
+
+gsi_status gsi_grouped_linear(const gsi_weights *w, const void *x, int64_t ldx, int32_t T,
+                              const int32_t *offsets, const int32_t *rows, void *y, int64_t ldy,
+                              int32_t R, void *stream) {
+  const gsi_status s = check_weights(w);
+  if (s != GSI_OK) return s;
+  if (R < 0 || T < 0 || (R > 0 && T == 0)) return GSI_E_SHAPE;
+  if (R == 0) return GSI_OK;
+  if (!offsets) return GSI_E_NULL;
+  return run_maps(w, x, ldx, T, offsets, rows, y, ldy, R, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,561 @@
+// Plain linear maps with few rows per expert on gfx950 MFMA.
+//
+//   stream_kernel : the weights of an expert are read once for a chunk of 16
+//                   TB rows.  Bound by HBM: at one token a weight is used
+//                   once, so the chunk's x is staged in LDS and the wavefronts
+//                   do nothing but stream weights into registers, a batch of
+//                   loads ahead of the products.  A wavefront owns 16 RB
+//                   weight rows; where there are fewer such blocks than the
+//                   chip has wavefronts, KS of them split the columns of a
+//                   block and are joined through LDS in a fixed order.
+//
+// 4-bit weights.  With w = s (q - z) a group's share of y is
+//   s (sum q x - z sum x) = s (sum (16 + q) x - (16 + z) sum x).
+// 16 + q is the bf16 0x4180 | q << 3, so two codes decode with one shift and
+// one and-or, exactly, and the matrix core multiplies them with bf16 x
+// exactly; sum x of the group comes from the same instruction with ones for
+// weights.  fp32 x is split into three bf16 parts (8 + 8 + 8 bits, exact),
+// each its own product.  Only the group's fp32 sums are rounded.
+//
+// The matrix operand A holds tokens and B weight rows, so that a lane's
+// accumulators all belong to one weight row and take one scale.  Row m of A
+// is token 4 (m % 4) + m / 4 of the chunk: up to four tokens then need only
+// the first accumulator of every lane.
+#include <type_traits>
+
+#include "gsi_maps.h"
+
+namespace gsi {
+namespace {
+
+// The chunk of rows that slot `s` of a launch computes: experts in order,
+// each in chunks of `chunk` rows.  Every wavefront looks it up by itself.
+struct Chunk {
+  int e, row, count;  // count 0: the slot is behind the last chunk
+};
+
+__device__ __forceinline__ Chunk find_chunk(const MArgs &a, int s, int chunk) {
+  if (!a.offsets) {
+    const int row = s * chunk;
+    return {0, row, min(chunk, a.R - row)};
+  }
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int e0 = 0; e0 < a.n; e0 += 64) {
+    const int e = e0 + lane;
+    int lo, hi;
+    expert_rows(a, e, &lo, &hi);
+    const int mine = (hi - lo + chunk - 1) / chunk;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += u;
+    }
+    const uint64_t over = __ballot(before + incl > s);
+    if (over) {
+      const int l = __ffsll((unsigned long long)over) - 1;
+      const int k = s - before - (__shfl(incl, l, 64) - __shfl(mine, l, 64));
+      const int row = __shfl(lo, l, 64) + k * chunk;
+      return {e0 + l, row, min(chunk, __shfl(hi, l, 64) - row)};
+    }
+    before += __shfl(incl, 63, 64);
+  }
+  return {0, 0, 0};
+}
+
+// The constants of decode(), in registers: with literals (v & mask) | bits
+// takes two instructions instead of one.
+struct DecodeBits {
+  uint32_t mask = 0x00780078u, one = 0x41804180u, low = 0x0f0f0f0fu, sixteen = 0x10101010u;
+  __device__ __forceinline__ DecodeBits() {
+    asm("" : "+s"(mask), "+v"(one));
+    asm("" : "+s"(low), "+v"(sixteen));
+  }
+};
+
+// Eight codes as bf16 16 + q, in the order of the nibbles 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ bf16x8_t decode(uint32_t c, const DecodeBits &k) {
+  u32x4_t o;
+  o[0] = ((c << 3) & k.mask) | k.one;
+  o[1] = ((c >> 1) & k.mask) | k.one;
+  o[2] = ((c >> 5) & k.mask) | k.one;
+  o[3] = ((c >> 9) & k.mask) | k.one;
+  return as_bf16x8(o);
+}
+
+// Eight values (four dwords of bf16 pairs) in that order.
+__device__ __forceinline__ u32x4_t pair_order(u32x4_t v) {
+  u32x4_t o;
+  o[0] = __builtin_amdgcn_perm(v[2], v[0], 0x05040100u);
+  o[1] = __builtin_amdgcn_perm(v[2], v[0], 0x07060302u);
+  o[2] = __builtin_amdgcn_perm(v[3], v[1], 0x05040100u);
+  o[3] = __builtin_amdgcn_perm(v[3], v[1], 0x07060302u);
+  return o;
+}
+
+// fp32 as three bf16 parts, by truncation: 24 significant bits are 8 + 8 + 8,
+// so their sum is the value.  Parts of Inf and NaN are not finite.
+__device__ __forceinline__ void split3(float v, uint32_t (&p)[3]) {
+  const uint32_t h = __float_as_uint(v) & 0xffff0000u;
+  const float r = v - __uint_as_float(h);
+  const uint32_t m = __float_as_uint(r) & 0xffff0000u;
+  const float s = r - __uint_as_float(m);
+  p[0] = h;
+  p[1] = m;
+  p[2] = __float_as_uint(s);
+}
+
+__device__ __forceinline__ uint32_t high_pair(uint32_t a, uint32_t b) {  // bf16 of a (low) and b (high)
+  return __builtin_amdgcn_perm(b, a, 0x07060302u);
+}
+
+// Eight fp32 values as bf16 part p of each, in the order of pair_order.
+__device__ __forceinline__ void split_octet(const f32x4_t (&u)[2], bf16x8_t (&out)[3]) {
+  u32x4_t o[3];
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {  // pair p: values p and p + 4
+    uint32_t lo[3], hi[3];
+    split3(u[0][p], lo);
+    split3(u[1][p], hi);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) o[k][p] = high_pair(lo[k], hi[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) out[k] = as_bf16x8(o[k]);
+}
+
+// A step is 64 bytes of each weight row: one 16-byte load of each of 64 lanes.
+template <Kind K>
+constexpr int kStepColumns = K == kQ4Bf16 || K == kQ4F32 ? 128 : K == kBf16 ? 32 : 16;
+
+constexpr int kStreamWaves = 8;
+constexpr int kStreamLds = 64 * 1024;  // x of a chunk; two workgroups of a CU hold theirs
+
+// How a launch splits its work.
+struct StreamShape {
+  int split;         // wavefronts that share the columns of a block of weight rows
+  int strips;        // workgroups per chunk
+  int columns;       // columns of x in LDS at a time, whole steps
+  int column_parts;  // of d
+};
+
+template <Kind K, int G, int TB, int RB, int U>
+struct Stream {
+  static constexpr bool q4 = K == kQ4Bf16 || K == kQ4F32;
+  static constexpr bool f32 = K == kQ4F32 || K == kF32;
+  static constexpr int es = f32 ? 4 : 2;
+  static constexpr int C = kStepColumns<K>;
+  static constexpr int XP = K == kQ4F32 ? 3 : 1;       // parts of x
+  static constexpr int xes = K == kF32 ? 4 : 2;        // bytes of a part
+  static constexpr int NG = q4 ? 128 / G : 1;          // scale groups of a step
+  static constexpr int BG = U * NG;                    // of a batch
+  static constexpr int SW = f32 ? BG : (BG + 1) / 2;   // their scales and zeros in dwords
+  static constexpr int ZW = (BG + 3) / 4;
+
+  // U steps of weights with their scales
+  struct Batch {
+    u32x4_t w[U][RB];
+    uint32_t s[q4 ? RB : 1][SW], z[q4 ? RB : 1][ZW];
+  };
+
+  const MArgs &a;
+  DecodeBits bits;
+  int quad, l16, row_bytes;
+  // the first block's first row, and this lane's offsets from there: 32 bits,
+  // for at most 32 rows
+  const uint8_t *wp, *sp, *zp;
+  uint32_t wo[RB], so[RB], zo[RB];
+
+  __device__ __forceinline__ Stream(const MArgs &args, int lane) : a(args) {
+    quad = lane >> 4, l16 = lane & 15;
+    row_bytes = q4 ? a.d / 2 : a.d * es;
+  }
+
+  // The blocks of weight rows from i0 < d_out on; rows behind the last read
+  // the last, and what they give is not stored.
+  __device__ __forceinline__ void rows_from(int e, int i0) {
+    const int64_t row = (int64_t)e * a.d_out + i0;
+    wp = a.W + e * a.w_stride + (int64_t)i0 * row_bytes;
+    if constexpr (q4) {
+      sp = a.scales + row * a.groups * es;
+      // without zeros their loads read 16 bytes of the scales, which there are
+      // at least, and the value is dropped
+      zp = a.zeros ? a.zeros + row * a.groups : a.scales;
+    }
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      const uint32_t i = min(16 * b + l16, a.d_out - 1 - i0);
+      wo[b] = i * row_bytes + 16 * quad;
+      if constexpr (q4) {
+        so[b] = i * a.groups * es;
+        zo[b] = a.zeros ? i * a.groups : 0;
+      }
+    }
+  }
+
+  template <typename T, int M, int N>
+  __device__ __forceinline__ static void copy_run(uint32_t (&o)[N], const uint8_t *p) {
+    struct Run {
+      T v[M];
+    };
+    __builtin_memcpy(o, p, sizeof(Run));
+  }
+
+  // The U whole steps from `step` on.
+  __device__ __forceinline__ void load(Batch &o, int step) const {
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) o.w[u][b] = *reinterpret_cast<const u32x4_t *>(wp + (wo[b] + (uint32_t)step * 64) + u * 64);
+      if constexpr (q4) {
+        using T = std::conditional_t<f32, uint32_t, uint16_t>;
+        copy_run<T, BG>(o.s[b], sp + (so[b] + (uint32_t)(step * NG * es)));
+        copy_run<uint8_t, BG>(o.z[b], zp + (zo[b] + (uint32_t)(a.zeros ? step * NG : 0)));
+      }
+    }
+  }
+
+  // Step `step` alone as step 0 of a batch; it may end behind the row.
+  __device__ __forceinline__ void load_last(Batch &o, int step) const {
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      o.w[0][b] = u32x4_t{0, 0, 0, 0};
+      if (step * 64 + 16 * quad < row_bytes) o.w[0][b] = *reinterpret_cast<const u32x4_t *>(wp + (wo[b] + (uint32_t)step * 64));
+      if constexpr (q4) {
+#pragma unroll
+        for (int g = 0; g < SW; ++g) o.s[b][g] = 0;
+        o.z[b][0] = 0;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const int at = min(step * NG + g, a.groups - 1);  // behind the last group x is zero
+          if constexpr (f32)
+            o.s[b][g] = *reinterpret_cast<const uint32_t *>(sp + (so[b] + 4u * at));
+          else
+            o.s[b][g / 2] |= (uint32_t) * reinterpret_cast<const uint16_t *>(sp + (so[b] + 2u * at)) << (16 * (g & 1));
+          o.z[b][0] |= (uint32_t)zp[zo[b] + (a.zeros ? at : 0)] << (8 * g);
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ static int x_stride(int columns) { return columns * xes + 16; }
+
+  // x of the chunk's columns [c0, c0 + columns) into LDS: a plane of 16 TB
+  // tokens for each part, zeros behind d and for rows without a source, octets
+  // in the order of decode() where the weights are codes.  Only the chunk's
+  // own rows are written; those behind them are never read.
+  __device__ __forceinline__ void stage(uint8_t *lds, const Chunk &ch, int c0, int columns) const {
+    constexpr int V = K == kF32 ? 4 : 8;  // columns of a 16-byte piece
+    const int pieces = columns / V, stride = x_stride(columns);
+    for (int k = threadIdx.x; k < ch.count * pieces; k += kStreamWaves * 64) {
+      const int m = k / pieces, p = k - m * pieces, c = c0 + p * V;
+      const int src = a.rows ? a.rows[ch.row + m] : ch.row + m;
+      const bool in = c < a.d && src >= 0 && src < a.T;
+      const uint8_t *at = a.x + ((int64_t)(in ? src : 0) * a.ldx + c) * es;
+      uint8_t *const to = lds + m * stride + p * 16;
+      if constexpr (K == kQ4F32) {
+        f32x4_t u[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        if (in) {
+          u[0] = *reinterpret_cast<const f32x4_t *>(at);
+          u[1] = *reinterpret_cast<const f32x4_t *>(at + 16);
+        }
+        bf16x8_t o[3];
+        split_octet(u, o);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) *reinterpret_cast<bf16x8_t *>(to + q * (ch.count * stride)) = o[q];
+      } else {
+        u32x4_t u = {0, 0, 0, 0};
+        if (in) u = *reinterpret_cast<const u32x4_t *>(at);
+        *reinterpret_cast<u32x4_t *>(to) = q4 ? pair_order(u) : u;
+      }
+    }
+  }
+
+  // Where this lane's tokens lie in LDS; a lane without a token reads the first.
+  struct Tokens {
+    const uint8_t *x[TB];
+    int plane;
+  };
+  __device__ __forceinline__ Tokens tokens(const uint8_t *lds, const Chunk &ch, int columns) const {
+    Tokens t;
+    const int stride = x_stride(columns);
+    t.plane = ch.count * stride;
+#pragma unroll
+    for (int j = 0; j < TB; ++j) {
+      const int m = 16 * j + 4 * (l16 & 3) + (l16 >> 2);
+      t.x[j] = lds + (m < ch.count ? m : 0) * stride + quad * (q4 && G == 128 ? 64 : 16);
+    }
+    return t;
+  }
+
+  // The products of a batch's first N steps into acc, x from `at` bytes on;
+  // accumulators from NI on stay zero.
+  template <int NI, int N>
+  __device__ __forceinline__ void multiply(f32x4_t (&acc)[RB][TB], const Batch &o, const Tokens &tk, int at) const {
+    uint32_t z16[q4 ? RB : 1][ZW];  // 16 + zero, a byte each
+    if constexpr (q4) {
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int k = 0; k < ZW; ++k) z16[b][k] = a.zeros ? (o.z[b][k] & bits.low) | bits.sixteen : 0x18181818u;
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      // step by step: hoisting the reads of x over all steps costs wavefronts
+      __builtin_amdgcn_sched_barrier(0);
+      const int xo = at + u * C * xes;
+      if constexpr (!q4) {
+        u32x4_t x[TB];
+#pragma unroll
+        for (int t = 0; t < TB; ++t) x[t] = *reinterpret_cast<const u32x4_t *>(tk.x[t] + xo);
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+          for (int t = 0; t < TB; ++t) {
+            if constexpr (K == kBf16) {
+              acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(x[t]), as_bf16x8(o.w[u][b]), acc[b][t], 0, 0, 0);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x[t][i]), __uint_as_float(o.w[u][b][i]),
+                                                                 acc[b][t], 0, 0, 0);
+            }
+          }
+      } else {
+        // Product i of a step covers, for G = 128, columns 32 quad + 8 i + e;
+        // for smaller groups columns 32 i + 8 quad + e, so that no product
+        // mixes groups.
+        constexpr int PG = 4 / NG;  // products of a group
+        const f32x4_t zero4 = {0, 0, 0, 0};
+        const u32x4_t one_bits = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+        u32x4_t c[RB];
+
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+          c[b] = o.w[u][b];
+          if constexpr (G < 128) {  // dword j of quad i <- dword i of quad j
+            const auto p = __builtin_amdgcn_permlane32_swap(c[b][0], c[b][2], false, false);
+            const auto q = __builtin_amdgcn_permlane32_swap(c[b][1], c[b][3], false, false);
+            const auto r = __builtin_amdgcn_permlane16_swap(p[0], q[0], false, false);
+            const auto s = __builtin_amdgcn_permlane16_swap(p[1], q[1], false, false);
+            c[b] = u32x4_t{r[0], r[1], s[0], s[1]};
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          if (TB > 1 && g > 0) __builtin_amdgcn_sched_barrier(0);
+          bf16x8_t w[RB][PG];
+          float s[RB], z[RB];
+#pragma unroll
+          for (int b = 0; b < RB; ++b) {
+            const int k = u * NG + g;
+#pragma unroll
+            for (int i = 0; i < PG; ++i) w[b][i] = decode(c[b][g * PG + i], bits);
+            s[b] = f32 ? __uint_as_float(o.s[b][k])
+                       : __uint_as_float(k & 1 ? o.s[b][k / 2] & 0xffff0000u : o.s[b][k / 2] << 16);
+            z[b] = (float)(z16[b][k / 4] >> (8 * (k & 3)) & 255);
+          }
+#pragma unroll
+          for (int t = 0; t < TB; ++t) {
+            f32x4_t q[RB], sx = zero4;
+#pragma unroll
+            for (int b = 0; b < RB; ++b) q[b] = zero4;
+#pragma unroll
+            for (int i = 0; i < PG; ++i)
+#pragma unroll
+              for (int p = 0; p < XP; ++p) {
+                const bf16x8_t x = as_bf16x8(*reinterpret_cast<const u32x4_t *>(
+                    tk.x[t] + p * tk.plane + xo + (g * PG + i) * (G == 128 ? 16 : 64)));
+                sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, as_bf16x8(one_bits), sx, 0, 0, 0);
+#pragma unroll
+                for (int b = 0; b < RB; ++b) q[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w[b][i], q[b], 0, 0, 0);
+              }
+#pragma unroll
+            for (int b = 0; b < RB; ++b) {
+#pragma unroll
+              for (int i = 0; i < NI; ++i) acc[b][t][i] += s[b] * (q[b][i] - z[b] * sx[i]);
+              // here, not after the next batch's loads, where the compiler
+              // would carry q and sx of every group to
+              asm volatile("" : "+v"(acc[b][t]));
+            }
+          }
+        }
+      }
+    }
+  }
+};
+
+template <Kind K, int G, int TB, int RB, int U>
+__global__ void __launch_bounds__(kStreamWaves * 64, TB == 1 ? 4 : 2) stream_kernel(MArgs a, StreamShape sh) {
+  using S = Stream<K, G, TB, RB, U>;
+  constexpr int kRed = RB * TB * 256;  // sums of a wavefront
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ float red[kStreamWaves][kRed];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Chunk ch = find_chunk(a, blockIdx.x / sh.strips, 16 * TB);
+  if (ch.count <= 0) return;
+  S s(a, lane);
+  // a workgroup's wavefronts: kStreamWaves / split blocks of weight rows, the
+  // columns of each in `split` shares of whole batches
+  const int side = wave / sh.split, share = wave % sh.split, sides = kStreamWaves / sh.split;
+  const int blocks = (a.d_out + 16 * RB - 1) / (16 * RB), groups = (blocks + sides - 1) / sides;
+  // accumulators of a lane that hold tokens
+  const int live = TB == 1 && S::q4 ? (ch.count + 3) / 4 : 4;
+  const auto tk = s.tokens(lds, ch, sh.columns);
+  // a part's columns: whole batches, dealt to the split in even shares; what
+  // is left of the row goes to the last share, step by step
+  const auto share_of = [&](int part, int *step0, int *first, int *end, int *rest, int *last) {
+    const int c0 = part * sh.columns, width = min(sh.columns, a.d - c0), batches = width / (S::C * U);
+    *step0 = c0 / S::C;
+    *first = *step0 + batches * share / sh.split * U;
+    *end = *step0 + batches * (share + 1) / sh.split * U;
+    *rest = *step0 + batches * U;
+    *last = share == sh.split - 1 ? *step0 + (width + S::C - 1) / S::C : 0;
+  };
+  // Of every part and of every block the first batch is on its way before the
+  // wavefront is done with the last one.
+  typename S::Batch o[2];
+  const auto first_batch = [&](int g, int part) {
+    int step0, first, end, rest, last;
+    share_of(part, &step0, &first, &end, &rest, &last);
+    s.rows_from(ch.e, min((g * sides + side) * 16 * RB, a.d_out - 1));
+    if (first < end) s.load(o[0], first);
+  };
+  int g = blockIdx.x % sh.strips;
+  if (g < groups) first_batch(g, 0);
+  for (; g < groups; g += sh.strips) {
+    f32x4_t acc[RB][TB] = {};
+    for (int part = 0; part < sh.column_parts; ++part) {
+      int step0, first, end, rest, last;
+      share_of(part, &step0, &first, &end, &rest, &last);
+      if (sh.column_parts > 1 || g < sh.strips) {
+        if (part > 0 || g >= sh.strips) __syncthreads();
+        s.stage(lds, ch, part * sh.columns, sh.columns);
+        __syncthreads();
+      }
+      const auto run = [&](auto ni) {
+        constexpr int NI = decltype(ni)::value;
+        for (int step = first; step < end; step += 2 * U) {
+          if (step + U < end) s.load(o[1], step + U);
+          s.template multiply<NI, U>(acc, o[0], tk, (step - step0) * S::C * S::xes);
+          if (step + 2 * U < end) s.load(o[0], step + 2 * U);
+          if (step + U < end) s.template multiply<NI, U>(acc, o[1], tk, (step + U - step0) * S::C * S::xes);
+        }
+        for (int step = rest; step < last; ++step) {
+          s.load_last(o[0], step);
+          s.template multiply<NI, 1>(acc, o[0], tk, (step - step0) * S::C * S::xes);
+        }
+      };
+      if (live == 1)
+        run(std::integral_constant<int, 1>{});
+      else if (live == 2)
+        run(std::integral_constant<int, 2>{});
+      else
+        run(std::integral_constant<int, 4>{});
+      if (part + 1 < sh.column_parts)
+        first_batch(g, part + 1);
+      else if (g + sh.strips < groups)
+        first_batch(g + sh.strips, 0);
+    }
+    if (sh.split > 1) {
+      if (g >= sh.strips) __syncthreads();  // the sums of the last group have been read
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            red[wave][(b * TB + t) * 256 + (4 * i + s.quad) * 16 + s.l16] = acc[b][t][i];
+      __syncthreads();
+    }
+    // sums of one output: its wavefront's own, or those of the split in order
+    const auto put = [&](int side0, int k, float v) {
+      const int b = k / (TB * 256), token = k / 16 % (16 * TB);
+      const int i = (g * sides + side0) * 16 * RB + 16 * b + k % 16, r = ch.row + token;
+      if (token >= ch.count || i >= a.d_out) return;
+      if (a.rows) {
+        const int src = a.rows[r];
+        if (src < 0 || src >= a.T) v = 0.f;
+      }
+      if constexpr (S::f32)
+        reinterpret_cast<float *>(a.y)[r * a.ldy + i] = v;
+      else
+        reinterpret_cast<__bf16 *>(a.y)[r * a.ldy + i] = (__bf16)v;
+    };
+    if (sh.split > 1) {
+      for (int k = threadIdx.x; k < sides * kRed; k += kStreamWaves * 64) {
+        const int side0 = k / kRed, in = k - side0 * kRed;
+        float v = 0.f;
+        for (int w = 0; w < sh.split; ++w) v += red[side0 * sh.split + w][in];
+        put(side0, in, v);
+      }
+    } else {
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) put(side, (b * TB + t) * 256 + (4 * i + s.quad) * 16 + s.l16, acc[b][t][i]);
+    }
+  }
+}
+
+template <Kind K, int G, int TB, int RB, int U>
+gsi_status launch_as(const MArgs &a, hipStream_t st) {
+  using S = Stream<K, G, TB, RB, U>;
+  const int experts = a.n < a.R ? a.n : a.R;
+  const int64_t chunks = (a.R + 16 * TB - 1) / (16 * TB) + (a.offsets ? experts : 0);
+  static_assert(16 * TB * S::XP * (S::C * U * S::xes + 16) <= kStreamLds, "one batch of columns fits");
+  StreamShape sh{};
+  // x of a chunk in LDS: all of it, or as many whole batches of columns as fit
+  const int tokens = a.R < 16 * TB ? a.R : 16 * TB;
+  const int unit = S::C * U, padded = (a.d + S::C - 1) / S::C * S::C;
+  const int room = (kStreamLds / (tokens * S::XP) - 16) / S::xes / unit * unit;
+  sh.columns = padded < room ? padded : room;
+  sh.column_parts = (a.d + sh.columns - 1) / sh.columns;
+  // The split with the fewest batches in a row for a wavefront, where 512
+  // workgroups run at once and joining a block costs about one batch.
+  const int blocks = (a.d_out + 16 * RB - 1) / (16 * RB), want = (512 + experts - 1) / experts;
+  const int batches = (sh.columns + unit - 1) / unit;
+  int64_t best = INT64_MAX;
+  for (int split = 1; split <= kStreamWaves && (split == 1 || split <= batches); split *= 2) {
+    const int sides = kStreamWaves / split, groups = (blocks + sides - 1) / sides;
+    const int strips = sh.column_parts > 1 || groups < want ? groups : want;
+    const int64_t rounds = sh.column_parts > 1 ? (groups + want - 1) / want : (groups + strips - 1) / strips;
+    const int64_t cost = rounds * ((batches + split - 1) / split + (split > 1 ? 1 : 0));
+    if (cost < best) best = cost, sh.split = split, sh.strips = strips;
+  }
+  if (chunks * sh.strips > INT32_MAX) return GSI_E_SHAPE;
+  const size_t lds = (size_t)tokens * S::XP * (sh.columns * S::xes + 16);
+  stream_kernel<K, G, TB, RB, U><<<(unsigned)(chunks * sh.strips), kStreamWaves * 64, lds, st>>>(a, sh);
+  return hipGetLastError() == hipSuccess ? GSI_OK : GSI_E_HIP;
+}
+
+template <Kind K, int G>
+gsi_status launch_kind(const MArgs &a, hipStream_t st) {
+  const int per = a.R / (a.n < a.R ? a.n : a.R);  // rows per expert, on average
+  constexpr int U = K == kQ4F32 ? 1 : 2;  // steps of a batch: three parts of x leave room for fewer in LDS
+  if (per > 32) return launch_as<K, G, 4, 2, U>(a, st);
+  if (per > 16) return launch_as<K, G, 2, 2, U>(a, st);
+  return launch_as<K, G, 1, 1, 2 * U>(a, st);
+}
+
+template <Kind K>
+gsi_status launch_group(const MArgs &a, int group, hipStream_t st) {
+  return group == 128 ? launch_kind<K, 128>(a, st)
+                      : (group == 64 ? launch_kind<K, 64>(a, st) : launch_kind<K, 32>(a, st));
+}
+
+}  // namespace
+
+gsi_status launch_stream(const MArgs &a, Kind kind, int group, hipStream_t st) {
+  switch (kind) {
+    case kQ4Bf16: return launch_group<kQ4Bf16>(a, group, st);
+    case kQ4F32: return launch_group<kQ4F32>(a, group, st);
+    case kBf16: return launch_kind<kBf16, 128>(a, st);
+    default: return launch_kind<kF32, 128>(a, st);
+  }
+}
+
+}  // namespace gsi

@@ -1,0 +1,323 @@
+// Plain linear maps with many rows per expert on gfx950 MFMA: 256 x 256 tiles.
+#include "gsi_maps.h"
+
+namespace gsi {
+namespace {
+
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+// The tiles of a launch.  Each expert's rows are cut into full row tiles of
+// BM and one shorter rest; every full tile comes before any rest, so that the
+// last round of the workgroups is made of short ones.  The full tiles are
+// dealt to the 8 XCDs (workgroup b runs on XCD b % 8) in contiguous shares, so
+// that workgroups that share an L2 work on neighbouring tiles: groups of
+// kSlotGroup row tiles, in each all column tiles, in each the row tiles.  The
+// rests, of all heights, are dealt one by one.
+constexpr int kXcds = 8;
+constexpr int kSlotGroup = 4;
+
+struct Tile {
+  int e, row, count, col;  // count 0: behind the last
+};
+
+struct Tiles {
+  int full, rest;  // row tiles
+};
+
+template <int BM>
+__device__ __forceinline__ Tiles count_tiles(const MArgs &a) {
+  int full = 0, rest = 0;
+  for (int e0 = 0; e0 < a.n; e0 += 64) {
+    int lo, hi;
+    expert_rows(a, e0 + (threadIdx.x & 63), &lo, &hi);
+    full += (hi - lo) / BM;
+    rest += (hi - lo) % BM != 0;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    full += __shfl_xor(full, o, 64);
+    rest += __shfl_xor(rest, o, 64);
+  }
+  return {__builtin_amdgcn_readfirstlane(full), __builtin_amdgcn_readfirstlane(rest)};
+}
+
+// Tile number `at` of XCD `xcd`.
+template <int BM>
+__device__ __forceinline__ Tile find_tile(const MArgs &a, const Tiles &n, int col_tiles, int xcd, int64_t at) {
+  const int lane = threadIdx.x & 63;
+  const int64_t full_tiles = (int64_t)n.full * col_tiles, rest_tiles = (int64_t)n.rest * col_tiles;
+  const int64_t share = (full_tiles + kXcds - 1) / kXcds;
+  const int64_t first = xcd * share, mine = max((int64_t)0, min(share, full_tiles - first));
+  const bool is_full = at < mine;
+  int slot, col;
+  if (is_full) {
+    const int64_t t = first + at;
+    const int g = (int)(t / (kSlotGroup * col_tiles)), in = (int)(t - (int64_t)g * kSlotGroup * col_tiles);
+    const int wide = min(kSlotGroup, n.full - g * kSlotGroup);
+    slot = g * kSlotGroup + in % wide;
+    col = in / wide;
+  } else {
+    const int64_t t = (at - mine) * kXcds + xcd;
+    if (t >= rest_tiles) return {0, 0, 0, 0};
+    slot = (int)(t / col_tiles);
+    col = (int)(t - (int64_t)slot * col_tiles);
+  }
+  int before = 0;
+  for (int e0 = 0; e0 < a.n; e0 += 64) {
+    int lo, hi;
+    expert_rows(a, e0 + lane, &lo, &hi);
+    const int has = is_full ? (hi - lo) / BM : ((hi - lo) % BM != 0);
+    int incl = has;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += u;
+    }
+    const uint64_t over = __ballot(before + incl > slot);
+    if (over) {
+      const int l = __ffsll((unsigned long long)over) - 1;
+      const int k = slot - before - (__builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(has, l));
+      const int row = __builtin_amdgcn_readlane(lo, l), rows = __builtin_amdgcn_readlane(hi, l) - row;
+      const int skip = is_full ? k * BM : rows / BM * BM;
+      return {e0 + l, row + skip, min(BM, rows - skip), col};
+    }
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return {0, 0, 0, 0};
+}
+
+// A tile row is BK columns in 16-byte pieces; piece c of row r lies at
+// position c ^ swizzle(r), so that the 16 rows that a read touches at once lie
+// in different banks.
+template <int BK>
+__device__ __forceinline__ int swizzle(int r) {
+  return BK == 64 ? r & 7 : (r >> 2) & 3;
+}
+template <int BK>
+__device__ __forceinline__ int tile_at(int r, int c) {
+  return r * (BK * 2) + ((c ^ swizzle<BK>(r)) << 4);
+}
+
+__device__ const u32x4_t kZeros = {0, 0, 0, 0};
+
+// 64 lanes' 16 bytes each, from anywhere, to 1 KiB of LDS in lane order.
+__device__ __forceinline__ void to_lds(const void *src, void *dst) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
+                                   (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
+}
+
+// Every wavefront's own loads to LDS but the last N have landed, then all wavefronts'.
+template <int N>
+__device__ __forceinline__ void landed() {
+  static_assert(N < 64, "vmcnt");
+  // the builtin, so that the compiler's own count knows of the wait
+  __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4 << 14) | (7 << 4));  // vmcnt(N) lgkmcnt(0)
+  asm volatile("s_barrier" ::: "memory");
+}
+
+// bf16 tiles of 256 tokens x 256 weight rows on 8 wavefronts, 2 x 4 of them,
+// each 32 TM tokens x 64 weight rows.  The columns go by in stages of 32; four
+// stages lie in LDS, filled by direct loads in a stream that runs on from one
+// tile into the next.
+constexpr int kWideBM = 256, kWideBN = 256, kWideBK = 32;
+constexpr int kWideStage = (kWideBM + kWideBN) * kWideBK * 2;
+constexpr int kWideLoads = kWideStage / 1024 / 8;  // loads of a wavefront per stage, half x, half W
+
+// Where a wavefront's loads of a stage come from.
+struct WideSource {
+  const uint8_t *x[kWideLoads / 2], *w[kWideLoads / 2];
+  int left;  // columns from this lane's next piece to the row's end
+};
+
+__device__ __forceinline__ WideSource wide_source(const MArgs &a, const Tile &tl, int wave, int lane) {
+  constexpr int L = kWideLoads / 2, RK = 16;  // rows of a KiB
+  // first column of this lane's piece: the same in all its rows, which lie
+  // whole KiB apart
+  const int sub = lane >> 2, piece = ((lane & 3) ^ swizzle<kWideBK>(sub)) * 8;
+  WideSource f;
+  f.left = tl.count > 0 ? a.d - piece : 0;
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int m = (wave * L + i) * RK + sub;
+    f.x[i] = f.w[i] = nullptr;
+    if (tl.count > 0) {
+      const int r = tl.row + min(m, tl.count - 1);
+      const int src = a.rows ? a.rows[r] : r;
+      f.x[i] = a.x + ((int64_t)(src < 0 || src >= a.T ? 0 : src) * a.ldx + piece) * 2;
+      f.w[i] = a.W + tl.e * a.w_stride + ((int64_t)min(tl.col * kWideBN + m, a.d_out - 1) * a.d + piece) * 2;
+    }
+  }
+  return f;
+}
+
+// Brings the next 32 columns.  A piece behind d is read from zeros, for x and
+// for W (their product must be zero), and so is a whole stage behind the last.
+__device__ __forceinline__ void wide_fetch(WideSource &f, uint8_t *st, int wave) {
+  constexpr int L = kWideLoads / 2;
+  const uint64_t zeros = reinterpret_cast<uint64_t>(&kZeros);
+  const uint64_t in = (int64_t)(-f.left) >> 63;  // all ones while left > 0
+  f.left -= kWideBK;
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    to_lds(reinterpret_cast<const void *>((reinterpret_cast<uint64_t>(f.x[i]) & in) | (zeros & ~in)),
+           st + (wave * L + i) * 1024);
+    f.x[i] += 2 * kWideBK;
+  }
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    to_lds(reinterpret_cast<const void *>((reinterpret_cast<uint64_t>(f.w[i]) & in) | (zeros & ~in)),
+           st + kWideBM * kWideBK * 2 + (wave * L + i) * 1024);
+    f.w[i] += 2 * kWideBK;
+  }
+}
+
+// One tile of at most 64 TM tokens.  Its first two stages have landed and the
+// third is on its way when it begins; it leaves those of the next tile (`nf`) so.
+template <int TM>
+__device__ __forceinline__ void wide_tile(const MArgs &a, const Tile &tl, WideSource &f, const WideSource &nf,
+                                          uint8_t *lds0, uint8_t *lds1, uint8_t *lds2, uint8_t *lds3) {
+  constexpr int TN = 2, kBlock = 32 * kWideBK * 2;  // 32 x 32 blocks of weight rows; bytes of 32 rows
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 2, wn = wave & 3, l32 = lane & 31, half = lane >> 5;
+  // which of this lane's tokens have a source; 0 for those behind the tile
+  uint32_t valid = 0;
+#pragma unroll
+  for (int j = 0; j < TM; ++j) {
+    const int m = (wm * TM + j) * 32 + l32;
+    if (m < tl.count) {
+      const int src = a.rows ? a.rows[tl.row + m] : tl.row + m;
+      valid |= (src >= 0 && src < a.T ? 1u : 0u) << j;
+    }
+  }
+
+  f32x16_t acc[TN][TM] = {};
+  int xat[2], wat[2];  // the swizzle of a row depends on its place in a block only
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    xat[s] = wm * TM * kBlock + tile_at<kWideBK>(l32, 2 * s + half);
+    wat[s] = kWideBM * kWideBK * 2 + wn * TN * kBlock + tile_at<kWideBK>(l32, 2 * s + half);
+  }
+  bf16x8_t wf[2][TN], xf[2][TM];
+  const auto read = [&](const uint8_t *st, int s) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+      wf[s][j] = as_bf16x8(*reinterpret_cast<const u32x4_t *>(st + wat[s] + j * kBlock));
+#pragma unroll
+    for (int j = 0; j < TM; ++j)
+      xf[s][j] = as_bf16x8(*reinterpret_cast<const u32x4_t *>(st + xat[s] + j * kBlock));
+  };
+  const auto multiply = [&](int s) {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int j = 0; j < TM; ++j)
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf[s][i], xf[s][j], acc[i][j], 0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // One step multiplies the stage `cur`, whose first 16 columns are in
+  // registers, and leaves those of `next` there.  Loads to LDS are issued
+  // between two products, where every read of LDS has come back: the compiler
+  // waits for all of them after such a load.  When a step ends only its own
+  // loads may be under way, so a stage has two steps to arrive; it is filled
+  // after the barrier behind its last reads.
+  const auto step = [&](const uint8_t *cur, const uint8_t *next, uint8_t *fill) {
+    read(cur, 1);
+    multiply(0);
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    wide_fetch(f, fill, wave);
+    read(next, 0);
+    multiply(1);
+    landed<kWideLoads>();
+  };
+  read(lds0, 0);
+  for (int k = 128; k < a.d; k += 128) {
+    step(lds0, lds1, lds3);
+    step(lds1, lds2, lds0);
+    step(lds2, lds3, lds1);
+    step(lds3, lds0, lds2);
+  }
+  // the last 128 columns (zeros behind d)
+  step(lds0, lds1, lds3);
+  f = nf;
+  step(lds1, lds2, lds0);
+  step(lds2, lds3, lds1);
+  step(lds3, lds0, lds2);
+
+  // Of each 16 weight rows of a token the lower lanes take eight and the
+  // upper ones the others, 16 bytes each.
+#pragma unroll
+  for (int j = 0; j < TM; ++j) {
+    const int m = (wm * TM + j) * 32 + l32;
+    uint8_t *const yp = a.y + 2 * ((int64_t)(tl.row + m) * a.ldy);
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; q += 2) {
+        uint32_t v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+          const bf16x2_t p = {(__bf16)acc[i][j][4 * q + 2 * r], (__bf16)acc[i][j][4 * q + 2 * r + 1]};
+          v[r] = valid >> j & 1 ? __builtin_bit_cast(uint32_t, p) : 0u;
+        }
+        const auto s0 = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
+        const auto s1 = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
+        const int o = tl.col * kWideBN + (wn * TN + i) * 32 + 8 * q + 8 * half;
+        if (m < tl.count && o < a.d_out)
+          *reinterpret_cast<u32x4_t *>(yp + 2 * o) = u32x4_t{s0[0], s1[0], s0[1], s1[1]};
+      }
+  }
+}
+
+// A workgroup for every CU, each walking its XCD's tiles; an expert's rest
+// takes the smallest of four heights that holds it.
+__global__ void __launch_bounds__(512) wide_kernel(MArgs a) {
+  // stages as separate objects, so that the compiler sees that filling one
+  // does not touch the others
+  __shared__ __attribute__((aligned(1024))) uint8_t lds0[kWideStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds1[kWideStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds2[kWideStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds3[kWideStage];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col_tiles = (a.d_out + kWideBN - 1) / kWideBN;
+  const Tiles n = count_tiles<kWideBM>(a);
+  const int xcd = blockIdx.x % kXcds, stride = gridDim.x / kXcds;
+  int64_t at = blockIdx.x / kXcds;
+  Tile tl = find_tile<kWideBM>(a, n, col_tiles, xcd, at);
+  if (tl.count <= 0) return;
+  WideSource f = wide_source(a, tl, wave, lane);
+  wide_fetch(f, lds0, wave);
+  wide_fetch(f, lds1, wave);
+  wide_fetch(f, lds2, wave);
+  landed<kWideLoads>();
+  for (;;) {
+    at += stride;
+    const Tile next = find_tile<kWideBM>(a, n, col_tiles, xcd, at);
+    const WideSource nf = wide_source(a, next, wave, lane);
+    if (tl.count > 192)
+      wide_tile<4>(a, tl, f, nf, lds0, lds1, lds2, lds3);
+    else if (tl.count > 128)
+      wide_tile<3>(a, tl, f, nf, lds0, lds1, lds2, lds3);
+    else if (tl.count > 64)
+      wide_tile<2>(a, tl, f, nf, lds0, lds1, lds2, lds3);
+    else
+      wide_tile<1>(a, tl, f, nf, lds0, lds1, lds2, lds3);
+    if (next.count <= 0) break;
+    tl = next;
+  }
+  // no load may reach the LDS after the workgroup has left it
+  landed<0>();
+}
+
+}  // namespace
+
+gsi_status launch_wide(const MArgs &a, hipStream_t st) {
+  constexpr int kCus = 256;
+  wide_kernel<<<kCus, 512, 0, st>>>(a);
+  return hipGetLastError() == hipSuccess ? GSI_OK : GSI_E_HIP;
+}
+
+}  // namespace gsi
