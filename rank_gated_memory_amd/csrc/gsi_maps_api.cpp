@@ -51,6 +51,7 @@ gsi_status run_maps(const gsi_weights *w, const void *x, int64_t ldx, int32_t T,
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const int per = R / (w->n < R ? w->n : R);  // rows per expert, on average
   if (w->bits == 0 && w->dtype == GSI_BF16 && per >= 64) return launch_wide(a, st);
+  if (w->bits == 4 && w->dtype == GSI_BF16 && per > 64) return launch_wide_q4(a, w->group, st);
   const bool f32 = w->dtype == GSI_FP32;
   return launch_stream(a, w->bits ? (f32 ? kQ4F32 : kQ4Bf16) : (f32 ? kF32 : kBf16), w->group, st);
 }

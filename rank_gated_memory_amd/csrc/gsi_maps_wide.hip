@@ -106,7 +106,10 @@ __device__ __forceinline__ void to_lds(const void *src, void *dst) {
                                    (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
 }
 
-// Every wavefront's own loads to LDS but the last N have landed, then all wavefronts'.
+// Every wavefront's own loads but the last N have landed, then all wavefronts'.
+// Loads return in order, so N may count any load issued since those that are
+// waited for; it must not be more than there are (a test counts them in the
+// compiled code).
 template <int N>
 __device__ __forceinline__ void landed() {
   static_assert(N < 64, "vmcnt");
@@ -312,11 +315,244 @@ __global__ void __launch_bounds__(512) wide_kernel(MArgs a) {
   landed<0>();
 }
 
+// 4-bit weights: tiles of 256 tokens x 128 weight rows on 8 wavefronts, 4 x 2
+// of them, each 32 TM tokens x 64 weight rows.  x arrives in LDS as above; the
+// codes go through registers, 64 bytes of each weight row at a time, and are
+// decoded once for all 256 tokens, to q - z, which bf16 holds exactly.  Every
+// group has a sum of its own in the matrix core's accumulators and is added
+// to the fp32 total with the group's scale, so nothing is rounded but fp32
+// sums.  Here A holds tokens and B weight rows: a lane's accumulators belong
+// to one weight row of each block and take one scale.
+constexpr int kQ4BN = 128;
+constexpr int kQ4X = kWideBM * kWideBK * 2, kQ4W = kQ4BN * kWideBK * 2;  // bytes of a stage
+
+// A stage's x and W, objects of their own: the compiler lets a store to LDS
+// wait for every load to LDS that may go to the same object.
+struct Q4Stage {
+  uint8_t *x, *w;
+};
+
+template <int G, int TM>
+__device__ __forceinline__ void q4_tile(const MArgs &a, const Tile &tl, const Q4Stage &lds0, const Q4Stage &lds1,
+                                        const Q4Stage &lds2, const Q4Stage &lds3) {
+  constexpr int TN = 2, kBlock = 32 * kWideBK * 2, NG = 128 / G;  // groups of 128 columns
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1, l32 = lane & 31, half = lane >> 5;
+  const int i0 = tl.col * kQ4BN;
+
+  // x: two loads to LDS of a wavefront per stage
+  const int sub = lane >> 2, piece = ((lane & 3) ^ swizzle<kWideBK>(sub)) * 8;
+  const uint8_t *xp[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = tl.row + min((wave * 2 + i) * 16 + sub, tl.count - 1);
+    const int src = a.rows ? a.rows[r] : r;
+    xp[i] = a.x + ((int64_t)(src < 0 || src >= a.T ? 0 : src) * a.ldx + piece) * 2;
+  }
+  int left = a.d - piece;
+  const uint64_t zero_page = reinterpret_cast<uint64_t>(&kZeros);
+  const auto fetch = [&](const Q4Stage &st) {
+    const uint64_t in = (int64_t)(-left) >> 63;  // all ones while left > 0
+    left -= kWideBK;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      to_lds(reinterpret_cast<const void *>((reinterpret_cast<uint64_t>(xp[i]) & in) | (zero_page & ~in)),
+             st.x + (wave * 2 + i) * 1024);
+      xp[i] += 2 * kWideBK;
+    }
+  };
+
+  // Codes: this thread's 16 bytes of weight row tid / 4, columns 32 (tid % 4)
+  // on of each 128, and the zeros of their groups.  Behind d it reads the
+  // row's first bytes and the last group's zero: x is zero there.
+  const int wr = tid >> 2, part = tid & 3, row_bytes = a.d / 2;
+  const int64_t row = (int64_t)tl.e * a.d_out + min(i0 + wr, a.d_out - 1);
+  const uint8_t *const cp = a.W + tl.e * a.w_stride + (int64_t)min(i0 + wr, a.d_out - 1) * row_bytes;
+  // without zeros as many bytes of the scales are read and dropped: a step's
+  // wait counts its loads
+  const uint8_t *const zp = (a.zeros ? a.zeros : a.scales) + row * a.groups;
+  struct Codes {
+    u32x4_t c;
+    uint32_t z[NG];
+  };
+  const auto load_codes = [&](Codes &o, int n) {
+    const int at = n * 64 + 16 * part;
+    o.c = *reinterpret_cast<const u32x4_t *>(cp + (at < row_bytes ? at : 0));
+#pragma unroll
+    for (int g = 0; g < NG; ++g) o.z[g] = zp[min(n * NG + g, a.groups - 1)];
+  };
+  // Stage s of 128 columns: its 32 codes of the row lie with lane s of the
+  // row's four lanes, dword p for lane p.
+  uint32_t mine[4];  // all ones for this lane's dword
+#pragma unroll
+  for (int p = 0; p < 4; ++p) mine[p] = part == p ? ~0u : 0u;
+  const auto decode_to = [&](const Q4Stage &st, const Codes &o, auto sc) {
+    constexpr int s = decltype(sc)::value, kPerm = s * 0x55;  // every lane of four reads lane s
+    uint32_t c = 0;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) c |= __builtin_amdgcn_mov_dpp(o.c[p], kPerm, 0xf, 0xf, true) & mine[p];
+    const float z = a.zeros ? (float)(o.z[s * 32 / G] & 15) : 8.f;
+    const uint32_t even = c & 0x0f0f0f0fu, odd = c >> 4 & 0x0f0f0f0fu;
+    u32x4_t w;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float lo = (float)(even >> (8 * k) & 255) - z, hi = (float)(odd >> (8 * k) & 255) - z;
+      w[k] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+    }
+    *reinterpret_cast<u32x4_t *>(st.w + tile_at<kWideBK>(wr, part)) = w;
+  };
+
+  // scales of this lane's weight rows
+  const uint16_t *sp[TN];
+#pragma unroll
+  for (int i = 0; i < TN; ++i)
+    sp[i] = reinterpret_cast<const uint16_t *>(a.scales) +
+            ((int64_t)tl.e * a.d_out + min(i0 + wn * 64 + i * 32 + l32, a.d_out - 1)) * a.groups;
+  const auto load_scales = [&](uint32_t (&o)[NG][TN], int n) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int i = 0; i < TN; ++i) o[g][i] = sp[i][min(n * NG + g, a.groups - 1)];
+  };
+
+  f32x16_t total[TN][TM] = {}, sum[TN][TM];
+  int xat[2], wat[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    xat[s] = wm * TM * kBlock + tile_at<kWideBK>(l32, 2 * s + half);
+    wat[s] = wn * TN * kBlock + tile_at<kWideBK>(l32, 2 * s + half);
+  }
+  bf16x8_t wf[2][TN], xf[2][TM];
+  const auto read = [&](const Q4Stage &st, int s) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+      wf[s][j] = as_bf16x8(*reinterpret_cast<const u32x4_t *>(st.w + wat[s] + j * kBlock));
+#pragma unroll
+    for (int j = 0; j < TM; ++j)
+      xf[s][j] = as_bf16x8(*reinterpret_cast<const u32x4_t *>(st.x + xat[s] + j * kBlock));
+  };
+  const auto multiply = [&](int s, auto first) {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
+    const f32x16_t none = {};
+#pragma unroll
+    for (int j = 0; j < TM; ++j)
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+        sum[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xf[s][j], wf[s][i], decltype(first)::value ? none : sum[i][j],
+                                                            0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  uint32_t sc[NG][TN];
+  // Step s of 128 columns, as in wide_tile; N loads of its own may be under
+  // way when it ends.
+  const auto step = [&](auto sc_, const Q4Stage &cur, const Q4Stage &next, const Q4Stage &fill, const Codes &o,
+                        auto n) {
+    constexpr int s = decltype(sc_)::value, per = G / 32;
+    read(cur, 1);
+    multiply(0, std::integral_constant<bool, s % per == 0>{});
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    fetch(fill);
+    decode_to(fill, o, std::integral_constant<int, (s + 3) % 4>{});
+    read(next, 0);
+    multiply(1, std::false_type{});
+    if constexpr ((s + 1) % per == 0) {
+#pragma unroll
+      for (int i = 0; i < TN; ++i) {
+        const float f = __uint_as_float(sc[s / per][i] << 16);
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) total[i][j][e] += f * sum[i][j][e];
+          asm volatile("" : "+v"(total[i][j]));  // here: the compiler would carry the sums on
+        }
+      }
+    }
+    landed<decltype(n)::value>();
+  };
+
+  constexpr int kOwn = 2, kMore = 1 + NG + NG * TN;  // loads of a step; of codes, zeros and scales
+  const int rounds = (a.d + 127) / 128;
+  Codes c0, c1, c2;
+  load_codes(c0, 0);
+  load_codes(c1, 1);
+  load_scales(sc, 0);
+  fetch(lds0);
+  fetch(lds1);
+  fetch(lds2);
+  decode_to(lds0, c0, std::integral_constant<int, 0>{});
+  decode_to(lds1, c0, std::integral_constant<int, 1>{});
+  decode_to(lds2, c0, std::integral_constant<int, 2>{});
+  landed<0>();
+  read(lds0, 0);
+  for (int n = 0; n < rounds; ++n) {
+    uint32_t sn[NG][TN];
+    load_codes(c2, n + 2);
+    load_scales(sn, n + 1);
+    step(std::integral_constant<int, 0>{}, lds0, lds1, lds3, c0, std::integral_constant<int, kOwn + kMore>{});
+    step(std::integral_constant<int, 1>{}, lds1, lds2, lds0, c1, std::integral_constant<int, kOwn>{});
+    step(std::integral_constant<int, 2>{}, lds2, lds3, lds1, c1, std::integral_constant<int, kOwn>{});
+    step(std::integral_constant<int, 3>{}, lds3, lds0, lds2, c1, std::integral_constant<int, kOwn>{});
+    c0 = c1;
+    c1 = c2;
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int i = 0; i < TN; ++i) sc[g][i] = sn[g][i];
+  }
+  landed<0>();
+
+#pragma unroll
+  for (int j = 0; j < TM; ++j)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int m = (wm * TM + j) * 32 + 8 * (e / 4) + 4 * half + e % 4;
+      if (m >= tl.count) continue;
+      const int r = tl.row + m;
+      const int src = a.rows ? a.rows[r] : r;
+      const bool has = src >= 0 && src < a.T;
+#pragma unroll
+      for (int i = 0; i < TN; ++i) {
+        const int o = i0 + wn * 64 + i * 32 + l32;
+        if (o < a.d_out) reinterpret_cast<__bf16 *>(a.y)[r * a.ldy + o] = has ? (__bf16)total[i][j][e] : (__bf16)0.f;
+      }
+    }
+}
+
+template <int G>
+__global__ void __launch_bounds__(512) q4_wide_kernel(MArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t x0[kQ4X], x1[kQ4X], x2[kQ4X], x3[kQ4X];
+  __shared__ __attribute__((aligned(1024))) uint8_t w0[kQ4W], w1[kQ4W], w2[kQ4W], w3[kQ4W];
+  const Tiles n = count_tiles<kWideBM>(a);
+  const Tile tl = find_tile<kWideBM>(a, n, (a.d_out + kQ4BN - 1) / kQ4BN, blockIdx.x % kXcds, blockIdx.x / kXcds);
+  if (tl.count <= 0) return;
+  if (tl.count > 128)
+    q4_tile<G, 2>(a, tl, {x0, w0}, {x1, w1}, {x2, w2}, {x3, w3});
+  else
+    q4_tile<G, 1>(a, tl, {x0, w0}, {x1, w1}, {x2, w2}, {x3, w3});
+}
+
 }  // namespace
 
 gsi_status launch_wide(const MArgs &a, hipStream_t st) {
   constexpr int kCus = 256;
   wide_kernel<<<kCus, 512, 0, st>>>(a);
+  return hipGetLastError() == hipSuccess ? GSI_OK : GSI_E_HIP;
+}
+
+gsi_status launch_wide_q4(const MArgs &a, int group, hipStream_t st) {
+  // full tiles and rests: at most R / 256 of the ones and one rest per expert
+  // with rows, each list rounded up to whole shares
+  const int64_t slots = a.R / kWideBM + (a.n < a.R ? a.n : a.R);
+  const int64_t grid = (slots * ((a.d_out + kQ4BN - 1) / kQ4BN) + 2 * kXcds) / kXcds * kXcds;
+  if (grid > INT32_MAX) return GSI_E_SHAPE;
+  if (group == 128)
+    q4_wide_kernel<128><<<(unsigned)grid, 512, 0, st>>>(a);
+  else if (group == 64)
+    q4_wide_kernel<64><<<(unsigned)grid, 512, 0, st>>>(a);
+  else
+    q4_wide_kernel<32><<<(unsigned)grid, 512, 0, st>>>(a);
   return hipGetLastError() == hipSuccess ? GSI_OK : GSI_E_HIP;
 }
 

@@ -54,3 +54,30 @@ def test_hot_kernels_keep_their_occupancy(source, pattern, waves, flags):
     for k, v in hits.items():
         assert v.get("Occupancy", 0) >= waves, f"{k}: {v}"
         assert v.get("VGPRs Spill", 0) == 0, f"{k} spills registers: {v}"
+
+
+@pytest.mark.skipif(not os.path.exists("/opt/rocm/bin/hipcc"), reason="hipcc not installed")
+def test_wide_maps_wait_for_their_stages(tmp_path):
+    """The wide map kernels let the loads of the running step be under way when
+    it ends (vmcnt counts them) and need every older one to have landed.  Were
+    there fewer loads in a step than it allows, e.g. because the compiler had
+    merged two, a stage could be read before it is there; no test of numbers
+    would show that reliably, so the compiled steps are counted."""
+    out = str(tmp_path / "wide.s")
+    cmd = ["/opt/rocm/bin/hipcc", *[f for f in build.FLAGS if f not in ("-shared", "-fPIC")],
+           "--cuda-device-only", "-S", os.path.join(CSRC, "gsi_maps_wide.hip"), "-o", out]
+    assert subprocess.run(cmd, capture_output=True, timeout=900).returncode == 0
+    loads, steps, allowed = 0, 0, None
+    for line in open(out):
+        op = line.split()[0] if line.split() else ""
+        if re.match(r"(global|buffer|flat|scratch)_load", op):
+            loads += 1
+        elif op == "s_waitcnt" and "vmcnt" in line:
+            allowed = int(re.search(r"vmcnt\((\d+)\)", line).group(1))
+        elif op == "s_barrier":
+            assert allowed is not None and allowed <= loads, f"{allowed} loads may be under way after {loads}"
+            steps += allowed > 0
+            loads, allowed = 0, None
+        elif line.startswith((".LBB", "_Z")) or op.startswith(("s_cbranch", "s_branch")):
+            loads, allowed = 0, None  # a step is straight-line code
+    assert steps >= 4 * 4 + 4 * 6, steps  # four heights of bf16 tiles, two of each group size
