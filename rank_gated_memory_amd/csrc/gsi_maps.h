@@ -37,6 +37,7 @@ enum Kind { kQ4Bf16, kQ4F32, kBf16, kF32 };
 // Launchers; group is 0 for dense kinds.  launch_wide: dense bf16.
 gsi_status launch_stream(const MArgs &a, Kind kind, int group, hipStream_t st);
 gsi_status launch_wide(const MArgs &a, hipStream_t st);
+gsi_status launch_small(const MArgs &a, Kind kind, hipStream_t st);       // dense
 gsi_status launch_wide_q4(const MArgs &a, int group, hipStream_t st);  // bf16 x
 
 namespace {

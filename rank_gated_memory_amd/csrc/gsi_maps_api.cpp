@@ -24,6 +24,33 @@ gsi_status check_weights(const gsi_weights *w) {
   return GSI_OK;
 }
 
+// Which kernel: the rows per expert and the tiles there are decide, both known
+// from the call's sizes alone (the offsets are on the device).
+gsi_status choose(const MArgs &a, const gsi_weights &w, hipStream_t st) {
+  const bool f32 = w.dtype == GSI_FP32;
+  const int64_t experts = a.n < a.R ? a.n : a.R, per = a.R / experts;
+  if (w.bits == 4) {
+    // Large tiles once they beat streaming the weights for every 16 rows: a
+    // round of 256 tiles takes as long as about 6000 blocks of 16 x 16 there
+    // (4096 -> 16384: 64 tokens 62 us in tiles, 37 us streamed; 100 tokens
+    // 63 and 62; 512 tokens 85 and 182).
+    const int64_t tiles = (a.R / 256 + experts) * ((a.d_out + 127) / 128);
+    const int64_t blocks = (a.R / 16 + experts) * ((a.d_out + 15) / 16);
+    if (!f32 && blocks >= 6000 * ((tiles + 255) / 256)) return launch_wide_q4(a, w.group, st);
+    return launch_stream(a, f32 ? kQ4F32 : kQ4Bf16, w.group, st);
+  }
+  // Streaming up to 8 rows per expert (16 experts 2048 -> 2048: 9 rows each
+  // 27 us both ways, 14 rows 40 us streamed and 28 us in small tiles).
+  if (per <= 8) return launch_stream(a, f32 ? kF32 : kBf16, 0, st);
+  // Large tiles where there is at least one for every CU, or half as many full
+  // ones (64 experts 2048 -> 4096, 32 rows each: 139 us, 178 in small tiles;
+  // 16 experts 2048 -> 1024, 100 rows: 54 and 30 us; 8 experts 2048 -> 2048,
+  // 300 rows: 57 and 64 us).
+  const int64_t tiles = (a.R / 256 + experts) * ((a.d_out + 255) / 256);
+  if (!f32 && (tiles >= 256 || (tiles >= 128 && per >= 128))) return launch_wide(a, st);
+  return launch_small(a, f32 ? kF32 : kBf16, st);
+}
+
 gsi_status run_maps(const gsi_weights *w, const void *x, int64_t ldx, int32_t T, const int32_t *offsets,
                     const int32_t *rows, void *y, int64_t ldy, int32_t R, void *stream) {
   const int es = w->dtype == GSI_FP32 ? 4 : 2;
@@ -49,11 +76,7 @@ gsi_status run_maps(const gsi_weights *w, const void *x, int64_t ldx, int32_t T,
   a.T = T;
   a.groups = w->bits ? (w->d + w->group - 1) / w->group : 0;
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  const int per = R / (w->n < R ? w->n : R);  // rows per expert, on average
-  if (w->bits == 0 && w->dtype == GSI_BF16 && per >= 64) return launch_wide(a, st);
-  if (w->bits == 4 && w->dtype == GSI_BF16 && per > 64) return launch_wide_q4(a, w->group, st);
-  const bool f32 = w->dtype == GSI_FP32;
-  return launch_stream(a, w->bits ? (f32 ? kQ4F32 : kQ4Bf16) : (f32 ? kF32 : kBf16), w->group, st);
+  return choose(a, *w, st);
 }
 
 }  // namespace

@@ -1,13 +1,18 @@
 // Plain linear maps with few rows per expert on gfx950 MFMA.
 //
-//   stream_kernel : the weights of an expert are read once for a chunk of 16
-//                   TB rows.  Bound by HBM: at one token a weight is used
+//   stream_kernel : the weights of an expert are read once for a chunk of up
+//                   to 16 rows.  Bound by HBM: at one token a weight is used
 //                   once, so the chunk's x is staged in LDS and the wavefronts
 //                   do nothing but stream weights into registers, a batch of
-//                   loads ahead of the products.  A wavefront owns 16 RB
-//                   weight rows; where there are fewer such blocks than the
-//                   chip has wavefronts, KS of them split the columns of a
-//                   block and are joined through LDS in a fixed order.
+//                   loads ahead of the products.  A wavefront owns 16 weight
+//                   rows; where there are fewer such blocks than the chip has
+//                   wavefronts, several split the columns of a block and are
+//                   joined through LDS in a fixed order.  Further chunks of an
+//                   expert read its weights again, out of the L2s.  (Chunks of
+//                   32 and 64 rows, with two blocks of weight rows per
+//                   wavefront, were slower at every number of rows: 28 and 69
+//                   us instead of 22 and 23 for 24 and 40 tokens of a 4-bit
+//                   4096 x 4096 map.)
 //
 // 4-bit weights.  With w = s (q - z) a group's share of y is
 //   s (sum q x - z sum x) = s (sum (16 + q) x - (16 + z) sum x).
@@ -140,7 +145,7 @@ struct StreamShape {
   int column_parts;  // of d
 };
 
-template <Kind K, int G, int TB, int RB, int U>
+template <Kind K, int G, int U>
 struct Stream {
   static constexpr bool q4 = K == kQ4Bf16 || K == kQ4F32;
   static constexpr bool f32 = K == kQ4F32 || K == kF32;
@@ -155,42 +160,37 @@ struct Stream {
 
   // U steps of weights with their scales
   struct Batch {
-    u32x4_t w[U][RB];
-    uint32_t s[q4 ? RB : 1][SW], z[q4 ? RB : 1][ZW];
+    u32x4_t w[U];
+    uint32_t s[SW], z[ZW];
   };
 
   const MArgs &a;
   DecodeBits bits;
   int quad, l16, row_bytes;
-  // the first block's first row, and this lane's offsets from there: 32 bits,
-  // for at most 32 rows
+  // the block's first row, and this lane's offsets from there: 32 bits, for at
+  // most 16 rows
   const uint8_t *wp, *sp, *zp;
-  uint32_t wo[RB], so[RB], zo[RB];
+  uint32_t wo, so, zo;
 
   __device__ __forceinline__ Stream(const MArgs &args, int lane) : a(args) {
     quad = lane >> 4, l16 = lane & 15;
     row_bytes = q4 ? a.d / 2 : a.d * es;
   }
 
-  // The blocks of weight rows from i0 < d_out on; rows behind the last read
+  // The block of weight rows from i0 < d_out on; rows behind the last read
   // the last, and what they give is not stored.
   __device__ __forceinline__ void rows_from(int e, int i0) {
     const int64_t row = (int64_t)e * a.d_out + i0;
+    const uint32_t i = min(l16, a.d_out - 1 - i0);
     wp = a.W + e * a.w_stride + (int64_t)i0 * row_bytes;
+    wo = i * row_bytes + 16 * quad;
     if constexpr (q4) {
       sp = a.scales + row * a.groups * es;
+      so = i * a.groups * es;
       // without zeros their loads read 16 bytes of the scales, which there are
       // at least, and the value is dropped
       zp = a.zeros ? a.zeros + row * a.groups : a.scales;
-    }
-#pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      const uint32_t i = min(16 * b + l16, a.d_out - 1 - i0);
-      wo[b] = i * row_bytes + 16 * quad;
-      if constexpr (q4) {
-        so[b] = i * a.groups * es;
-        zo[b] = a.zeros ? i * a.groups : 0;
-      }
+      zo = a.zeros ? i * a.groups : 0;
     }
   }
 
@@ -205,46 +205,40 @@ struct Stream {
   // The U whole steps from `step` on.
   __device__ __forceinline__ void load(Batch &o, int step) const {
 #pragma unroll
-    for (int b = 0; b < RB; ++b) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) o.w[u][b] = *reinterpret_cast<const u32x4_t *>(wp + (wo[b] + (uint32_t)step * 64) + u * 64);
-      if constexpr (q4) {
-        using T = std::conditional_t<f32, uint32_t, uint16_t>;
-        copy_run<T, BG>(o.s[b], sp + (so[b] + (uint32_t)(step * NG * es)));
-        copy_run<uint8_t, BG>(o.z[b], zp + (zo[b] + (uint32_t)(a.zeros ? step * NG : 0)));
-      }
+    for (int u = 0; u < U; ++u) o.w[u] = *reinterpret_cast<const u32x4_t *>(wp + (wo + (uint32_t)step * 64) + u * 64);
+    if constexpr (q4) {
+      using T = std::conditional_t<f32, uint32_t, uint16_t>;
+      copy_run<T, BG>(o.s, sp + (so + (uint32_t)(step * NG * es)));
+      copy_run<uint8_t, BG>(o.z, zp + (zo + (uint32_t)(a.zeros ? step * NG : 0)));
     }
   }
 
   // Step `step` alone as step 0 of a batch; it may end behind the row.
   __device__ __forceinline__ void load_last(Batch &o, int step) const {
+    o.w[0] = u32x4_t{0, 0, 0, 0};
+    if (step * 64 + 16 * quad < row_bytes) o.w[0] = *reinterpret_cast<const u32x4_t *>(wp + (wo + (uint32_t)step * 64));
+    if constexpr (q4) {
 #pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      o.w[0][b] = u32x4_t{0, 0, 0, 0};
-      if (step * 64 + 16 * quad < row_bytes) o.w[0][b] = *reinterpret_cast<const u32x4_t *>(wp + (wo[b] + (uint32_t)step * 64));
-      if constexpr (q4) {
+      for (int g = 0; g < SW; ++g) o.s[g] = 0;
+      o.z[0] = 0;
 #pragma unroll
-        for (int g = 0; g < SW; ++g) o.s[b][g] = 0;
-        o.z[b][0] = 0;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const int at = min(step * NG + g, a.groups - 1);  // behind the last group x is zero
-          if constexpr (f32)
-            o.s[b][g] = *reinterpret_cast<const uint32_t *>(sp + (so[b] + 4u * at));
-          else
-            o.s[b][g / 2] |= (uint32_t) * reinterpret_cast<const uint16_t *>(sp + (so[b] + 2u * at)) << (16 * (g & 1));
-          o.z[b][0] |= (uint32_t)zp[zo[b] + (a.zeros ? at : 0)] << (8 * g);
-        }
+      for (int g = 0; g < NG; ++g) {
+        const int at = min(step * NG + g, a.groups - 1);  // behind the last group x is zero
+        if constexpr (f32)
+          o.s[g] = *reinterpret_cast<const uint32_t *>(sp + (so + 4u * at));
+        else
+          o.s[g / 2] |= (uint32_t) * reinterpret_cast<const uint16_t *>(sp + (so + 2u * at)) << (16 * (g & 1));
+        o.z[0] |= (uint32_t)zp[zo + (a.zeros ? at : 0)] << (8 * g);
       }
     }
   }
 
   __device__ __forceinline__ static int x_stride(int columns) { return columns * xes + 16; }
 
-  // x of the chunk's columns [c0, c0 + columns) into LDS: a plane of 16 TB
-  // tokens for each part, zeros behind d and for rows without a source, octets
-  // in the order of decode() where the weights are codes.  Only the chunk's
-  // own rows are written; those behind them are never read.
+  // x of the chunk's columns [c0, c0 + columns) into LDS: a plane of tokens for
+  // each part, zeros behind d and for rows without a source, octets in the
+  // order of decode() where the weights are codes.  Only the chunk's own rows
+  // are written; those behind them are never read.
   __device__ __forceinline__ void stage(uint8_t *lds, const Chunk &ch, int c0, int columns) const {
     constexpr int V = K == kF32 ? 4 : 8;  // columns of a 16-byte piece
     const int pieces = columns / V, stride = x_stride(columns);
@@ -272,33 +266,24 @@ struct Stream {
     }
   }
 
-  // Where this lane's tokens lie in LDS; a lane without a token reads the first.
-  struct Tokens {
-    const uint8_t *x[TB];
+  // Where this lane's token lies in LDS; a lane without a token reads the first.
+  struct Token {
+    const uint8_t *x;
     int plane;
   };
-  __device__ __forceinline__ Tokens tokens(const uint8_t *lds, const Chunk &ch, int columns) const {
-    Tokens t;
-    const int stride = x_stride(columns);
-    t.plane = ch.count * stride;
-#pragma unroll
-    for (int j = 0; j < TB; ++j) {
-      const int m = 16 * j + 4 * (l16 & 3) + (l16 >> 2);
-      t.x[j] = lds + (m < ch.count ? m : 0) * stride + quad * (q4 && G == 128 ? 64 : 16);
-    }
-    return t;
+  __device__ __forceinline__ Token token(const uint8_t *lds, const Chunk &ch, int columns) const {
+    const int stride = x_stride(columns), m = 4 * (l16 & 3) + (l16 >> 2);
+    return {lds + (m < ch.count ? m : 0) * stride + quad * (q4 && G == 128 ? 64 : 16), ch.count * stride};
   }
 
   // The products of a batch's first N steps into acc, x from `at` bytes on;
   // accumulators from NI on stay zero.
   template <int NI, int N>
-  __device__ __forceinline__ void multiply(f32x4_t (&acc)[RB][TB], const Batch &o, const Tokens &tk, int at) const {
-    uint32_t z16[q4 ? RB : 1][ZW];  // 16 + zero, a byte each
+  __device__ __forceinline__ void multiply(f32x4_t &acc, const Batch &o, const Token &tk, int at) const {
+    uint32_t z16[ZW];  // 16 + zero, a byte each
     if constexpr (q4) {
 #pragma unroll
-      for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int k = 0; k < ZW; ++k) z16[b][k] = a.zeros ? (o.z[b][k] & bits.low) | bits.sixteen : 0x18181818u;
+      for (int k = 0; k < ZW; ++k) z16[k] = a.zeros ? (o.z[k] & bits.low) | bits.sixteen : 0x18181818u;
     }
 #pragma unroll
     for (int u = 0; u < N; ++u) {
@@ -306,103 +291,74 @@ struct Stream {
       __builtin_amdgcn_sched_barrier(0);
       const int xo = at + u * C * xes;
       if constexpr (!q4) {
-        u32x4_t x[TB];
+        const u32x4_t x = *reinterpret_cast<const u32x4_t *>(tk.x + xo);
+        if constexpr (K == kBf16) {
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(x), as_bf16x8(o.w[u]), acc, 0, 0, 0);
+        } else {
 #pragma unroll
-        for (int t = 0; t < TB; ++t) x[t] = *reinterpret_cast<const u32x4_t *>(tk.x[t] + xo);
-#pragma unroll
-        for (int b = 0; b < RB; ++b)
-#pragma unroll
-          for (int t = 0; t < TB; ++t) {
-            if constexpr (K == kBf16) {
-              acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(x[t]), as_bf16x8(o.w[u][b]), acc[b][t], 0, 0, 0);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x[t][i]), __uint_as_float(o.w[u][b][i]),
-                                                                 acc[b][t], 0, 0, 0);
-            }
-          }
+          for (int i = 0; i < 4; ++i)
+            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x[i]), __uint_as_float(o.w[u][i]), acc, 0, 0, 0);
+        }
       } else {
         // Product i of a step covers, for G = 128, columns 32 quad + 8 i + e;
         // for smaller groups columns 32 i + 8 quad + e, so that no product
         // mixes groups.
         constexpr int PG = 4 / NG;  // products of a group
         const f32x4_t zero4 = {0, 0, 0, 0};
-        const u32x4_t one_bits = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-        u32x4_t c[RB];
-
-#pragma unroll
-        for (int b = 0; b < RB; ++b) {
-          c[b] = o.w[u][b];
-          if constexpr (G < 128) {  // dword j of quad i <- dword i of quad j
-            const auto p = __builtin_amdgcn_permlane32_swap(c[b][0], c[b][2], false, false);
-            const auto q = __builtin_amdgcn_permlane32_swap(c[b][1], c[b][3], false, false);
-            const auto r = __builtin_amdgcn_permlane16_swap(p[0], q[0], false, false);
-            const auto s = __builtin_amdgcn_permlane16_swap(p[1], q[1], false, false);
-            c[b] = u32x4_t{r[0], r[1], s[0], s[1]};
-          }
+        const u32x4_t ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+        u32x4_t c = o.w[u];
+        if constexpr (G < 128) {  // dword j of quad i <- dword i of quad j
+          const auto p = __builtin_amdgcn_permlane32_swap(c[0], c[2], false, false);
+          const auto q = __builtin_amdgcn_permlane32_swap(c[1], c[3], false, false);
+          const auto r = __builtin_amdgcn_permlane16_swap(p[0], q[0], false, false);
+          const auto s = __builtin_amdgcn_permlane16_swap(p[1], q[1], false, false);
+          c = u32x4_t{r[0], r[1], s[0], s[1]};
         }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          if (TB > 1 && g > 0) __builtin_amdgcn_sched_barrier(0);
-          bf16x8_t w[RB][PG];
-          float s[RB], z[RB];
+          const int k = u * NG + g;
+          const float s = f32 ? __uint_as_float(o.s[k])
+                              : __uint_as_float(k & 1 ? o.s[k / 2] & 0xffff0000u : o.s[k / 2] << 16);
+          const float z = (float)(z16[k / 4] >> (8 * (k & 3)) & 255);
+          f32x4_t q = zero4, sx = zero4;
 #pragma unroll
-          for (int b = 0; b < RB; ++b) {
-            const int k = u * NG + g;
+          for (int i = 0; i < PG; ++i) {
+            const bf16x8_t w = decode(c[g * PG + i], bits);
 #pragma unroll
-            for (int i = 0; i < PG; ++i) w[b][i] = decode(c[b][g * PG + i], bits);
-            s[b] = f32 ? __uint_as_float(o.s[b][k])
-                       : __uint_as_float(k & 1 ? o.s[b][k / 2] & 0xffff0000u : o.s[b][k / 2] << 16);
-            z[b] = (float)(z16[b][k / 4] >> (8 * (k & 3)) & 255);
-          }
-#pragma unroll
-          for (int t = 0; t < TB; ++t) {
-            f32x4_t q[RB], sx = zero4;
-#pragma unroll
-            for (int b = 0; b < RB; ++b) q[b] = zero4;
-#pragma unroll
-            for (int i = 0; i < PG; ++i)
-#pragma unroll
-              for (int p = 0; p < XP; ++p) {
-                const bf16x8_t x = as_bf16x8(*reinterpret_cast<const u32x4_t *>(
-                    tk.x[t] + p * tk.plane + xo + (g * PG + i) * (G == 128 ? 16 : 64)));
-                sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, as_bf16x8(one_bits), sx, 0, 0, 0);
-#pragma unroll
-                for (int b = 0; b < RB; ++b) q[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w[b][i], q[b], 0, 0, 0);
-              }
-#pragma unroll
-            for (int b = 0; b < RB; ++b) {
-#pragma unroll
-              for (int i = 0; i < NI; ++i) acc[b][t][i] += s[b] * (q[b][i] - z[b] * sx[i]);
-              // here, not after the next batch's loads, where the compiler
-              // would carry q and sx of every group to
-              asm volatile("" : "+v"(acc[b][t]));
+            for (int p = 0; p < XP; ++p) {
+              const bf16x8_t x = as_bf16x8(*reinterpret_cast<const u32x4_t *>(tk.x + p * tk.plane + xo +
+                                                                              (g * PG + i) * (G == 128 ? 16 : 64)));
+              sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, as_bf16x8(ones), sx, 0, 0, 0);
+              q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, q, 0, 0, 0);
             }
           }
+#pragma unroll
+          for (int i = 0; i < NI; ++i) acc[i] += s * (q[i] - z * sx[i]);
+          // here, not after the next batch's loads, where the compiler would
+          // carry q and sx of every group to
+          asm volatile("" : "+v"(acc));
         }
       }
     }
   }
 };
 
-template <Kind K, int G, int TB, int RB, int U>
-__global__ void __launch_bounds__(kStreamWaves * 64, TB == 1 ? 4 : 2) stream_kernel(MArgs a, StreamShape sh) {
-  using S = Stream<K, G, TB, RB, U>;
-  constexpr int kRed = RB * TB * 256;  // sums of a wavefront
+template <Kind K, int G, int U>
+__global__ void __launch_bounds__(kStreamWaves * 64, 4) stream_kernel(MArgs a, StreamShape sh) {
+  using S = Stream<K, G, U>;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  __shared__ float red[kStreamWaves][kRed];
+  __shared__ float red[kStreamWaves][256];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Chunk ch = find_chunk(a, blockIdx.x / sh.strips, 16 * TB);
+  const Chunk ch = find_chunk(a, blockIdx.x / sh.strips, 16);
   if (ch.count <= 0) return;
   S s(a, lane);
   // a workgroup's wavefronts: kStreamWaves / split blocks of weight rows, the
   // columns of each in `split` shares of whole batches
   const int side = wave / sh.split, share = wave % sh.split, sides = kStreamWaves / sh.split;
-  const int blocks = (a.d_out + 16 * RB - 1) / (16 * RB), groups = (blocks + sides - 1) / sides;
+  const int blocks = (a.d_out + 15) / 16, groups = (blocks + sides - 1) / sides;
   // accumulators of a lane that hold tokens
-  const int live = TB == 1 && S::q4 ? (ch.count + 3) / 4 : 4;
-  const auto tk = s.tokens(lds, ch, sh.columns);
+  const int live = S::q4 ? (ch.count + 3) / 4 : 4;
+  const auto tk = s.token(lds, ch, sh.columns);
   // a part's columns: whole batches, dealt to the split in even shares; what
   // is left of the row goes to the last share, step by step
   const auto share_of = [&](int part, int *step0, int *first, int *end, int *rest, int *last) {
@@ -419,13 +375,13 @@ __global__ void __launch_bounds__(kStreamWaves * 64, TB == 1 ? 4 : 2) stream_ker
   const auto first_batch = [&](int g, int part) {
     int step0, first, end, rest, last;
     share_of(part, &step0, &first, &end, &rest, &last);
-    s.rows_from(ch.e, min((g * sides + side) * 16 * RB, a.d_out - 1));
+    s.rows_from(ch.e, min((g * sides + side) * 16, a.d_out - 1));
     if (first < end) s.load(o[0], first);
   };
   int g = blockIdx.x % sh.strips;
   if (g < groups) first_batch(g, 0);
   for (; g < groups; g += sh.strips) {
-    f32x4_t acc[RB][TB] = {};
+    f32x4_t acc = {};
     for (int part = 0; part < sh.column_parts; ++part) {
       int step0, first, end, rest, last;
       share_of(part, &step0, &first, &end, &rest, &last);
@@ -458,22 +414,10 @@ __global__ void __launch_bounds__(kStreamWaves * 64, TB == 1 ? 4 : 2) stream_ker
       else if (g + sh.strips < groups)
         first_batch(g + sh.strips, 0);
     }
-    if (sh.split > 1) {
-      if (g >= sh.strips) __syncthreads();  // the sums of the last group have been read
-#pragma unroll
-      for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int t = 0; t < TB; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            red[wave][(b * TB + t) * 256 + (4 * i + s.quad) * 16 + s.l16] = acc[b][t][i];
-      __syncthreads();
-    }
-    // sums of one output: its wavefront's own, or those of the split in order
-    const auto put = [&](int side0, int k, float v) {
-      const int b = k / (TB * 256), token = k / 16 % (16 * TB);
-      const int i = (g * sides + side0) * 16 * RB + 16 * b + k % 16, r = ch.row + token;
-      if (token >= ch.count || i >= a.d_out) return;
+    // one output: token k / 16 and weight row k % 16 of block `b`
+    const auto put = [&](int b, int k, float v) {
+      const int i = (g * sides + b) * 16 + k % 16, r = ch.row + k / 16;
+      if (k / 16 >= ch.count || i >= a.d_out) return;
       if (a.rows) {
         const int src = a.rows[r];
         if (src < 0 || src >= a.T) v = 0.f;
@@ -484,39 +428,38 @@ __global__ void __launch_bounds__(kStreamWaves * 64, TB == 1 ? 4 : 2) stream_ker
         reinterpret_cast<__bf16 *>(a.y)[r * a.ldy + i] = (__bf16)v;
     };
     if (sh.split > 1) {
-      for (int k = threadIdx.x; k < sides * kRed; k += kStreamWaves * 64) {
-        const int side0 = k / kRed, in = k - side0 * kRed;
+      if (g >= sh.strips) __syncthreads();  // the sums of the last block have been read
+#pragma unroll
+      for (int i = 0; i < 4; ++i) red[wave][(4 * i + s.quad) * 16 + s.l16] = acc[i];
+      __syncthreads();
+      for (int k = threadIdx.x; k < sides * 256; k += kStreamWaves * 64) {
         float v = 0.f;
-        for (int w = 0; w < sh.split; ++w) v += red[side0 * sh.split + w][in];
-        put(side0, in, v);
+        for (int w = 0; w < sh.split; ++w) v += red[k / 256 * sh.split + w][k % 256];
+        put(k / 256, k % 256, v);
       }
     } else {
 #pragma unroll
-      for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int t = 0; t < TB; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) put(side, (b * TB + t) * 256 + (4 * i + s.quad) * 16 + s.l16, acc[b][t][i]);
+      for (int i = 0; i < 4; ++i) put(side, (4 * i + s.quad) * 16 + s.l16, acc[i]);
     }
   }
 }
 
-template <Kind K, int G, int TB, int RB, int U>
+template <Kind K, int G, int U>
 gsi_status launch_as(const MArgs &a, hipStream_t st) {
-  using S = Stream<K, G, TB, RB, U>;
+  using S = Stream<K, G, U>;
+  static_assert(16 * S::XP * (S::C * U * S::xes + 16) <= kStreamLds, "one batch of columns fits");
   const int experts = a.n < a.R ? a.n : a.R;
-  const int64_t chunks = (a.R + 16 * TB - 1) / (16 * TB) + (a.offsets ? experts : 0);
-  static_assert(16 * TB * S::XP * (S::C * U * S::xes + 16) <= kStreamLds, "one batch of columns fits");
+  const int64_t chunks = (a.R + 15) / 16 + (a.offsets ? experts : 0);
   StreamShape sh{};
   // x of a chunk in LDS: all of it, or as many whole batches of columns as fit
-  const int tokens = a.R < 16 * TB ? a.R : 16 * TB;
+  const int tokens = a.R < 16 ? a.R : 16;
   const int unit = S::C * U, padded = (a.d + S::C - 1) / S::C * S::C;
   const int room = (kStreamLds / (tokens * S::XP) - 16) / S::xes / unit * unit;
   sh.columns = padded < room ? padded : room;
   sh.column_parts = (a.d + sh.columns - 1) / sh.columns;
   // The split with the fewest batches in a row for a wavefront, where 512
   // workgroups run at once and joining a block costs about one batch.
-  const int blocks = (a.d_out + 16 * RB - 1) / (16 * RB), want = (512 + experts - 1) / experts;
+  const int blocks = (a.d_out + 15) / 16, want = (512 + experts - 1) / experts;
   const int batches = (sh.columns + unit - 1) / unit;
   int64_t best = INT64_MAX;
   for (int split = 1; split <= kStreamWaves && (split == 1 || split <= batches); split *= 2) {
@@ -528,33 +471,25 @@ gsi_status launch_as(const MArgs &a, hipStream_t st) {
   }
   if (chunks * sh.strips > INT32_MAX) return GSI_E_SHAPE;
   const size_t lds = (size_t)tokens * S::XP * (sh.columns * S::xes + 16);
-  stream_kernel<K, G, TB, RB, U><<<(unsigned)(chunks * sh.strips), kStreamWaves * 64, lds, st>>>(a, sh);
+  stream_kernel<K, G, U><<<(unsigned)(chunks * sh.strips), kStreamWaves * 64, lds, st>>>(a, sh);
   return hipGetLastError() == hipSuccess ? GSI_OK : GSI_E_HIP;
 }
 
-template <Kind K, int G>
-gsi_status launch_kind(const MArgs &a, hipStream_t st) {
-  const int per = a.R / (a.n < a.R ? a.n : a.R);  // rows per expert, on average
-  constexpr int U = K == kQ4F32 ? 1 : 2;  // steps of a batch: three parts of x leave room for fewer in LDS
-  if (per > 32) return launch_as<K, G, 4, 2, U>(a, st);
-  if (per > 16) return launch_as<K, G, 2, 2, U>(a, st);
-  return launch_as<K, G, 1, 1, 2 * U>(a, st);
-}
-
 template <Kind K>
-gsi_status launch_group(const MArgs &a, int group, hipStream_t st) {
-  return group == 128 ? launch_kind<K, 128>(a, st)
-                      : (group == 64 ? launch_kind<K, 64>(a, st) : launch_kind<K, 32>(a, st));
+gsi_status launch_codes(const MArgs &a, int group, hipStream_t st) {
+  constexpr int U = K == kQ4F32 ? 2 : 4;  // three parts of x leave room for fewer columns in LDS
+  return group == 128 ? launch_as<K, 128, U>(a, st)
+                      : (group == 64 ? launch_as<K, 64, U>(a, st) : launch_as<K, 32, U>(a, st));
 }
 
 }  // namespace
 
 gsi_status launch_stream(const MArgs &a, Kind kind, int group, hipStream_t st) {
   switch (kind) {
-    case kQ4Bf16: return launch_group<kQ4Bf16>(a, group, st);
-    case kQ4F32: return launch_group<kQ4F32>(a, group, st);
-    case kBf16: return launch_kind<kBf16, 128>(a, st);
-    default: return launch_kind<kF32, 128>(a, st);
+    case kQ4Bf16: return launch_codes<kQ4Bf16>(a, group, st);
+    case kQ4F32: return launch_codes<kQ4F32>(a, group, st);
+    case kBf16: return launch_as<kBf16, 128, 4>(a, st);
+    default: return launch_as<kF32, 128, 4>(a, st);
   }
 }
 

@@ -533,6 +533,125 @@ __global__ void __launch_bounds__(512) q4_wide_kernel(MArgs a) {
     q4_tile<G, 1>(a, tl, {x0, w0}, {x1, w1}, {x2, w2}, {x3, w3});
 }
 
+// Small tiles: 64 tokens x 64 weight rows on four wavefronts, 2 x 2 of them,
+// each 32 x 32, for fp32 (whose products are slow enough to be bound by them
+// at any tile) and for bf16 with too few large tiles for the chip.  Several
+// workgroups share a CU.  A stage is 64 bytes of each row; the 16 bytes that a
+// lane reads of a row are one operand of 8 columns in bf16 and four of one
+// column in fp32, lanes 32 to 63 taking the other columns.
+constexpr int kSmallB = 64;
+constexpr int kSmallStage = 2 * kSmallB * 64;
+
+template <bool F32>
+__global__ void __launch_bounds__(256) small_kernel(MArgs a) {
+  constexpr int es = F32 ? 4 : 2, C = 64 / es;  // columns of a stage
+  __shared__ __attribute__((aligned(1024))) uint8_t lds0[kSmallStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds1[kSmallStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds2[kSmallStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds3[kSmallStage];
+  const Tiles n = count_tiles<kSmallB>(a);
+  const Tile tl =
+      find_tile<kSmallB>(a, n, (a.d_out + kSmallB - 1) / kSmallB, blockIdx.x % kXcds, blockIdx.x / kXcds);
+  if (tl.count <= 0) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1, l32 = lane & 31, half = lane >> 5;
+  const int i0 = tl.col * kSmallB;
+
+  // a KiB of x and a KiB of W of each stage
+  const int sub = lane >> 2, piece = ((lane & 3) ^ swizzle<32>(sub)) * 16, m0 = wave * 16 + sub;
+  const uint8_t *xp, *wp;
+  {
+    const int r = tl.row + min(m0, tl.count - 1);
+    const int src = a.rows ? a.rows[r] : r;
+    xp = a.x + (int64_t)(src < 0 || src >= a.T ? 0 : src) * a.ldx * es + piece;
+    wp = a.W + tl.e * a.w_stride + (int64_t)min(i0 + m0, a.d_out - 1) * a.d * es + piece;
+  }
+  int left = a.d * es - piece;  // bytes from this lane's next piece to the row's end
+  const uint64_t zeros = reinterpret_cast<uint64_t>(&kZeros);
+  const auto fetch = [&](uint8_t *st) {
+    const uint64_t in = (int64_t)(-left) >> 63;
+    left -= 64;
+    to_lds(reinterpret_cast<const void *>((reinterpret_cast<uint64_t>(xp) & in) | (zeros & ~in)), st + wave * 1024);
+    to_lds(reinterpret_cast<const void *>((reinterpret_cast<uint64_t>(wp) & in) | (zeros & ~in)),
+           st + kSmallB * 64 + wave * 1024);
+    xp += 64;
+    wp += 64;
+  };
+
+  f32x16_t acc = {};
+  int xat[2], wat[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    xat[s] = wm * 2048 + tile_at<32>(l32, 2 * s + half);
+    wat[s] = kSmallB * 64 + wn * 2048 + tile_at<32>(l32, 2 * s + half);
+  }
+  u32x4_t wf[2], xf[2];
+  const auto read = [&](const uint8_t *st, int s) {
+    wf[s] = *reinterpret_cast<const u32x4_t *>(st + wat[s]);
+    xf[s] = *reinterpret_cast<const u32x4_t *>(st + xat[s]);
+  };
+  const auto multiply = [&](int s) {
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (F32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(wf[s][i]), __uint_as_float(xf[s][i]), acc, 0, 0, 0);
+    } else {
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(wf[s]), as_bf16x8(xf[s]), acc, 0, 0, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const auto step = [&](const uint8_t *cur, const uint8_t *next, uint8_t *fill) {  // as in wide_tile
+    read(cur, 1);
+    multiply(0);
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    fetch(fill);
+    read(next, 0);
+    multiply(1);
+    landed<2>();
+  };
+  fetch(lds0);
+  fetch(lds1);
+  fetch(lds2);
+  landed<2>();
+  read(lds0, 0);
+  if (wm * 32 < tl.count) {
+    for (int k = 0; k < a.d; k += 4 * C) {
+      step(lds0, lds1, lds3);
+      step(lds1, lds2, lds0);
+      step(lds2, lds3, lds1);
+      step(lds3, lds0, lds2);
+    }
+  } else {  // no token of this half: it brings its share of the stages
+    for (int k = 0; k < a.d; k += 4 * C) {
+      fetch(lds3), landed<2>();
+      fetch(lds0), landed<2>();
+      fetch(lds1), landed<2>();
+      fetch(lds2), landed<2>();
+    }
+  }
+  landed<0>();
+
+  const int m = wm * 32 + l32;
+  if (m >= tl.count) return;
+  const int r = tl.row + m, src = a.rows ? a.rows[r] : r;
+  const bool has = src >= 0 && src < a.T;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int o = i0 + wn * 32 + 8 * q + 4 * half;
+    if (o >= a.d_out) continue;
+    f32x4_t v = {acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+    if (!has) v = f32x4_t{0, 0, 0, 0};
+    uint8_t *const yp = a.y + (r * a.ldy + o) * es;
+    if constexpr (F32) {
+      *reinterpret_cast<f32x4_t *>(yp) = v;
+    } else {
+      typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
+      *reinterpret_cast<bf16x4_t *>(yp) = bf16x4_t{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+    }
+  }
+}
+
 }  // namespace
 
 gsi_status launch_wide(const MArgs &a, hipStream_t st) {
@@ -553,6 +672,17 @@ gsi_status launch_wide_q4(const MArgs &a, int group, hipStream_t st) {
     q4_wide_kernel<64><<<(unsigned)grid, 512, 0, st>>>(a);
   else
     q4_wide_kernel<32><<<(unsigned)grid, 512, 0, st>>>(a);
+  return hipGetLastError() == hipSuccess ? GSI_OK : GSI_E_HIP;
+}
+
+gsi_status launch_small(const MArgs &a, Kind kind, hipStream_t st) {
+  const int64_t slots = a.R / kSmallB + (a.n < a.R ? a.n : a.R);
+  const int64_t grid = (slots * ((a.d_out + kSmallB - 1) / kSmallB) + 2 * kXcds) / kXcds * kXcds;
+  if (grid > INT32_MAX) return GSI_E_SHAPE;
+  if (kind == kF32)
+    small_kernel<true><<<(unsigned)grid, 256, 0, st>>>(a);
+  else
+    small_kernel<false><<<(unsigned)grid, 256, 0, st>>>(a);
   return hipGetLastError() == hipSuccess ? GSI_OK : GSI_E_HIP;
 }
 
