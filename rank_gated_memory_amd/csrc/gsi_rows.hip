@@ -2,6 +2,8 @@
 // undoes it (gsi_group_rows, gsi_group_combine).
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "../../include/gsi.h"
 
 namespace gsi {
@@ -20,24 +22,53 @@ namespace {
 constexpr int kRowsThreads = 1024;
 constexpr int kRowsWaves = kRowsThreads / 64;
 
+// Bound by the reads of all numbers by every workgroup, out of the L2s, twice:
+// a lane reads four choices at once and has four such reads under way (131072
+// choices over 256 experts: 39 us one choice at a time).
+constexpr int kRowsAhead = 4;
+
 template <typename I>
 __global__ void __launch_bounds__(kRowsThreads)
 group_rows_kernel(const I *ids, int n_flat, int top, int n, int32_t *offsets, int32_t *rows, int32_t *pos) {
   __shared__ int less_sh[kRowsWaves], mine_sh[kRowsWaves];
   const int e = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int span = ((n_flat + kRowsWaves - 1) / kRowsWaves + 63) / 64 * 64;
+  const int span = ((n_flat + kRowsWaves - 1) / kRowsWaves + 255) / 256 * 256;
   const int lo = min((int64_t)n_flat, (int64_t)wave * span), hi = min((int64_t)n_flat, (int64_t)lo + span);
-  // number of a choice: its expert, or n if it is dropped
-  const auto number = [&](int f) {
-    const I v = ids[f];
-    return v >= 0 && v < (I)n ? (int)v : n;
+  struct Four {
+    I v[4];
   };
+  // calls use(f, v) with the choices v[0..3] = ids[f..f + 3] of the span, the
+  // lanes in order; behind the span a number is -1, which no expert has
+  const auto each = [&](const auto &use) {
+    constexpr int kStep = 256 * kRowsAhead;
+    int f0 = lo;
+    for (; f0 + kStep <= hi; f0 += kStep) {
+      Four v[kRowsAhead];
+#pragma unroll
+      for (int j = 0; j < kRowsAhead; ++j) __builtin_memcpy(&v[j], ids + f0 + 256 * j + 4 * lane, sizeof(Four));
+#pragma unroll
+      for (int j = 0; j < kRowsAhead; ++j) use(f0 + 256 * j + 4 * lane, v[j]);
+    }
+    for (; f0 < hi; f0 += 256) {
+      Four v;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int f = f0 + 4 * lane + c;
+        v.v[c] = ids[f < hi ? f : lo];
+        if (f >= hi) v.v[c] = -1;
+      }
+      use(f0 + 4 * lane, v);
+    }
+  };
+  typedef std::make_unsigned_t<I> U;  // a dropped number is at least n as such
   int less = 0, mine = 0;
-  for (int f = lo + lane; f < hi; f += 64) {
-    const int v = number(f);
-    less += v < e;
-    mine += v == e;
-  }
+  each([&](int, const Four &v) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      less += (U)v.v[c] < (U)e;
+      mine += v.v[c] == (I)e;
+    }
+  });
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
     less += __shfl_xor(less, o, 64);
@@ -48,32 +79,43 @@ group_rows_kernel(const I *ids, int n_flat, int top, int n, int32_t *offsets, in
     mine_sh[wave] = mine;
   }
   __syncthreads();
-  int first = 0, at = 0, total = 0;
+  int first = 0, before = 0;
   for (int w = 0; w < kRowsWaves; ++w) {
     first += less_sh[w];
-    at += w < wave ? mine_sh[w] : 0;
-    total += mine_sh[w];
+    before += w < wave ? mine_sh[w] : 0;
   }
   if (threadIdx.x == 0) offsets[e] = first;  // e == n: the kept choices
-  at += first;
   if (e == n) {
     for (int f = first + threadIdx.x; f < n_flat; f += kRowsThreads) rows[f] = -1;
-    for (int f = lo + lane; f < hi; f += 64)
-      if (number(f) == n) pos[f] = -1;
+    each([&](int f, const Four &v) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (f + c < hi && (U)v.v[c] >= (U)n) pos[f + c] = -1;
+    });
     return;
   }
-  if (total == 0) return;
-  for (int f0 = lo; f0 < hi; f0 += 64) {
-    const int f = f0 + lane;
-    const bool is = f < hi && number(f) == e;
-    const uint64_t m = __ballot(is);
-    if (is) {
-      const int r = at + __popcll(m & ((1ull << lane) - 1));
-      rows[r] = f / top;
-      pos[f] = r;
+  if (mine == 0) return;
+  int at = first + before;
+  each([&](int f, const Four &v) {
+    bool is[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) is[c] = v.v[c] == (I)e;
+    if (__ballot(is[0] || is[1] || is[2] || is[3]) == 0) return;
+    // choices of earlier lanes, then this lane's own in order
+    int r = at;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint64_t m = __ballot(is[c]);
+      r += __popcll(m & ((1ull << lane) - 1));
+      at += __popcll(m);
     }
-    at += __popcll(m);
-  }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (is[c]) {
+        rows[r] = (f + c) / top;
+        pos[f + c] = r++;
+      }
+  });
 }
 
 // gsi_group_combine: one pass over the rows, fp32 sums in the order of j.
@@ -107,24 +149,36 @@ struct Vec<__bf16> {
   }
 };
 
+// Bound by HBM (8191 tokens of four rows of 4096 bf16 and a residual: 397 MB).
+// A token's positions and weights are the same for its whole workgroup; four
+// rows are under way at a time.
 template <typename E>
 __global__ void __launch_bounds__(256)
 combine_kernel(const E *y, int64_t ldy, int R, const int32_t *pos, const float *weights, const E *base, int64_t ldb,
-               E *out, int64_t ldo, int top, int d) {
-  constexpr int V = Vec<E>::n;
-  const int per = (d / V + 255) / 256;  // workgroups per token
-  const int t = blockIdx.x / per;
-  const int c = ((blockIdx.x % per) * 256 + threadIdx.x) * V;
+               E *out, int64_t ldo, int top, int d, int per) {
+  constexpr int V = Vec<E>::n, kAhead = 4;
+  const int t = blockIdx.x / per;  // `per` workgroups of a token
+  const int c = ((blockIdx.x - t * per) * 256 + threadIdx.x) * V;
   if (c >= d) return;
-  float acc[V] = {}, v[V];
+  float acc[V] = {};
   if (base) Vec<E>::load(base + t * ldb + c, acc);
-  for (int j = 0; j < top; ++j) {
-    const int p = pos[(int64_t)t * top + j];
-    if (p < 0 || p >= R) continue;
-    const float w = weights ? weights[(int64_t)t * top + j] : 1.f;
-    Vec<E>::load(y + p * ldy + c, v);
+  for (int j0 = 0; j0 < top; j0 += kAhead) {
+    float w[kAhead], v[kAhead][V];
+    bool has[kAhead];
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] += w * v[i];
+    for (int j = 0; j < kAhead; ++j) {
+      const int64_t at = (int64_t)t * top + min(j0 + j, top - 1);
+      const int p = pos[at];
+      has[j] = j0 + j < top && p >= 0 && p < R;
+      w[j] = weights ? weights[at] : 1.f;
+      if (has[j]) Vec<E>::load(y + p * ldy + c, v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (!has[j]) continue;
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += w[j] * v[j][i];
+    }
   }
   Vec<E>::store(out + t * ldo + c, acc);
 }
@@ -169,17 +223,18 @@ gsi_status gsi_group_combine(const void *y, int64_t ldy, int32_t R, const int32_
   if (!aligned(y, 16) || !aligned(out, 16) || !aligned(base, 16) || !aligned(pos, 4) || !aligned(weights, 4) ||
       ldo % vec || (R > 0 && ldy % vec) || (base && ldb % vec))
     return GSI_E_ALIGN;
-  const int64_t grid = (int64_t)T * ((d / vec + 255) / 256);
+  const int per = (d / vec + 255) / 256;
+  const int64_t grid = (int64_t)T * per;
   if (grid > INT32_MAX) return GSI_E_SHAPE;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   if (dtype == GSI_FP32)
     combine_kernel<float><<<(unsigned)grid, 256, 0, st>>>(static_cast<const float *>(y), ldy, R, pos, weights,
                                                           static_cast<const float *>(base), ldb,
-                                                          static_cast<float *>(out), ldo, top, d);
+                                                          static_cast<float *>(out), ldo, top, d, per);
   else
     combine_kernel<__bf16><<<(unsigned)grid, 256, 0, st>>>(static_cast<const __bf16 *>(y), ldy, R, pos, weights,
                                                            static_cast<const __bf16 *>(base), ldb,
-                                                           static_cast<__bf16 *>(out), ldo, top, d);
+                                                           static_cast<__bf16 *>(out), ldo, top, d, per);
   return hipGetLastError() == hipSuccess ? GSI_OK : GSI_E_HIP;
 }
 
