@@ -23,8 +23,7 @@ constexpr int kRowsThreads = 1024;
 constexpr int kRowsWaves = kRowsThreads / 64;
 
 // Bound by the reads of all numbers by every workgroup, out of the L2s, twice:
-// a lane reads four choices at once and has four such reads under way (131072
-// choices over 256 experts: 39 us one choice at a time).
+// a lane reads four choices at once and has four such reads under way.
 constexpr int kRowsAhead = 4;
 
 template <typename I>
@@ -118,6 +117,136 @@ group_rows_kernel(const I *ids, int n_flat, int top, int n, int32_t *offsets, in
   });
 }
 
+// Many choices: three launches whose work grows with the choices alone.  The
+// flat order is cut into blocks of kPlaceBlock choices (the last takes what is
+// left); the block's counts per expert, and then its first rows per expert,
+// lie in the block's own part of pos until the block overwrites them with its
+// result, so no workspace is needed (a block has at least as many choices as
+// there are experts).
+// From this many choices on (16384 choices over 32 to 256 experts: 7.7 us in
+// one launch, 11 in three; 32768 over 8: 10.6 and 10.5; 131072 over 256: 38
+// and 15).
+constexpr int kPlaceFrom = 32768;
+constexpr int kPlaceBlock = 2048;
+static_assert(kPlaceBlock >= 1024, "a block's part of pos holds a count for every expert");
+
+__device__ __forceinline__ int place_end(int b, int n_flat) {
+  return b == (int)gridDim.x - 1 ? n_flat : (b + 1) * kPlaceBlock;
+}
+
+template <typename I>
+__global__ void __launch_bounds__(kRowsThreads) count_kernel(const I *ids, int n_flat, int n, int32_t *pos) {
+  __shared__ int count[1024];
+  for (int e = threadIdx.x; e < n; e += kRowsThreads) count[e] = 0;
+  __syncthreads();
+  const int lo = blockIdx.x * kPlaceBlock, hi = place_end(blockIdx.x, n_flat);
+  for (int f = lo + threadIdx.x; f < hi; f += kRowsThreads) {
+    const I v = ids[f];
+    if (v >= 0 && v < (I)n) atomicAdd(&count[v], 1);  // a sum of integers: the order does not matter
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < n; e += kRowsThreads) pos[lo + e] = count[e];
+}
+
+// Every block's counts become the choices of the same expert in earlier
+// blocks, the totals the experts' first rows.
+__global__ void __launch_bounds__(kRowsThreads) scan_kernel(int blocks, int n, int32_t *offsets, int32_t *pos) {
+  __shared__ int total[1024];
+  const int e = threadIdx.x;
+  int run = 0;
+  if (e < n) {
+    constexpr int kAhead = 16;
+    for (int b0 = 0; b0 < blocks; b0 += kAhead) {
+      int c[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) c[j] = b0 + j < blocks ? pos[(int64_t)(b0 + j) * kPlaceBlock + e] : 0;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (b0 + j < blocks) pos[(int64_t)(b0 + j) * kPlaceBlock + e] = run;
+        run += c[j];
+      }
+    }
+  }
+  total[e] = e < n ? run : 0;
+  for (int o = 1; o < 1024; o <<= 1) {  // inclusive sums
+    __syncthreads();
+    const int before = e >= o ? total[e - o] : 0;
+    __syncthreads();
+    total[e] += before;
+  }
+  if (e < n) {
+    offsets[e] = total[e] - run;
+    if (e == n - 1) offsets[n] = total[e];
+  }
+}
+
+template <typename I>
+__global__ void __launch_bounds__(kRowsThreads)
+place_kernel(const I *ids, int n_flat, int top, int n, const int32_t *offsets, int32_t *rows, int32_t *pos) {
+  extern __shared__ int next[];  // [wavefront][expert]: the next row
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lo = blockIdx.x * kPlaceBlock, hi = place_end(blockIdx.x, n_flat);
+  const int span = ((hi - lo + kRowsWaves - 1) / kRowsWaves + 63) / 64 * 64;
+  const int f0 = min(lo + wave * span, hi), f1 = min(f0 + span, hi);
+  for (int k = threadIdx.x; k < kRowsWaves * n; k += kRowsThreads) next[k] = 0;
+  __syncthreads();
+  int *const mine = next + wave * n;
+  for (int f = f0 + lane; f < f1; f += 64) {
+    const I v = ids[f];
+    if (v >= 0 && v < (I)n) atomicAdd(&mine[v], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < n; e += kRowsThreads) {
+    int run = offsets[e] + pos[lo + e];
+    for (int w = 0; w < kRowsWaves; ++w) {
+      const int c = next[w * n + e];
+      next[w * n + e] = run;
+      run += c;
+    }
+  }
+  __syncthreads();
+  for (int f = lo + threadIdx.x; f < hi; f += kRowsThreads)
+    if (f >= offsets[n]) rows[f] = -1;
+  for (int f = f0; f < f1; f += 64) {
+    const bool in = f + lane < f1;
+    const I v = in ? ids[f + lane] : (I)-1;
+    const bool kept = v >= 0 && v < (I)n;
+    const int e = kept ? (int)v : 0;
+    // the lanes with this lane's expert, a bit of its number at a time
+    uint64_t same = __ballot(kept);
+    for (int bit = 1; bit < n; bit <<= 1) {
+      const uint64_t m = __ballot(e & bit);
+      same &= e & bit ? m : ~m;
+    }
+    const int rank = __popcll(same & ((1ull << lane) - 1));
+    const int r = kept ? mine[e] + rank : -1;
+    // every lane has read its row before the first of each expert moves it on
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (kept) {
+      if (rank == 0) mine[e] = r + __popcll(same);
+      rows[r] = (f + lane) / top;
+    }
+    if (in) pos[f + lane] = r;
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+template <typename I>
+void launch_rows(const I *ids, int flat, int top, int n, int32_t *offsets, int32_t *rows, int32_t *pos,
+                 hipStream_t st) {
+  if (flat < kPlaceFrom) {
+    group_rows_kernel<I><<<n + 1, kRowsThreads, 0, st>>>(ids, flat, top, n, offsets, rows, pos);
+    return;
+  }
+  const int blocks = flat / kPlaceBlock;
+  count_kernel<I><<<blocks, kRowsThreads, 0, st>>>(ids, flat, n, pos);
+  scan_kernel<<<1, kRowsThreads, 0, st>>>(blocks, n, offsets, pos);
+  place_kernel<I><<<blocks, kRowsThreads, (size_t)kRowsWaves * n * sizeof(int), st>>>(ids, flat, top, n, offsets, rows,
+                                                                                  pos);
+}
+
 // gsi_group_combine: one pass over the rows, fp32 sums in the order of j.
 template <typename E>
 struct Vec;
@@ -201,11 +330,9 @@ gsi_status gsi_group_rows(const void *ids, int32_t ids_bytes, int32_t T, int32_t
   const int flat = T * top;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   if (ids_bytes == 4)
-    group_rows_kernel<int32_t><<<n + 1, kRowsThreads, 0, st>>>(static_cast<const int32_t *>(ids), flat, top, n,
-                                                               offsets, rows, pos);
+    launch_rows(static_cast<const int32_t *>(ids), flat, top, n, offsets, rows, pos, st);
   else
-    group_rows_kernel<int64_t><<<n + 1, kRowsThreads, 0, st>>>(static_cast<const int64_t *>(ids), flat, top, n,
-                                                               offsets, rows, pos);
+    launch_rows(static_cast<const int64_t *>(ids), flat, top, n, offsets, rows, pos, st);
   return hipGetLastError() == hipSuccess ? GSI_OK : GSI_E_HIP;
 }
 

@@ -363,15 +363,23 @@ def gsi_calibrate(A: torch.Tensor, V0: torch.Tensor, iters: int, V=None, ws=None
 
 # ---- plain linear maps: weights in 4 bits, weights of many experts ----
 
+# The raw handle of a device's current stream without building a Stream object
+# (a microsecond and a half of a call's five), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(where: str, fn, device: torch.device, stream, *args):
     """fn(*args, stream) on `device`: its own current stream unless one is given,
     whatever device is current."""
     if device.type != "cuda":
         raise ValueError(f"{where}: tensors must be on the GPU")
+    index, current = device.index, torch.cuda.current_device()
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    raw = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
-    if device.index is None or device.index == torch.cuda.current_device():
+        raw = _raw_stream(current if index is None else index)
+    else:
+        raw = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+    if index is None or index == current:
         status = fn(*args, raw)
     else:
         with torch.cuda.device(device):
@@ -382,17 +390,19 @@ def _call(where: str, fn, device: torch.device, stream, *args):
 
 def _rows2d(t: torch.Tensor, name: str, dtype, device, cols: int, n: int | None = None) -> int:
     """The row stride of a [n][cols] tensor whose rows are contiguous."""
-    if t.dim() != 2 or t.shape[1] != cols or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name} must be [{'n' if n is None else n}][{cols}], is {tuple(t.shape)}")
-    if t.dtype != dtype or t.device != device:
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols or (n is not None and shape[0] != n):
+        raise ValueError(f"{name} must be [{'n' if n is None else n}][{cols}], is {tuple(shape)}")
+    if t.dtype is not dtype or t.device != device:
         raise ValueError(f"{name} must be {dtype} on {device}, is {t.dtype} on {t.device}")
-    if t.stride(1) != 1 and cols > 1:
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), cols)
+    return s0 if shape[0] > 1 or s0 > cols else cols
 
 
 def _ints(t: torch.Tensor, name: str, shape, device):
-    if t.dtype != torch.int32 or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.device != device or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous int32 {tuple(shape)} on {device}, "
                          f"is {t.dtype} {tuple(t.shape)} on {t.device}")
 
@@ -433,12 +443,14 @@ def gsi_q4_linear(w: Q4, x: torch.Tensor, y: torch.Tensor | None = None, stream=
     and gives y [1][d_out]."""
     if x.dim() == 1:
         x = x[None]
-    ldx = _rows2d(x, "x", w.dtype, w.device, w.d)
+    dtype, dev, d_out = w.dtype, w.device, w.d_out
+    ldx = _rows2d(x, "x", dtype, dev, w.d)
     T = x.shape[0]
     if y is None:
-        y = torch.empty((T, w.d_out), dtype=w.dtype, device=w.device)
-    ldy = _rows2d(y, "y", w.dtype, w.device, w.d_out, T)
-    _call("gsi_q4_linear", lib().gsi_q4_linear, w.device, stream, w.struct, x.data_ptr(), ldx, y.data_ptr(), ldy, T)
+        y, ldy = torch.empty((T, d_out), dtype=dtype, device=dev), d_out
+    else:
+        ldy = _rows2d(y, "y", dtype, dev, d_out, T)
+    _call("gsi_q4_linear", lib().gsi_q4_linear, dev, stream, w.struct, x.data_ptr(), ldx, y.data_ptr(), ldy, T)
     return y
 
 
@@ -465,8 +477,9 @@ def gsi_grouped_linear(w, x: torch.Tensor, offsets: torch.Tensor, rows: torch.Te
     if rows is not None:
         _ints(rows, "rows", (R,), dev)
     if y is None:
-        y = torch.empty((R, d_out), dtype=dtype, device=dev)
-    ldy = _rows2d(y, "y", dtype, dev, d_out, R)
+        y, ldy = torch.empty((R, d_out), dtype=dtype, device=dev), d_out
+    else:
+        ldy = _rows2d(y, "y", dtype, dev, d_out, R)
     _call("gsi_grouped_linear", lib().gsi_grouped_linear, dev, stream, struct, x.data_ptr(), ldx, x.shape[0],
           offsets.data_ptr(), _ptr(rows), y.data_ptr(), ldy, R)
     return y
@@ -483,8 +496,8 @@ def gsi_group_rows(ids: torch.Tensor, n: int, offsets: torch.Tensor | None = Non
     dev = ids.device
     if offsets is None and rows is None and pos is None:
         at = T * top
-        both = torch.empty(2 * at + n + 1, dtype=torch.int32, device=dev)
-        rows, pos, offsets = both[:at], both[at:2 * at].view(T, top), both[2 * at:]
+        rows, pos, offsets = torch.empty(2 * at + n + 1, dtype=torch.int32, device=dev).split((at, at, n + 1))
+        pos = pos.view(T, top)
     else:
         offsets = torch.empty(n + 1, dtype=torch.int32, device=dev) if offsets is None else offsets
         rows = torch.empty(T * top, dtype=torch.int32, device=dev) if rows is None else rows
@@ -513,8 +526,9 @@ def gsi_group_combine(y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor 
         raise ValueError("weights must be contiguous fp32 like pos")
     ldb = 0 if base is None else _rows2d(base, "base", dtype, dev, d, T)
     if out is None:
-        out = torch.empty((T, d), dtype=dtype, device=dev)
-    ldo = _rows2d(out, "out", dtype, dev, d, T)
+        out, ldo = torch.empty((T, d), dtype=dtype, device=dev), d
+    else:
+        ldo = _rows2d(out, "out", dtype, dev, d, T)
     _call("gsi_group_combine", lib().gsi_group_combine, dev, stream, y.data_ptr(), ldy, y.shape[0], pos.data_ptr(),
           _ptr(weights), _ptr(base), ldb, out.data_ptr(), ldo, T, top, d, _dtype_code(y))
     return out

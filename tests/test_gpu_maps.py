@@ -309,7 +309,8 @@ def test_grouped_addresses_past_32_bits(kind, R):
 
 @pytest.mark.parametrize("dtype", [torch.int32, torch.int64], ids=["int32", "int64"])
 @pytest.mark.parametrize("T,top,n", [(1, 1, 1), (1, 8, 64), (5, 2, 3), (64, 1, 7), (333, 3, 65), (1024, 6, 256),
-                                     (700, 4, 1024), (20000, 2, 16)])
+                                     (700, 4, 1024), (20000, 2, 16),
+                                     (4095, 8, 256), (4096, 8, 3), (33000, 1, 1), (9001, 5, 1024), (16389, 8, 256)])
 def test_group_rows(T, top, n, dtype):
     g = gen(T + n)
     ids = torch.randint(-1 if T % 2 else 0, n + T % 2, (T, top), generator=g, device=DEV).to(dtype)
