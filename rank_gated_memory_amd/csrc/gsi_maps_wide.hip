@@ -7,66 +7,89 @@ namespace {
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 // The tiles of a launch.  Each expert's rows are cut into full row tiles of
-// BM and one shorter rest; every full tile comes before any rest, so that the
-// last round of the workgroups is made of short ones.  The full tiles are
-// dealt to the 8 XCDs (workgroup b runs on XCD b % 8) in contiguous shares, so
-// that workgroups that share an L2 work on neighbouring tiles: groups of
-// kSlotGroup row tiles, in each all column tiles, in each the row tiles.  The
-// rests, of all heights, are dealt one by one.
+// BM and one shorter rest, of one of four heights.  The full tiles are dealt
+// to the 8 XCDs (workgroup b runs on XCD b % 8) in contiguous shares, so that
+// workgroups that share an L2 work on neighbouring tiles: groups of kSlotGroup
+// row tiles, in each all column tiles, in each the row tiles.  The rests are
+// dealt one by one.  An XCD's list holds its full tiles and then its rests, the
+// high ones first, so that workgroups that take them in order end together.
 constexpr int kXcds = 8;
 constexpr int kSlotGroup = 4;
+constexpr int kHeights = 4;
 
 struct Tile {
   int e, row, count, col;  // count 0: behind the last
 };
 
+// Row tiles of each kind: kind 0 is full, kind k a rest of at most
+// (kHeights + 1 - k) quarters of BM.
 struct Tiles {
-  int full, rest;  // row tiles
+  int of[kHeights + 1];
 };
 
 template <int BM>
+__device__ __forceinline__ int rest_kind(int rows) {  // 0 without a rest
+  const int rest = rows % BM;
+  return rest ? kHeights + 1 - (rest + BM / kHeights - 1) / (BM / kHeights) : 0;
+}
+
+template <int BM>
 __device__ __forceinline__ Tiles count_tiles(const MArgs &a) {
-  int full = 0, rest = 0;
+  Tiles n = {};
   for (int e0 = 0; e0 < a.n; e0 += 64) {
     int lo, hi;
     expert_rows(a, e0 + (threadIdx.x & 63), &lo, &hi);
-    full += (hi - lo) / BM;
-    rest += (hi - lo) % BM != 0;
+    n.of[0] += (hi - lo) / BM;
+    const int kind = rest_kind<BM>(hi - lo);
+#pragma unroll
+    for (int k = 1; k <= kHeights; ++k) n.of[k] += __popcll(__ballot(kind == k));
   }
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    full += __shfl_xor(full, o, 64);
-    rest += __shfl_xor(rest, o, 64);
-  }
-  return {__builtin_amdgcn_readfirstlane(full), __builtin_amdgcn_readfirstlane(rest)};
+  for (int o = 32; o > 0; o >>= 1) n.of[0] += __shfl_xor(n.of[0], o, 64);
+#pragma unroll
+  for (int k = 0; k <= kHeights; ++k) n.of[k] = __builtin_amdgcn_readfirstlane(n.of[k]);
+  return n;
+}
+
+// The tiles of XCD `xcd`: full ones, and all.
+__device__ __forceinline__ int64_t full_share(const Tiles &n, int col_tiles, int xcd, int64_t *first) {
+  const int64_t tiles = (int64_t)n.of[0] * col_tiles, share = (tiles + kXcds - 1) / kXcds;
+  *first = xcd * share;
+  return max((int64_t)0, min(share, tiles - *first));
+}
+
+__device__ __forceinline__ int64_t all_share(const Tiles &n, int col_tiles, int xcd) {
+  int64_t first, rests = 0;
+#pragma unroll
+  for (int k = 1; k <= kHeights; ++k) rests += n.of[k];
+  return full_share(n, col_tiles, xcd, &first) + (rests * col_tiles - xcd + kXcds - 1) / kXcds;
 }
 
 // Tile number `at` of XCD `xcd`.
 template <int BM>
 __device__ __forceinline__ Tile find_tile(const MArgs &a, const Tiles &n, int col_tiles, int xcd, int64_t at) {
   const int lane = threadIdx.x & 63;
-  const int64_t full_tiles = (int64_t)n.full * col_tiles, rest_tiles = (int64_t)n.rest * col_tiles;
-  const int64_t share = (full_tiles + kXcds - 1) / kXcds;
-  const int64_t first = xcd * share, mine = max((int64_t)0, min(share, full_tiles - first));
-  const bool is_full = at < mine;
-  int slot, col;
-  if (is_full) {
+  if (at >= all_share(n, col_tiles, xcd)) return {0, 0, 0, 0};
+  int64_t first;
+  const int64_t mine = full_share(n, col_tiles, xcd, &first);
+  int kind = 0, slot, col;
+  if (at < mine) {
     const int64_t t = first + at;
     const int g = (int)(t / (kSlotGroup * col_tiles)), in = (int)(t - (int64_t)g * kSlotGroup * col_tiles);
-    const int wide = min(kSlotGroup, n.full - g * kSlotGroup);
+    const int wide = min(kSlotGroup, n.of[0] - g * kSlotGroup);
     slot = g * kSlotGroup + in % wide;
     col = in / wide;
   } else {
     const int64_t t = (at - mine) * kXcds + xcd;
-    if (t >= rest_tiles) return {0, 0, 0, 0};
     slot = (int)(t / col_tiles);
     col = (int)(t - (int64_t)slot * col_tiles);
+    for (kind = 1; kind < kHeights && slot >= n.of[kind]; ++kind) slot -= n.of[kind];
   }
   int before = 0;
   for (int e0 = 0; e0 < a.n; e0 += 64) {
     int lo, hi;
     expert_rows(a, e0 + lane, &lo, &hi);
-    const int has = is_full ? (hi - lo) / BM : ((hi - lo) % BM != 0);
+    const int has = kind == 0 ? (hi - lo) / BM : rest_kind<BM>(hi - lo) == kind;
     int incl = has;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -78,7 +101,7 @@ __device__ __forceinline__ Tile find_tile(const MArgs &a, const Tiles &n, int co
       const int l = __ffsll((unsigned long long)over) - 1;
       const int k = slot - before - (__builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(has, l));
       const int row = __builtin_amdgcn_readlane(lo, l), rows = __builtin_amdgcn_readlane(hi, l) - row;
-      const int skip = is_full ? k * BM : rows / BM * BM;
+      const int skip = kind == 0 ? k * BM : rows / BM * BM;
       return {e0 + l, row + skip, min(BM, rows - skip), col};
     }
     before += __builtin_amdgcn_readlane(incl, 63);
@@ -275,8 +298,11 @@ __device__ __forceinline__ void wide_tile(const MArgs &a, const Tile &tl, WideSo
   }
 }
 
-// A workgroup for every CU, each walking its XCD's tiles; an expert's rest
-// takes the smallest of four heights that holds it.
+// A workgroup for every CU.  The workgroups of an XCD take its list in turn,
+// every second turn from the other end, which gives each about the same; XCDs
+// with odd numbers walk their turns backwards, so that low rests, which are
+// bound by the weights from HBM, run beside full tiles of other XCDs, which are
+// not.
 __global__ void __launch_bounds__(512) wide_kernel(MArgs a) {
   // stages as separate objects, so that the compiler sees that filling one
   // does not touch the others
@@ -287,9 +313,16 @@ __global__ void __launch_bounds__(512) wide_kernel(MArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col_tiles = (a.d_out + kWideBN - 1) / kWideBN;
   const Tiles n = count_tiles<kWideBM>(a);
-  const int xcd = blockIdx.x % kXcds, stride = gridDim.x / kXcds;
-  int64_t at = blockIdx.x / kXcds;
-  Tile tl = find_tile<kWideBM>(a, n, col_tiles, xcd, at);
+  const int xcd = blockIdx.x % kXcds, me = blockIdx.x / kXcds, all = gridDim.x / kXcds;
+  const int64_t tiles = all_share(n, col_tiles, xcd), turns = (tiles + all - 1) / all;
+  const auto tile_of = [&](int64_t k) -> Tile {  // of this workgroup's turn k
+    if (k >= turns) return {0, 0, 0, 0};
+    const int64_t r = xcd & 1 ? turns - 1 - k : k;
+    return find_tile<kWideBM>(a, n, col_tiles, xcd, r * all + (r & 1 ? all - 1 - me : me));
+  };
+  int64_t k = 0;
+  Tile tl = tile_of(0);
+  if (tl.count <= 0) tl = tile_of(k = 1);  // the last turn is not for all
   if (tl.count <= 0) return;
   WideSource f = wide_source(a, tl, wave, lane);
   wide_fetch(f, lds0, wave);
@@ -297,8 +330,7 @@ __global__ void __launch_bounds__(512) wide_kernel(MArgs a) {
   wide_fetch(f, lds2, wave);
   landed<kWideLoads>();
   for (;;) {
-    at += stride;
-    const Tile next = find_tile<kWideBM>(a, n, col_tiles, xcd, at);
+    const Tile next = tile_of(++k);
     const WideSource nf = wide_source(a, next, wave, lane);
     if (tl.count > 192)
       wide_tile<4>(a, tl, f, nf, lds0, lds1, lds2, lds3);
