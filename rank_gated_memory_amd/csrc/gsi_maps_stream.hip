@@ -26,6 +26,8 @@
 // accumulators all belong to one weight row and take one scale.  Row m of A
 // is token 4 (m % 4) + m / 4 of the chunk: up to four tokens then need only
 // the first accumulator of every lane.
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "gsi_maps.h"
@@ -135,7 +137,8 @@ template <Kind K>
 constexpr int kStepColumns = K == kQ4Bf16 || K == kQ4F32 ? 128 : K == kBf16 ? 32 : 16;
 
 constexpr int kStreamWaves = 8;
-constexpr int kStreamLds = 64 * 1024;  // x of a chunk; two workgroups of a CU hold theirs
+constexpr int kStreamLds = 64 * 1024;        // x of a chunk; two workgroups of a CU hold theirs
+constexpr int kStreamLdsAlone = 144 * 1024;  // of a workgroup that has the CU for itself
 
 // How a launch splits its work.
 struct StreamShape {
@@ -450,24 +453,35 @@ gsi_status launch_as(const MArgs &a, hipStream_t st) {
   static_assert(16 * S::XP * (S::C * U * S::xes + 16) <= kStreamLds, "one batch of columns fits");
   const int experts = a.n < a.R ? a.n : a.R;
   const int64_t chunks = (a.R + 15) / 16 + (a.offsets ? experts : 0);
-  StreamShape sh{};
-  // x of a chunk in LDS: all of it, or as many whole batches of columns as fit
+  // The cheapest shape, in half batches that a wavefront goes through in a row
+  // until the last chunk is done: joining a split block costs about one, and
+  // x that does not fit, one part after the other, two for each part.  Then a
+  // workgroup may also have the CU for itself, with fewer and longer parts (16
+  // tokens through a 4-bit 16384 -> 4096 map: 64 us in parts of 1536 columns,
+  // two workgroups on a CU, and 39 us in parts of 4096, one on a CU; 300 tokens
+  // over 32 experts 4096 -> 1024: 68 and 78 us).
+  const int64_t busy = a.offsets ? std::max<int64_t>(experts, a.R / 16) : chunks;  // chunks with rows, about
   const int tokens = a.R < 16 ? a.R : 16;
-  const int unit = S::C * U, padded = (a.d + S::C - 1) / S::C * S::C;
-  const int room = (kStreamLds / (tokens * S::XP) - 16) / S::xes / unit * unit;
-  sh.columns = padded < room ? padded : room;
-  sh.column_parts = (a.d + sh.columns - 1) / sh.columns;
-  // The split with the fewest batches in a row for a wavefront, where 512
-  // workgroups run at once and joining a block costs about one batch.
-  const int blocks = (a.d_out + 15) / 16, want = (512 + experts - 1) / experts;
-  const int batches = (sh.columns + unit - 1) / unit;
-  int64_t best = INT64_MAX;
-  for (int split = 1; split <= kStreamWaves && (split == 1 || split <= batches); split *= 2) {
-    const int sides = kStreamWaves / split, groups = (blocks + sides - 1) / sides;
-    const int strips = sh.column_parts > 1 || groups < want ? groups : want;
-    const int64_t rounds = sh.column_parts > 1 ? (groups + want - 1) / want : (groups + strips - 1) / strips;
-    const int64_t cost = rounds * ((batches + split - 1) / split + (split > 1 ? 1 : 0));
-    if (cost < best) best = cost, sh.split = split, sh.strips = strips;
+  const int unit = S::C * U, padded = (a.d + S::C - 1) / S::C * S::C, blocks = (a.d_out + 15) / 16;
+  StreamShape sh{};
+  double best = INFINITY;
+  for (int alone = 0; alone < 2; ++alone) {
+    const int room = ((alone ? kStreamLdsAlone : kStreamLds) / (tokens * S::XP) - 16) / S::xes / unit * unit;
+    const int columns = std::min(padded, room), parts = (a.d + columns - 1) / columns;
+    const int batches = (columns + unit - 1) / unit;
+    const int64_t at_once = alone ? 256 : 512, want = (at_once + busy - 1) / busy;
+    for (int split = 1; split <= kStreamWaves && (split == 1 || split <= batches); split *= 2) {
+      const int sides = kStreamWaves / split, groups = (blocks + sides - 1) / sides;
+      // x that fits is staged once for all of a workgroup's blocks
+      const int strips = parts > 1 ? groups : (int)std::min<int64_t>(groups, want);
+      const int64_t part = 2 * ((batches + split - 1) / split) + (parts > 1 ? 2 : 0);
+      const int64_t turn = (groups + strips - 1) / strips * (parts * part + (split > 1 ? 1 : 0));
+      // workgroups that share a CU overlap: their last round need not be full
+      const double load = (double)strips * busy / at_once;
+      const double cost = turn * (alone ? std::ceil(load) : std::max(1.0, load));
+      if (cost < best) best = cost, sh = {split, strips, columns, parts};
+    }
+    if (parts == 1) break;
   }
   if (chunks * sh.strips > INT32_MAX) return GSI_E_SHAPE;
   const size_t lds = (size_t)tokens * S::XP * (sh.columns * S::xes + 16);

@@ -82,7 +82,7 @@ def bits(t):
 @pytest.mark.parametrize("d,d_out,T", [
     (32, 8, 1), (64, 24, 2), (96, 16, 15), (160, 136, 16), (224, 72, 17), (1056, 1000, 1), (1056, 264, 33),
     (4096, 512, 1), (4096, 1024, 5), (2080, 520, 64), (480, 264, 65), (1024, 392, 130), (992, 640, 300),
-    (4096, 264, 257),
+    (4096, 264, 257), (8224, 136, 16), (16384, 72, 21),
 ])
 def test_q4_linear(d, d_out, T, dtype, group):
     g = gen(d + d_out + T + group)
@@ -198,6 +198,7 @@ def to_offsets(counts, first=0):
     (64, 24, [1]), (96, 8, [0, 1, 0]), (160, 40, [3, 0, 16, 17, 1]), (256, 136, [0, 0, 200, 0, 5]),
     (1056, 264, [1] * 9), (288, 72, [i % 4 for i in range(150)]), (512, 384, [130, 127, 0, 1, 129, 257]),
     (672, 520, [64, 65, 63, 0, 300]), (2048, 256, [33, 31, 500]), (128, 128, [1000, 1]),
+    (5152, 72, [16, 2, 0, 5]),
 ])
 def test_grouped_linear(d, d_out, counts, kind):
     g = gen(d + d_out + len(counts))
