@@ -39,9 +39,14 @@ gsi_status choose(const MArgs &a, const gsi_weights &w, hipStream_t st) {
     if (!f32 && blocks >= 6000 * ((tiles + 255) / 256)) return launch_wide_q4(a, w.group, st);
     return launch_stream(a, f32 ? kQ4F32 : kQ4Bf16, w.group, st);
   }
-  // Streaming up to 8 rows per expert (16 experts 2048 -> 2048: 9 rows each
-  // 27 us both ways, 14 rows 40 us streamed and 28 us in small tiles).
-  if (per <= 8) return launch_stream(a, f32 ? kF32 : kBf16, 0, st);
+  // Streaming for few rows per expert (16 experts 2048 -> 2048, 8 and 12 rows
+  // each: bf16 23 and 36 us, 26 both in small tiles; fp32 51 and 65 us, 72 and
+  // 73), and as long as its blocks of 16 x 16 do not go round the chip twice:
+  // one small tile per CU or less is all latency (bf16 8 experts 4096 -> 256, 40
+  // rows each, 448 blocks: 21 us, 31 in small tiles; 4 experts 4096 -> 1024, 24
+  // rows, 640 blocks: 19 and 30 us, 40 rows, 896 blocks: 37 and 30 us).
+  const int64_t blocks = (a.R / 16 + experts) * ((a.d_out + 15) / 16);
+  if (per <= (f32 ? 12 : 8) || blocks <= 800) return launch_stream(a, f32 ? kF32 : kBf16, 0, st);
   // Large tiles where there is at least one for every CU, or half as many full
   // ones (64 experts 2048 -> 4096, 32 rows each: 139 us, 178 in small tiles;
   // 16 experts 2048 -> 1024, 100 rows: 54 and 30 us; 8 experts 2048 -> 2048,

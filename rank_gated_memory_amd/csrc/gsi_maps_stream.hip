@@ -13,6 +13,14 @@
 //                   wavefront, were slower at every number of rows: 28 and 69
 //                   us instead of 22 and 23 for 24 and 40 tokens of a 4-bit
 //                   4096 x 4096 map.)
+//                   24 tokens' 192 rows over 128 experts in 4 bits, 4096 ->
+//                   1536: 266 MB in 41 to 46 us, 6.2 TB/s.  8 experts' bf16
+//                   maps 2048 -> 2816 for one token: 92 MB in 19 us.  A 4-bit
+//                   4096 x 4096 map for one token, 8.8 MB: 6 us, most of it
+//                   launch and latency; 5 tokens 4096 -> 50400, 113 MB: 32 us,
+//                   where reading the weights in this pattern alone takes 23.
+//                   With more tokens the staging of x shows: 13 fp32 tokens
+//                   5120 -> 13824, 47 MB: 32 us.
 //
 // 4-bit weights.  With w = s (q - z) a group's share of y is
 //   s (sum q x - z sum x) = s (sum (16 + q) x - (16 + z) sum x).
@@ -144,8 +152,7 @@ constexpr int kStreamLdsAlone = 144 * 1024;  // of a workgroup that has the CU f
 struct StreamShape {
   int split;         // wavefronts that share the columns of a block of weight rows
   int strips;        // workgroups per chunk
-  int columns;       // columns of x in LDS at a time, whole steps
-  int column_parts;  // of d
+  int room;          // bytes of LDS for x
 };
 
 template <Kind K, int G, int U>
@@ -346,6 +353,14 @@ struct Stream {
   }
 };
 
+// Columns of `tokens` rows of x that fit into `room` bytes: all `padded` ones of
+// a row, or whole batches.
+template <typename S, int U>
+__host__ __device__ constexpr int columns_in(int room, int tokens, int padded) {
+  const int fit = (room / (tokens * S::XP) - 16) / S::xes;
+  return fit >= padded ? padded : fit / (S::C * U) * (S::C * U);
+}
+
 template <Kind K, int G, int U>
 __global__ void __launch_bounds__(kStreamWaves * 64, 4) stream_kernel(MArgs a, StreamShape sh) {
   using S = Stream<K, G, U>;
@@ -361,11 +376,15 @@ __global__ void __launch_bounds__(kStreamWaves * 64, 4) stream_kernel(MArgs a, S
   const int blocks = (a.d_out + 15) / 16, groups = (blocks + sides - 1) / sides;
   // accumulators of a lane that hold tokens
   const int live = S::q4 ? (ch.count + 3) / 4 : 4;
-  const auto tk = s.token(lds, ch, sh.columns);
+  // columns of x in LDS at a time, whole steps, and the parts of d
+  const int padded = (a.d + S::C - 1) / S::C * S::C;
+  const int columns = __builtin_amdgcn_readfirstlane(columns_in<S, U>(sh.room, ch.count, padded));
+  const int parts = (a.d + columns - 1) / columns;
+  const auto tk = s.token(lds, ch, columns);
   // a part's columns: whole batches, dealt to the split in even shares; what
   // is left of the row goes to the last share, step by step
   const auto share_of = [&](int part, int *step0, int *first, int *end, int *rest, int *last) {
-    const int c0 = part * sh.columns, width = min(sh.columns, a.d - c0), batches = width / (S::C * U);
+    const int c0 = part * columns, width = min(columns, a.d - c0), batches = width / (S::C * U);
     *step0 = c0 / S::C;
     *first = *step0 + batches * share / sh.split * U;
     *end = *step0 + batches * (share + 1) / sh.split * U;
@@ -385,12 +404,12 @@ __global__ void __launch_bounds__(kStreamWaves * 64, 4) stream_kernel(MArgs a, S
   if (g < groups) first_batch(g, 0);
   for (; g < groups; g += sh.strips) {
     f32x4_t acc = {};
-    for (int part = 0; part < sh.column_parts; ++part) {
+    for (int part = 0; part < parts; ++part) {
       int step0, first, end, rest, last;
       share_of(part, &step0, &first, &end, &rest, &last);
-      if (sh.column_parts > 1 || g < sh.strips) {
+      if (parts > 1 || g < sh.strips) {
         if (part > 0 || g >= sh.strips) __syncthreads();
-        s.stage(lds, ch, part * sh.columns, sh.columns);
+        s.stage(lds, ch, part * columns, columns);
         __syncthreads();
       }
       const auto run = [&](auto ni) {
@@ -412,7 +431,7 @@ __global__ void __launch_bounds__(kStreamWaves * 64, 4) stream_kernel(MArgs a, S
         run(std::integral_constant<int, 2>{});
       else
         run(std::integral_constant<int, 4>{});
-      if (part + 1 < sh.column_parts)
+      if (part + 1 < parts)
         first_batch(g, part + 1);
       else if (g + sh.strips < groups)
         first_batch(g + sh.strips, 0);
@@ -461,15 +480,19 @@ gsi_status launch_as(const MArgs &a, hipStream_t st) {
   // two workgroups on a CU, and 39 us in parts of 4096, one on a CU; 300 tokens
   // over 32 experts 4096 -> 1024: 68 and 78 us).
   const int64_t busy = a.offsets ? std::max<int64_t>(experts, a.R / 16) : chunks;  // chunks with rows, about
+  // Experts with more rows than others: more and smaller workgroups than run at
+  // once even that out (100 tokens, six of 128 experts each, bf16 1024 -> 2048:
+  // 73 us with one round of workgroups, 54 with four).
+  const int64_t uneven = a.offsets && a.R > a.n ? 4 : 1;
   const int tokens = a.R < 16 ? a.R : 16;
   const int unit = S::C * U, padded = (a.d + S::C - 1) / S::C * S::C, blocks = (a.d_out + 15) / 16;
   StreamShape sh{};
   double best = INFINITY;
   for (int alone = 0; alone < 2; ++alone) {
-    const int room = ((alone ? kStreamLdsAlone : kStreamLds) / (tokens * S::XP) - 16) / S::xes / unit * unit;
-    const int columns = std::min(padded, room), parts = (a.d + columns - 1) / columns;
+    const int columns = columns_in<S, U>(alone ? kStreamLdsAlone : kStreamLds, tokens, padded);
+    const int parts = (a.d + columns - 1) / columns;
     const int batches = (columns + unit - 1) / unit;
-    const int64_t at_once = alone ? 256 : 512, want = (at_once + busy - 1) / busy;
+    const int64_t at_once = alone ? 256 : 512, want = (uneven * at_once + busy - 1) / busy;
     for (int split = 1; split <= kStreamWaves && (split == 1 || split <= batches); split *= 2) {
       const int sides = kStreamWaves / split, groups = (blocks + sides - 1) / sides;
       // x that fits is staged once for all of a workgroup's blocks
@@ -479,13 +502,12 @@ gsi_status launch_as(const MArgs &a, hipStream_t st) {
       // workgroups that share a CU overlap: their last round need not be full
       const double load = (double)strips * busy / at_once;
       const double cost = turn * (alone ? std::ceil(load) : std::max(1.0, load));
-      if (cost < best) best = cost, sh = {split, strips, columns, parts};
+      if (cost < best) best = cost, sh = {split, strips, tokens * S::XP * (columns * S::xes + 16)};
     }
     if (parts == 1) break;
   }
   if (chunks * sh.strips > INT32_MAX) return GSI_E_SHAPE;
-  const size_t lds = (size_t)tokens * S::XP * (sh.columns * S::xes + 16);
-  stream_kernel<K, G, U><<<(unsigned)(chunks * sh.strips), kStreamWaves * 64, lds, st>>>(a, sh);
+  stream_kernel<K, G, U><<<(unsigned)(chunks * sh.strips), kStreamWaves * 64, sh.room, st>>>(a, sh);
   return hipGetLastError() == hipSuccess ? GSI_OK : GSI_E_HIP;
 }
 

@@ -1,4 +1,11 @@
-// Plain linear maps with many rows per expert on gfx950 MFMA: 256 x 256 tiles.
+// Plain linear maps with many rows per expert on gfx950 MFMA, in tiles that
+// use every byte of W for many rows:
+//
+//   wide_kernel    : bf16, 256 x 256 tiles
+//   q4_wide_kernel : 4-bit weights and bf16 x, 256 x 128 tiles
+//   small_kernel   : 64 x 64 tiles, fp32 and few bf16 rows
+//
+// All stage their operands through LDS by direct loads, several stages ahead.
 #include "gsi_maps.h"
 
 namespace gsi {
@@ -144,7 +151,12 @@ __device__ __forceinline__ void landed() {
 // bf16 tiles of 256 tokens x 256 weight rows on 8 wavefronts, 2 x 4 of them,
 // each 32 TM tokens x 64 weight rows.  The columns go by in stages of 32; four
 // stages lie in LDS, filled by direct loads in a stream that runs on from one
-// tile into the next.
+// tile into the next.  Bound by the matrix cores and the clock they leave (one
+// 8192^3 product: 1140 TFLOP/s, MFMA busy 61 % of the cycles at 1.76 GHz).
+// 4096 tokens, four of 32 ragged experts each, 2048 -> 4096: 275 GFLOP in 330
+// to 350 us; with as many rows for every expert 305 (before the order of the
+// tiles was tuned: two stages of 64 columns 3 % slower than four of 32, loads
+// through registers 11 %).
 constexpr int kWideBM = 256, kWideBN = 256, kWideBK = 32;
 constexpr int kWideStage = (kWideBM + kWideBN) * kWideBK * 2;
 constexpr int kWideLoads = kWideStage / 1024 / 8;  // loads of a wavefront per stage, half x, half W
@@ -302,7 +314,9 @@ __device__ __forceinline__ void wide_tile(const MArgs &a, const Tile &tl, WideSo
 // every second turn from the other end, which gives each about the same; XCDs
 // with odd numbers walk their turns backwards, so that low rests, which are
 // bound by the weights from HBM, run beside full tiles of other XCDs, which are
-// not.
+// not (the ragged prompt above: 375 us with the list taken in order, 350 so;
+// every second workgroup backwards instead of every second XCD parts
+// neighbours that share an L2: 302 -> 365 us with even experts).
 __global__ void __launch_bounds__(512) wide_kernel(MArgs a) {
   // stages as separate objects, so that the compiler sees that filling one
   // does not touch the others
@@ -354,7 +368,10 @@ __global__ void __launch_bounds__(512) wide_kernel(MArgs a) {
 // group has a sum of its own in the matrix core's accumulators and is added
 // to the fp32 total with the group's scale, so nothing is rounded but fp32
 // sums.  Here A holds tokens and B weight rows: a lane's accumulators belong
-// to one weight row of each block and take one scale.
+// to one weight row of each block and take one scale.  Bound by issue: the
+// decoding and the scaling of the group sums run beside the products (2047
+// tokens 4096 -> 16384, groups of 128: 275 GFLOP in 324 us, 850 TFLOP/s, MFMA
+// busy 35 %; 764 us in the streaming kernel).
 constexpr int kQ4BN = 128;
 constexpr int kQ4X = kWideBM * kWideBK * 2, kQ4W = kQ4BN * kWideBK * 2;  // bytes of a stage
 
@@ -570,7 +587,10 @@ __global__ void __launch_bounds__(512) q4_wide_kernel(MArgs a) {
 // at any tile) and for bf16 with too few large tiles for the chip.  Several
 // workgroups share a CU.  A stage is 64 bytes of each row; the 16 bytes that a
 // lane reads of a row are one operand of 8 columns in bf16 and four of one
-// column in fp32, lanes 32 to 63 taking the other columns.
+// column in fp32, lanes 32 to 63 taking the other columns.  fp32 is bound by
+// its products where there are rows enough (333 tokens, three of 8 ragged
+// experts each, 1000 -> 1208: 2.4 GFLOP in 38 us, 63 TFLOP/s of the 135 that a
+// large product reaches; MFMA busy 33 %; 96 us in the streaming kernel).
 constexpr int kSmallB = 64;
 constexpr int kSmallStage = 2 * kSmallB * 64;
 
