@@ -30,13 +30,15 @@ gsi_status choose(const MArgs &a, const gsi_weights &w, hipStream_t st) {
   const bool f32 = w.dtype == GSI_FP32;
   const int64_t experts = a.n < a.R ? a.n : a.R, per = a.R / experts;
   if (w.bits == 4) {
-    // Large tiles once they beat streaming the weights for every 16 rows: a
-    // round of 256 tiles takes as long as about 6000 blocks of 16 x 16 there
-    // (4096 -> 16384: 64 tokens 62 us in tiles, 37 us streamed; 100 tokens
-    // 63 and 62; 512 tokens 85 and 182).
+    // Large tiles once they beat streaming the weights for every 16 rows: as
+    // many tiles as CUs, or fewer, take as long as about 9000 blocks of 16 x 16
+    // there (4096 -> 16384: 64 tokens 63 us in tiles, 39 us streamed; 128
+    // tokens 63 and 70; 512 tokens 86 and 243; 9120 -> 4608: 384 tokens 194 and
+    // 164, 512 tokens 192 and 210; 32 experts 2048 -> 2048: 1200 rows 70 and 63,
+    // 2400 rows 81 and 109).
     const int64_t tiles = (a.R / 256 + experts) * ((a.d_out + 127) / 128);
     const int64_t blocks = (a.R / 16 + experts) * ((a.d_out + 15) / 16);
-    if (!f32 && blocks >= 6000 * ((tiles + 255) / 256)) return launch_wide_q4(a, w.group, st);
+    if (!f32 && blocks >= 9000 && blocks / 9000. >= tiles / 256.) return launch_wide_q4(a, w.group, st);
     return launch_stream(a, f32 ? kQ4F32 : kQ4Bf16, w.group, st);
   }
   // Streaming for few rows per expert (16 experts 2048 -> 2048, 8 and 12 rows

@@ -305,6 +305,70 @@ def test_grouped_addresses_past_32_bits(kind, R):
     close(y[:, some], X @ W.T, np.abs(X) @ S.T, d, BF16, f"far {kind}")
 
 
+# ---- many rows: the tiled kernels ----
+
+# 256 x 128 tiles for 4 bits, 256 x 256 and 64 x 64 ones for bf16, 64 x 64 for fp32
+TILED = [("q4", 1048), ("bf16", 2056), ("bf16", 264), ("fp32", 264)]
+RAGGED = [1300, 0, 257, 700, 128, 1, 193]
+
+
+@pytest.mark.parametrize("d", [96, 288, 1056])
+@pytest.mark.parametrize("kind,d_out", TILED)
+def test_grouped_many_rows(kind, d_out, d):
+    g = gen(d + d_out)
+    R, T = sum(RAGGED), 900
+    w = make_weights(g, kind, len(RAGGED), d_out, d)
+    x = torch.randn(T, d, generator=g, device=DEV).to(F32 if kind == "fp32" else BF16)
+    offsets = to_offsets(RAGGED, first=3)
+    rows = torch.randint(1, T, (R + 8,), generator=g, device=DEV, dtype=torch.int32)
+    rows[3], rows[5 + R // 2], rows[R + 2] = -1, T, 2**31 - 1
+    x[0] = float("nan")  # row 0 stands in for no other row
+    wide = torch.randn(R + 8, d_out + 16, generator=g, device=DEV).to(x.dtype)
+    before, y = wide.clone(), wide.clone()
+    gsi.gsi_grouped_linear(w, x, offsets, rows, y=y[:, 8:-8])
+    check_grouped(w, kind, x, offsets, rows, y[:, 8:-8], before[:, 8:-8], f"many {kind} {d}x{d_out}")
+    assert torch.equal(bits(y[:, :8]), bits(before[:, :8])) and torch.equal(bits(y[:, -8:]), bits(before[:, -8:]))
+    again = before.clone()
+    gsi.gsi_grouped_linear(w, x, offsets, rows, y=again[:, 8:-8])
+    assert torch.equal(bits(again), bits(y))
+
+
+@pytest.mark.parametrize("kind,d_out", TILED)
+def test_grouped_many_rows_non_finite_and_bad_offsets(kind, d_out):
+    g = gen(d_out + 1)
+    R, d = sum(RAGGED), 160
+    w = make_weights(g, kind, len(RAGGED), d_out, d)
+    x = torch.randn(R, d, generator=g, device=DEV).to(F32 if kind == "fp32" else BF16)
+    offsets = to_offsets(RAGGED)
+    ref = gsi.gsi_grouped_linear(w, x, offsets)
+    for at, bad in ((0, float("inf")), (1299, float("nan")), (R - 1, float("-inf"))):
+        z = x.clone()
+        z[at, d - 1] = bad
+        y = gsi.gsi_grouped_linear(w, z, offsets)
+        keep = [t for t in range(R) if t != at]
+        assert torch.equal(bits(y[keep]), bits(ref[keep])) and not torch.isfinite(y[at]).any()
+    guard = torch.full((R + 20, d_out), 3.0, device=DEV, dtype=x.dtype)
+    bad = torch.tensor([-9, 1500, 5, 2**31 - 1, -5, 900, 2**31 - 1, -2**31], dtype=torch.int32, device=DEV)
+    gsi.gsi_grouped_linear(w, x, bad, y=guard[10:10 + R])
+    torch.cuda.synchronize()
+    assert bool((guard[:10] == 3.0).all()) and bool((guard[10 + R:] == 3.0).all())
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("d,T", [(96, 2305), (416, 2400), (1056, 2560)])
+def test_q4_many_tokens(d, T, group):
+    g = gen(d + T + group)
+    w = make_q4(g, (1048,), d, group, BF16, zeros=T % 2 == 1)
+    wide = torch.full((T, d + 24), float("nan"), device=DEV, dtype=BF16)
+    x = wide[:, 8:8 + d]
+    x.copy_(torch.randn(T, d, generator=g, device=DEV))
+    x[:, d // 3] *= 30
+    y = gsi.gsi_q4_linear(w, x)
+    W, S = q4_64(w)
+    X = f64(x)
+    close(y, X @ W.T, np.abs(X) @ S.T, d, BF16, f"q4 {d} {T} {group}")
+
+
 # ---- grouping and combining ----
 
 
