@@ -286,6 +286,9 @@ gsi_status gsi_calibrate(const gsi_calib *c, void *ws, size_t ws_bytes, void *st
  *   - x and y are given with row strides ldx and ldy in elements, multiples
  *     of 16 bytes; only the d (d_out) leading elements of a row are touched.
  *   - y must not overlap any input.
+ *   - A launch holds fewer than 2^32 threads: calls whose rows (with 16 more
+ *     for each expert) times d_out reach 2^31 may give GSI_E_SHAPE, and are
+ *     then cut by rows.
  *   - A token with Inf or NaN gives outputs that are not finite; the other
  *     tokens are unaffected.
  *

@@ -32,6 +32,9 @@ struct MArgs {
   int32_t groups;          // scale groups of a row
 };
 
+// A launch holds fewer than 2^32 threads.
+constexpr int64_t kMostThreads = (1LL << 32) - 1;
+
 enum Kind { kQ4Bf16, kQ4F32, kBf16, kF32 };
 
 // Launchers; group is 0 for dense kinds.  launch_wide: dense bf16.

@@ -506,7 +506,7 @@ gsi_status launch_as(const MArgs &a, hipStream_t st) {
     }
     if (parts == 1) break;
   }
-  if (chunks * sh.strips > INT32_MAX) return GSI_E_SHAPE;
+  if (chunks * sh.strips * kStreamWaves * 64 > kMostThreads) return GSI_E_SHAPE;
   stream_kernel<K, G, U><<<(unsigned)(chunks * sh.strips), kStreamWaves * 64, sh.room, st>>>(a, sh);
   return hipGetLastError() == hipSuccess ? GSI_OK : GSI_E_HIP;
 }

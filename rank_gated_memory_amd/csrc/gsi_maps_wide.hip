@@ -717,7 +717,7 @@ gsi_status launch_wide_q4(const MArgs &a, int group, hipStream_t st) {
   // with rows, each list rounded up to whole shares
   const int64_t slots = a.R / kWideBM + (a.n < a.R ? a.n : a.R);
   const int64_t grid = (slots * ((a.d_out + kQ4BN - 1) / kQ4BN) + 2 * kXcds) / kXcds * kXcds;
-  if (grid > INT32_MAX) return GSI_E_SHAPE;
+  if (grid * 512 > kMostThreads) return GSI_E_SHAPE;
   if (group == 128)
     q4_wide_kernel<128><<<(unsigned)grid, 512, 0, st>>>(a);
   else if (group == 64)
@@ -730,7 +730,7 @@ gsi_status launch_wide_q4(const MArgs &a, int group, hipStream_t st) {
 gsi_status launch_small(const MArgs &a, Kind kind, hipStream_t st) {
   const int64_t slots = a.R / kSmallB + (a.n < a.R ? a.n : a.R);
   const int64_t grid = (slots * ((a.d_out + kSmallB - 1) / kSmallB) + 2 * kXcds) / kXcds * kXcds;
-  if (grid > INT32_MAX) return GSI_E_SHAPE;
+  if (grid * 256 > kMostThreads) return GSI_E_SHAPE;
   if (kind == kF32)
     small_kernel<true><<<(unsigned)grid, 256, 0, st>>>(a);
   else

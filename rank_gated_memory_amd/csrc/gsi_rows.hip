@@ -353,7 +353,7 @@ gsi_status gsi_group_combine(const void *y, int64_t ldy, int32_t R, const int32_
     return GSI_E_ALIGN;
   const int per = (d / vec + 255) / 256;
   const int64_t grid = (int64_t)T * per;
-  if (grid > INT32_MAX) return GSI_E_SHAPE;
+  if (grid * 256 > UINT32_MAX) return GSI_E_SHAPE;  // a launch holds fewer than 2^32 threads
   const hipStream_t st = static_cast<hipStream_t>(stream);
   if (dtype == GSI_FP32)
     combine_kernel<float><<<(unsigned)grid, 256, 0, st>>>(static_cast<const float *>(y), ldy, R, pos, weights,

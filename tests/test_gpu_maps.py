@@ -369,6 +369,46 @@ def test_q4_many_tokens(d, T, group):
     close(y, X @ W.T, np.abs(X) @ S.T, d, BF16, f"q4 {d} {T} {group}")
 
 
+@pytest.mark.parametrize("kind,n,d,d_out,R", [("q4", 10, 131072, 8192, 2400), ("fp32", 17, 8192, 8192, 400)])
+def test_grouped_many_rows_past_32_bits(kind, n, d, d_out, R):
+    """As above for the tiles: the last expert's weights and the last rows lie far behind the first."""
+    g = gen(15)
+    dtype = BF16 if kind == "q4" else F32
+    if kind == "q4":
+        codes = torch.zeros(n, d_out, d // 2, device=DEV, dtype=torch.uint8)
+        codes[-1] = torch.randint(0, 256, (d_out, d // 2), generator=g, device=DEV, dtype=torch.uint8)
+        w = gsi.Q4(codes, torch.full((n, d_out, d // 128), 0.01, device=DEV, dtype=BF16), None, group=128)
+    else:
+        w = torch.zeros(n, d_out, d, device=DEV)
+        w[-1].normal_(0, d**-0.5, generator=g)
+    ld = (1 << 31) // (R - 1) // 8 * 8 + 64
+    x = torch.empty_strided((R, d), (max(ld, d), 1), device=DEV, dtype=dtype)
+    x.copy_(torch.randn(R, d, generator=g, device=DEV))
+    y = torch.empty_strided((R, d_out), (ld, 1), device=DEV, dtype=dtype)
+    gsi.gsi_grouped_linear(w, x, to_offsets([0] * (n - 1) + [R]), y=y)
+    some, at = torch.arange(0, d_out, 211, device=DEV), torch.arange(0, R, 57, device=DEV)
+    if kind == "q4":
+        W, S = q4_64(gsi.Q4(w.codes[-1][some], w.scales[-1][some].contiguous(), None, group=128))
+    else:
+        W = f64(w[-1][some])
+        S = np.abs(W)
+    X = f64(x[at])
+    close(y[at][:, some], X @ W.T, np.abs(X) @ S.T, d, dtype, f"far tiles {kind}")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q4"])
+@pytest.mark.parametrize("R", [40, 6000])
+def test_grouped_over_thousands_of_experts(kind, R):
+    g = gen(R)
+    n, d, d_out = 3000, 32, 16
+    w = make_weights(g, kind, n, d_out, d)
+    ids = torch.randint(0, n, (R, 1), generator=g, device=DEV)
+    offsets = torch.searchsorted(torch.sort(ids[:, 0]).values, torch.arange(n + 1, device=DEV)).to(torch.int32)
+    x = torch.randn(R, d, generator=g, device=DEV).to(BF16)
+    before = torch.zeros(R, d_out, device=DEV, dtype=BF16)
+    check_grouped(w, kind, x, offsets, None, gsi.gsi_grouped_linear(w, x, offsets), before, f"{n} experts {kind}")
+
+
 # ---- grouping and combining ----
 
 

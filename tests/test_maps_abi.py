@@ -117,6 +117,14 @@ def test_group_combine_empty():
     assert gsi.lib().gsi_group_combine(None, 64, 0, None, None, None, 0, None, 64, 0, 2, 64, 1, None) == GSI_OK
 
 
+def test_refuses_what_no_launch_holds():
+    """2^32 threads and more, before anything is launched."""
+    assert gsi.lib().gsi_group_combine(FAKE, 64, 9, FAKE, None, None, 0, FAKE, 64, 1 << 24, 2, 64, 1, None) == E_SHAPE
+    assert q4(weights(dtype=0, d=1 << 14, d_out=1 << 16), ldx=1 << 14, ldy=1 << 16, T=1 << 20) == E_SHAPE
+    assert q4(weights(dtype=1, d_out=1 << 16), ldy=1 << 16, T=1 << 24) == E_SHAPE
+    assert grouped(dense(dtype=0, d_out=1 << 16), ldy=1 << 16, R=1 << 24, T=1 << 24) == E_SHAPE
+
+
 def test_binding_refuses():
     codes = torch.zeros(64, 128, dtype=torch.uint8)
     scales = torch.ones(64, 2)
