@@ -587,10 +587,14 @@ __global__ void __launch_bounds__(512) q4_wide_kernel(MArgs a) {
 // at any tile) and for bf16 with too few large tiles for the chip.  Several
 // workgroups share a CU.  A stage is 64 bytes of each row; the 16 bytes that a
 // lane reads of a row are one operand of 8 columns in bf16 and four of one
-// column in fp32, lanes 32 to 63 taking the other columns.  fp32 is bound by
-// its products where there are rows enough (333 tokens, three of 8 ragged
-// experts each, 1000 -> 1208: 2.4 GFLOP in 38 us, 63 TFLOP/s of the 135 that a
-// large product reaches; MFMA busy 33 %; 96 us in the streaming kernel).
+// column in fp32, lanes 32 to 63 taking the other columns.  A tile of at most
+// 32 tokens has each pair of wavefronts take half of every stage, and their
+// sums joined (200 tokens, four of 8 experts each, fp32 2048 -> 2048: 99 us with
+// the second half of the tokens idle, 89 so; tiles of 32 tokens throughout: 96).
+// fp32 is bound by its products where there are rows enough (333 tokens, three
+// of 8 ragged experts each, 1000 -> 1208: 2.4 GFLOP in 38 us, 63 TFLOP/s of the
+// 135 that a large product reaches; MFMA busy 33 %; 96 us in the streaming
+// kernel).
 constexpr int kSmallB = 64;
 constexpr int kSmallStage = 2 * kSmallB * 64;
 
@@ -631,10 +635,13 @@ __global__ void __launch_bounds__(256) small_kernel(MArgs a) {
   };
 
   f32x16_t acc = {};
+  // where the operands of half a stage lie; in a low tile both halves of the
+  // wavefronts have the same tokens and each its own half of every stage
+  const bool low = tl.count <= 32;
   int xat[2], wat[2];
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    xat[s] = wm * 2048 + tile_at<32>(l32, 2 * s + half);
+    xat[s] = (low ? 0 : wm * 2048) + tile_at<32>(l32, 2 * s + half);
     wat[s] = kSmallB * 64 + wn * 2048 + tile_at<32>(l32, 2 * s + half);
   }
   u32x4_t wf[2], xf[2];
@@ -662,28 +669,53 @@ __global__ void __launch_bounds__(256) small_kernel(MArgs a) {
     multiply(1);
     landed<2>();
   };
+  // of a low tile: registers p hold this stage, the others take the next
+  const int mine = xat[wm], mine_w = wat[wm];
+  const auto read_low = [&](const uint8_t *st, int p) {
+    wf[p] = *reinterpret_cast<const u32x4_t *>(st + mine_w);
+    xf[p] = *reinterpret_cast<const u32x4_t *>(st + mine);
+  };
+  const auto step_low = [&](int p, const uint8_t *next, uint8_t *fill) {
+    fetch(fill);
+    read_low(next, 1 - p);
+    multiply(p);
+    landed<2>();
+  };
   fetch(lds0);
   fetch(lds1);
   fetch(lds2);
   landed<2>();
-  read(lds0, 0);
-  if (wm * 32 < tl.count) {
+  if (low) {
+    read_low(lds0, 0);
+    for (int k = 0; k < a.d; k += 4 * C) {
+      step_low(0, lds1, lds3);
+      step_low(1, lds2, lds0);
+      step_low(0, lds3, lds1);
+      step_low(1, lds0, lds2);
+    }
+  } else {
+    read(lds0, 0);
     for (int k = 0; k < a.d; k += 4 * C) {
       step(lds0, lds1, lds3);
       step(lds1, lds2, lds0);
       step(lds2, lds3, lds1);
       step(lds3, lds0, lds2);
     }
-  } else {  // no token of this half: it brings its share of the stages
-    for (int k = 0; k < a.d; k += 4 * C) {
-      fetch(lds3), landed<2>();
-      fetch(lds0), landed<2>();
-      fetch(lds1), landed<2>();
-      fetch(lds2), landed<2>();
-    }
   }
   landed<0>();
 
+  if (low) {  // the sums of the second halves, in the room of a stage
+    static_assert(2 * 16 * 64 * 4 <= kSmallStage);
+    float *const other = reinterpret_cast<float *>(lds0) + wn * (16 * 64) + lane;
+    if (wm) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) other[i * 64] = acc[i];
+    }
+    landed<0>();
+    if (wm) return;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] += other[i * 64];
+  }
   const int m = wm * 32 + l32;
   if (m >= tl.count) return;
   const int r = tl.row + m, src = a.rows ? a.rows[r] : r;
