@@ -14,13 +14,14 @@
 //                   us instead of 22 and 23 for 24 and 40 tokens of a 4-bit
 //                   4096 x 4096 map.)
 //                   24 tokens' 192 rows over 128 experts in 4 bits, 4096 ->
-//                   1536: 266 MB in 41 to 46 us, 6.2 TB/s.  8 experts' bf16
-//                   maps 2048 -> 2816 for one token: 92 MB in 19 us.  A 4-bit
-//                   4096 x 4096 map for one token, 8.8 MB: 6 us, most of it
-//                   launch and latency; 5 tokens 4096 -> 50400, 113 MB: 32 us,
-//                   where reading the weights in this pattern alone takes 23.
-//                   With more tokens the staging of x shows: 13 fp32 tokens
-//                   5120 -> 13824, 47 MB: 32 us.
+//                   1536: 36 to 56 us for about 160 MB, by how uneven the
+//                   experts are.  8 experts' bf16 maps 2048 -> 2816 for one
+//                   token: 92 MB in 19 us.  A 4-bit 4096 x 4096 map for one
+//                   token, 8.8 MB: 6 us, most of it launch and latency; 5
+//                   tokens 4096 -> 50400, 113 MB: 32 us, where reading the
+//                   weights in this pattern alone takes 23.  With more tokens
+//                   the staging of x shows: 13 fp32 tokens 5120 -> 13824, 47
+//                   MB: 28 us.
 //
 // 4-bit weights.  With w = s (q - z) a group's share of y is
 //   s (sum q x - z sum x) = s (sum (16 + q) x - (16 + z) sum x).
@@ -144,7 +145,7 @@ __device__ __forceinline__ void split_octet(const f32x4_t (&u)[2], bf16x8_t (&ou
 template <Kind K>
 constexpr int kStepColumns = K == kQ4Bf16 || K == kQ4F32 ? 128 : K == kBf16 ? 32 : 16;
 
-constexpr int kStreamWaves = 8;
+constexpr int kStreamWaves = 16;  // at most, of a workgroup that has the CU for itself; 8 of one that shares it
 constexpr int kStreamLds = 64 * 1024;        // x of a chunk; two workgroups of a CU hold theirs
 constexpr int kStreamLdsAlone = 144 * 1024;  // of a workgroup that has the CU for itself
 
@@ -153,6 +154,7 @@ struct StreamShape {
   int split;         // wavefronts that share the columns of a block of weight rows
   int strips;        // workgroups per chunk
   int room;          // bytes of LDS for x
+  int waves;         // of a workgroup
 };
 
 template <Kind K, int G, int U>
@@ -249,10 +251,10 @@ struct Stream {
   // each part, zeros behind d and for rows without a source, octets in the
   // order of decode() where the weights are codes.  Only the chunk's own rows
   // are written; those behind them are never read.
-  __device__ __forceinline__ void stage(uint8_t *lds, const Chunk &ch, int c0, int columns) const {
+  __device__ __forceinline__ void stage(uint8_t *lds, const Chunk &ch, int c0, int columns, int threads) const {
     constexpr int V = K == kF32 ? 4 : 8;  // columns of a 16-byte piece
     const int pieces = columns / V, stride = x_stride(columns);
-    for (int k = threadIdx.x; k < ch.count * pieces; k += kStreamWaves * 64) {
+    for (int k = threadIdx.x; k < ch.count * pieces; k += threads) {
       const int m = k / pieces, p = k - m * pieces, c = c0 + p * V;
       const int src = a.rows ? a.rows[ch.row + m] : ch.row + m;
       const bool in = c < a.d && src >= 0 && src < a.T;
@@ -372,7 +374,7 @@ __global__ void __launch_bounds__(kStreamWaves * 64, 4) stream_kernel(MArgs a, S
   S s(a, lane);
   // a workgroup's wavefronts: kStreamWaves / split blocks of weight rows, the
   // columns of each in `split` shares of whole batches
-  const int side = wave / sh.split, share = wave % sh.split, sides = kStreamWaves / sh.split;
+  const int side = wave / sh.split, share = wave % sh.split, sides = sh.waves / sh.split;
   const int blocks = (a.d_out + 15) / 16, groups = (blocks + sides - 1) / sides;
   // accumulators of a lane that hold tokens
   const int live = S::q4 ? (ch.count + 3) / 4 : 4;
@@ -409,7 +411,7 @@ __global__ void __launch_bounds__(kStreamWaves * 64, 4) stream_kernel(MArgs a, S
       share_of(part, &step0, &first, &end, &rest, &last);
       if (parts > 1 || g < sh.strips) {
         if (part > 0 || g >= sh.strips) __syncthreads();
-        s.stage(lds, ch, part * columns, columns);
+        s.stage(lds, ch, part * columns, columns, sh.waves * 64);
         __syncthreads();
       }
       const auto run = [&](auto ni) {
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(kStreamWaves * 64, 4) stream_kernel(MArgs a, S
 #pragma unroll
       for (int i = 0; i < 4; ++i) red[wave][(4 * i + s.quad) * 16 + s.l16] = acc[i];
       __syncthreads();
-      for (int k = threadIdx.x; k < sides * 256; k += kStreamWaves * 64) {
+      for (int k = threadIdx.x; k < sides * 256; k += sh.waves * 64) {
         float v = 0.f;
         for (int w = 0; w < sh.split; ++w) v += red[k / 256 * sh.split + w][k % 256];
         put(k / 256, k % 256, v);
@@ -477,8 +479,10 @@ gsi_status launch_as(const MArgs &a, hipStream_t st) {
   // x that does not fit, one part after the other, two for each part.  Then a
   // workgroup may also have the CU for itself, with fewer and longer parts (16
   // tokens through a 4-bit 16384 -> 4096 map: 64 us in parts of 1536 columns,
-  // two workgroups on a CU, and 39 us in parts of 4096, one on a CU; 300 tokens
-  // over 32 experts 4096 -> 1024: 68 and 78 us).
+  // two workgroups on a CU, and 40 us in parts of 4096, one on a CU; 300 tokens
+  // over 32 experts 4096 -> 1024: 68 and 78 us), of 8 wavefronts or of 16 (64
+  // tokens 4096 -> 16384: 37 and 33 us; 16 tokens 4096 -> 4096, whose blocks 16
+  // leave on half of the CUs: 10.3 and 11.6).
   const int64_t busy = a.offsets ? std::max<int64_t>(experts, a.R / 16) : chunks;  // chunks with rows, about
   // Experts with more rows than others: more and smaller workgroups than run at
   // once even that out (100 tokens, six of 128 experts each, bf16 1024 -> 2048:
@@ -488,13 +492,15 @@ gsi_status launch_as(const MArgs &a, hipStream_t st) {
   const int unit = S::C * U, padded = (a.d + S::C - 1) / S::C * S::C, blocks = (a.d_out + 15) / 16;
   StreamShape sh{};
   double best = INFINITY;
-  for (int alone = 0; alone < 2; ++alone) {
+  for (int mode = 0; mode < 3; ++mode) {  // two workgroups on a CU, one of 8 wavefronts, one of 16
+    const bool alone = mode > 0;
     const int columns = columns_in<S, U>(alone ? kStreamLdsAlone : kStreamLds, tokens, padded);
     const int parts = (a.d + columns - 1) / columns;
     const int batches = (columns + unit - 1) / unit;
+    const int waves = mode == 2 ? kStreamWaves : kStreamWaves / 2;
     const int64_t at_once = alone ? 256 : 512, want = (uneven * at_once + busy - 1) / busy;
-    for (int split = 1; split <= kStreamWaves && (split == 1 || split <= batches); split *= 2) {
-      const int sides = kStreamWaves / split, groups = (blocks + sides - 1) / sides;
+    for (int split = 1; split <= waves && (split == 1 || split <= batches); split *= 2) {
+      const int sides = waves / split, groups = (blocks + sides - 1) / sides;
       // x that fits is staged once for all of a workgroup's blocks
       const int strips = parts > 1 ? groups : (int)std::min<int64_t>(groups, want);
       const int64_t part = 2 * ((batches + split - 1) / split) + (parts > 1 ? 2 : 0);
@@ -502,12 +508,12 @@ gsi_status launch_as(const MArgs &a, hipStream_t st) {
       // workgroups that share a CU overlap: their last round need not be full
       const double load = (double)strips * busy / at_once;
       const double cost = turn * (alone ? std::ceil(load) : std::max(1.0, load));
-      if (cost < best) best = cost, sh = {split, strips, tokens * S::XP * (columns * S::xes + 16)};
+      if (cost < best) best = cost, sh = {split, strips, tokens * S::XP * (columns * S::xes + 16), waves};
     }
-    if (parts == 1) break;
+    if (parts == 1 && !alone) break;
   }
-  if (chunks * sh.strips * kStreamWaves * 64 > kMostThreads) return GSI_E_SHAPE;
-  stream_kernel<K, G, U><<<(unsigned)(chunks * sh.strips), kStreamWaves * 64, sh.room, st>>>(a, sh);
+  if (chunks * sh.strips * sh.waves * 64 > kMostThreads) return GSI_E_SHAPE;
+  stream_kernel<K, G, U><<<(unsigned)(chunks * sh.strips), sh.waves * 64, sh.room, st>>>(a, sh);
   return hipGetLastError() == hipSuccess ? GSI_OK : GSI_E_HIP;
 }
 
