@@ -388,6 +388,17 @@ def _call(where: str, fn, device: torch.device, stream, *args):
         raise GsiError(status, where)
 
 
+def _empty(shape, dtype, device: torch.device, stream) -> torch.Tensor:
+    """A new output, allocated on the stream that the call runs on: memory freed
+    on the current one may still be written by what runs there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _rows2d(t: torch.Tensor, name: str, dtype, device, cols: int, n: int | None = None) -> int:
     """The row stride of a [n][cols] tensor whose rows are contiguous."""
     shape = t.shape
@@ -447,7 +458,7 @@ def gsi_q4_linear(w: Q4, x: torch.Tensor, y: torch.Tensor | None = None, stream=
     ldx = _rows2d(x, "x", dtype, dev, w.d)
     T = x.shape[0]
     if y is None:
-        y, ldy = torch.empty((T, d_out), dtype=dtype, device=dev), d_out
+        y, ldy = _empty((T, d_out), dtype, dev, stream), d_out
     else:
         ldy = _rows2d(y, "y", dtype, dev, d_out, T)
     _call("gsi_q4_linear", lib().gsi_q4_linear, dev, stream, w.struct, x.data_ptr(), ldx, y.data_ptr(), ldy, T)
@@ -477,7 +488,7 @@ def gsi_grouped_linear(w, x: torch.Tensor, offsets: torch.Tensor, rows: torch.Te
     if rows is not None:
         _ints(rows, "rows", (R,), dev)
     if y is None:
-        y, ldy = torch.empty((R, d_out), dtype=dtype, device=dev), d_out
+        y, ldy = _empty((R, d_out), dtype, dev, stream), d_out
     else:
         ldy = _rows2d(y, "y", dtype, dev, d_out, R)
     _call("gsi_grouped_linear", lib().gsi_grouped_linear, dev, stream, struct, x.data_ptr(), ldx, x.shape[0],
@@ -496,12 +507,12 @@ def gsi_group_rows(ids: torch.Tensor, n: int, offsets: torch.Tensor | None = Non
     dev = ids.device
     if offsets is None and rows is None and pos is None:
         at = T * top
-        rows, pos, offsets = torch.empty(2 * at + n + 1, dtype=torch.int32, device=dev).split((at, at, n + 1))
+        rows, pos, offsets = _empty(2 * at + n + 1, torch.int32, dev, stream).split((at, at, n + 1))
         pos = pos.view(T, top)
     else:
-        offsets = torch.empty(n + 1, dtype=torch.int32, device=dev) if offsets is None else offsets
-        rows = torch.empty(T * top, dtype=torch.int32, device=dev) if rows is None else rows
-        pos = torch.empty((T, top), dtype=torch.int32, device=dev) if pos is None else pos
+        offsets = _empty(n + 1, torch.int32, dev, stream) if offsets is None else offsets
+        rows = _empty(T * top, torch.int32, dev, stream) if rows is None else rows
+        pos = _empty((T, top), torch.int32, dev, stream) if pos is None else pos
         _ints(offsets, "offsets", (n + 1,), dev)
         _ints(rows, "rows", (T * top,), dev)
         _ints(pos, "pos", (T, top), dev)
@@ -526,7 +537,7 @@ def gsi_group_combine(y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor 
         raise ValueError("weights must be contiguous fp32 like pos")
     ldb = 0 if base is None else _rows2d(base, "base", dtype, dev, d, T)
     if out is None:
-        out, ldo = torch.empty((T, d), dtype=dtype, device=dev), d
+        out, ldo = _empty((T, d), dtype, dev, stream), d
     else:
         ldo = _rows2d(out, "out", dtype, dev, d, T)
     _call("gsi_group_combine", lib().gsi_group_combine, dev, stream, y.data_ptr(), ldy, y.shape[0], pos.data_ptr(),

@@ -552,3 +552,27 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for a, y in zip(alone, ys):
         assert all(torch.equal(bits(a), bits(v)) for v in y)
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_new_outputs_belong_to_the_stream_of_the_call(raw):
+    """An output is not put where work of the current stream is still to write."""
+    g = gen(22)
+    w = make_q4(g, (1024,), 1024, 128, BF16)
+    x = torch.randn(512, 1024, generator=g, device=DEV).to(BF16)
+    ids = torch.randint(0, 8, (1 << 19, 1), generator=g, device=DEV).to(torch.int32)
+    want, order = gsi.gsi_q4_linear(w, x), gsi.gsi_group_rows(ids, 8)
+    a = torch.randn(4096, 4096, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    junk = [torch.empty_like(want), torch.empty(2 * ids.numel() + 9, device=DEV, dtype=torch.int32)]
+    for _ in range(20):
+        a = a @ a * 1e-3
+    for j in junk:
+        j.fill_(7)
+    del junk, j
+    stream = side.cuda_stream if raw else side
+    y = gsi.gsi_q4_linear(w, x, stream=stream)
+    got = gsi.gsi_group_rows(ids, 8, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(bits(y), bits(want)) and all(torch.equal(p, q) for p, q in zip(got, order))
