@@ -473,7 +473,7 @@ gsi_status launch_as(const MArgs &a, hipStream_t st) {
   using S = Stream<K, G, U>;
   static_assert(16 * S::XP * (S::C * U * S::xes + 16) <= kStreamLds, "one batch of columns fits");
   const int experts = a.n < a.R ? a.n : a.R;
-  const int64_t chunks = (a.R + 15) / 16 + (a.offsets ? experts : 0);
+  const int64_t chunks = ((int64_t)a.R + 15) / 16 + (a.offsets ? experts : 0);  // a.R + 15 may pass 2^31
   // The cheapest shape, in half batches that a wavefront goes through in a row
   // until the last chunk is done: joining a split block costs about one, and
   // x that does not fit, one part after the other, two for each part.  Then a

@@ -125,6 +125,16 @@ def test_refuses_what_no_launch_holds():
     assert grouped(dense(dtype=0, d_out=1 << 16), ldy=1 << 16, R=1 << 24, T=1 << 24) == E_SHAPE
 
 
+@pytest.mark.parametrize("rows", [2**31 - 16, 2**31 - 15, 2**31 - 1])
+@pytest.mark.parametrize("dtype", [0, 1], ids=["fp32", "bf16"])
+def test_refuses_the_largest_row_counts(rows, dtype):
+    """Counts next to 2^31, where sums of 32 bits would wrap: with and without offsets."""
+    w = dict(d=32, d_out=8, dtype=dtype)
+    assert q4(weights(**w), ldx=32, ldy=8, T=rows) == E_SHAPE
+    assert grouped(weights(n=4, **w), ldx=32, ldy=8, R=rows) == E_SHAPE
+    assert grouped(weights(n=4096, **w), ldx=32, ldy=8, R=rows) == E_SHAPE
+
+
 def test_binding_refuses():
     codes = torch.zeros(64, 128, dtype=torch.uint8)
     scales = torch.ones(64, 2)
