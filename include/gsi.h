@@ -286,9 +286,11 @@ gsi_status gsi_calibrate(const gsi_calib *c, void *ws, size_t ws_bytes, void *st
  *   - x and y are given with row strides ldx and ldy in elements, multiples
  *     of 16 bytes; only the d (d_out) leading elements of a row are touched.
  *   - y must not overlap any input.
- *   - A launch holds fewer than 2^32 threads: calls whose rows (with 16 more
- *     for each expert) times d_out reach 2^31 may give GSI_E_SHAPE, and are
- *     then cut by rows.
+ *   - A launch holds fewer than 2^32 threads, and a map of few outputs still
+ *     takes a whole workgroup for 16 rows: gsi_q4_linear and
+ *     gsi_grouped_linear may give GSI_E_SHAPE from (R + 16 n) (d_out + 127) =
+ *     2^32 on (R rows of y, n maps; for 8 outputs some 31 million rows).  Such
+ *     calls are cut by rows.
  *   - A token with Inf or NaN gives outputs that are not finite; the other
  *     tokens are unaffected.
  *
@@ -301,8 +303,9 @@ gsi_status gsi_calibrate(const gsi_calib *c, void *ws, size_t ws_bytes, void *st
  *            are read), or NULL for 8 everywhere
  *   group  : 32, 64 or 128 columns of a row per scale; the last group of a
  *            row may be shorter
- * d is a multiple of 8 (bits = 0) or 32 (bits = 4), at most 2^20; d_out a
- * multiple of 8, at most 2^24; W 16-byte aligned, stride a multiple of 16
+ * n is 1..4096 (gsi_group_rows orders choices among at most 1024); d is a
+ * multiple of 8 (bits = 0) or 32 (bits = 4), at most 2^20; d_out a multiple
+ * of 8, at most 2^24; W 16-byte aligned, stride a multiple of 16
  * bytes.  Products accumulate in fp32: codes and bf16 values multiply
  * exactly, a group's scale multiplies the group's fp32 sum, and y is
  * rounded once.  With 4-bit weights and |x| near the largest fp32 value the
@@ -330,7 +333,8 @@ gsi_status gsi_q4_linear(const gsi_weights *w, const void *x, int64_t ldx, void 
  *   offsets : [n + 1] int32 (device), nondecreasing within [0, R]
  *   rows    : [R] int32 (device), the x row of each y row, or NULL for r
  *             itself; an entry outside [0, T) gives a y row of zeros
- *   T       : rows of x;  R : rows of y (and of `rows`)
+ *   T       : rows of x, at least 1 where R > 0
+ *   R       : rows of y (and of `rows`)
  * Rows of y outside [offsets[0], offsets[n]) are left as they were.  The
  * offsets are read on the device: nothing waits for them on the host, and
  * entries outside [0, R] are clamped to it.  R == 0 is a no-op. */
@@ -347,7 +351,8 @@ gsi_status gsi_grouped_linear(const gsi_weights *w, const void *x, int64_t ldx, 
  *   rows    : [T * top] int32, the token t of each grouped row; -1 behind
  *             the last kept one
  *   pos     : [T * top] int32, the grouped row of each choice, -1 if dropped
- * n in 1..1024, T * top <= 2^26.  T == 0 writes the offsets only. */
+ * n in 1..1024, T * top <= 2^26.  T == 0 writes the offsets only.  The
+ * outputs overlap neither ids nor each other. */
 gsi_status gsi_group_rows(const void *ids, int32_t ids_bytes, int32_t T, int32_t top, int32_t n,
                           int32_t *offsets, int32_t *rows, int32_t *pos, void *stream);
 
@@ -359,7 +364,9 @@ gsi_status gsi_group_rows(const void *ids, int32_t ids_bytes, int32_t T, int32_t
  *   weights : [T][top] fp32, or NULL for 1
  *   base    : T rows, row stride ldb, or NULL for 0
  *   out     : T rows, row stride ldo; may be base itself (same stride)
- * d a multiple of 8, top in 1..64. */
+ * d a multiple of 8, at most 2^20; top in 1..64.  A token takes a workgroup
+ * for every 4 KiB of its row, the last one rounded up: 2^24 of them and more
+ * give GSI_E_SHAPE. */
 gsi_status gsi_group_combine(const void *y, int64_t ldy, int32_t R, const int32_t *pos,
                              const float *weights, const void *base, int64_t ldb, void *out,
                              int64_t ldo, int32_t T, int32_t top, int32_t d, int32_t dtype,

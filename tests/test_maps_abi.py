@@ -135,6 +135,39 @@ def test_refuses_the_largest_row_counts(rows, dtype):
     assert grouped(weights(n=4096, **w), ldx=32, ldy=8, R=rows) == E_SHAPE
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="on a GPU these calls would be launched on addresses that are none")
+@pytest.mark.parametrize("n", [1, 64, 4096])
+@pytest.mark.parametrize("d_out", [8, 24, 136, 144, 264, 800, 8192, 1 << 20])
+@pytest.mark.parametrize("d", [32, 5120, 16384])
+def test_calls_within_the_documented_size_are_not_refused(d, d_out, n):
+    """(R + 16 n)(d_out + 127) just below 2^32, at every form; without a device the launch itself fails."""
+    R = (2**32 - 1) // (d_out + 127) - 16 * n
+    if R < 1:
+        pytest.skip("no rows left")
+    for dtype in (0, 1):
+        if n == 1:
+            assert q4(weights(d=d, d_out=d_out, dtype=dtype), ldx=d, ldy=d_out, T=R) == E_HIP
+        assert grouped(weights(d=d, d_out=d_out, n=n, dtype=dtype), ldx=d, ldy=d_out, R=R) == E_HIP
+        assert grouped(dense(d=d, d_out=d_out, n=n, dtype=dtype), ldx=d, ldy=d_out, R=R) == E_HIP
+
+
+def test_combines_the_documented_number_of_workgroups():
+    """A workgroup for every token and started 4 KiB of its row, fewer than 2^24 of them."""
+    def call(T, d, dtype):
+        return gsi.lib().gsi_group_combine(FAKE, d, 9, FAKE, None, None, 0, FAKE, d, T, 2, d, dtype, None)
+    for d, dtype, per in ((8, 1, 1), (2048, 1, 1), (2056, 1, 2), (1024, 0, 1), (1032, 0, 2), (1 << 20, 0, 1024)):
+        most = ((1 << 24) - 1) // per
+        assert call(most + 1, d, dtype) == E_SHAPE
+        if not torch.cuda.is_available():
+            assert call(most, d, dtype) == E_HIP
+
+
+def test_refuses_narrow_maps_that_no_launch_holds():
+    """A map of 8 outputs takes a whole workgroup for 16 rows."""
+    assert q4(weights(d=32, d_out=8, dtype=0), ldx=32, ldy=8, T=1 << 27) == E_SHAPE
+    assert grouped(weights(n=4, d=32, d_out=8, dtype=0), ldx=32, ldy=8, R=1 << 27) == E_SHAPE
+
+
 def test_binding_refuses():
     codes = torch.zeros(64, 128, dtype=torch.uint8)
     scales = torch.ones(64, 2)
