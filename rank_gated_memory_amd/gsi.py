@@ -399,6 +399,12 @@ def _empty(shape, dtype, device: torch.device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _sizes(where: str, *sizes: int):
+    """The library's sizes are int32, and ctypes drops the bits above without a word."""
+    if max(sizes) >= 1 << 31:
+        raise ValueError(f"{where}: sizes must be below 2^31, are {sizes}")
+
+
 def _rows2d(t: torch.Tensor, name: str, dtype, device, cols: int, n: int | None = None) -> int:
     """The row stride of a [n][cols] tensor whose rows are contiguous."""
     shape = t.shape
@@ -436,6 +442,7 @@ class Q4:
         self.codes, self.scales, self.zeros, self.group = codes, scales, zeros, group
         self.n = codes.shape[0] if codes.dim() == 3 else 1
         self.d_out, self.d = codes.shape[-2], 2 * codes.shape[-1]
+        _sizes("Q4", self.n, self.d_out, self.d)
         self.dtype, self.device = scales.dtype, codes.device
         want = (*codes.shape[:-1], (self.d + group - 1) // group)
         for t, name in ((scales, "scales"), (zeros, "zeros")):
@@ -457,6 +464,7 @@ def gsi_q4_linear(w: Q4, x: torch.Tensor, y: torch.Tensor | None = None, stream=
     dtype, dev, d_out = w.dtype, w.device, w.d_out
     ldx = _rows2d(x, "x", dtype, dev, w.d)
     T = x.shape[0]
+    _sizes("gsi_q4_linear", T)
     if y is None:
         y, ldy = _empty((T, d_out), dtype, dev, stream), d_out
     else:
@@ -484,6 +492,7 @@ def gsi_grouped_linear(w, x: torch.Tensor, offsets: torch.Tensor, rows: torch.Te
         struct = GsiWeightsStruct(d, d_out, n, _dtype_code(w), 0, 0, stride, w.data_ptr(), None, None)
     ldx = _rows2d(x, "x", dtype, dev, d)
     R = x.shape[0] if rows is None else rows.shape[0]
+    _sizes("gsi_grouped_linear", x.shape[0], R, n, d_out, d)
     _ints(offsets, "offsets", (n + 1,), dev)
     if rows is not None:
         _ints(rows, "rows", (R,), dev)
@@ -505,6 +514,7 @@ def gsi_group_rows(ids: torch.Tensor, n: int, offsets: torch.Tensor | None = Non
         raise ValueError("ids must be contiguous [T][top], int32 or int64")
     T, top = ids.shape
     dev = ids.device
+    _sizes("gsi_group_rows", T, top, n)
     if offsets is None and rows is None and pos is None:
         at = T * top
         rows, pos, offsets = _empty(2 * at + n + 1, torch.int32, dev, stream).split((at, at, n + 1))
@@ -530,6 +540,7 @@ def gsi_group_combine(y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor 
         raise ValueError("y must be [R][d] and pos [T][top]")
     T, top = pos.shape
     d, dtype, dev = y.shape[1], y.dtype, y.device
+    _sizes("gsi_group_combine", T, top, y.shape[0], d)
     ldy = _rows2d(y, "y", dtype, dev, d)
     _ints(pos, "pos", (T, top), dev)
     if weights is not None and (weights.dtype != torch.float32 or weights.device != dev or not weights.is_contiguous()

@@ -211,6 +211,31 @@ def test_binding_refuses():
             gsi.gsi_group_combine(**{**dict(y=x, pos=pos), **kw})
 
 
+def test_binding_refuses_sizes_past_32_bits():
+    """2^32 + 5 rows must not become 5 on their way into the library (meta tensors: no memory behind them)."""
+    big = 2**32 + 5
+
+    def meta(*shape, dtype=torch.bfloat16):
+        return torch.empty(*shape, dtype=dtype, device="meta")
+    i32, u8 = torch.int32, torch.uint8
+    w, off = meta(2, 8, 8), meta(3, dtype=i32)
+    few = gsi.Q4(meta(8, 16, dtype=u8), meta(8, 1), None, group=32)
+    for call in (lambda: gsi.gsi_q4_linear(few, meta(big, 32)),
+                 lambda: gsi.gsi_grouped_linear(w, meta(big, 8), off),
+                 lambda: gsi.gsi_grouped_linear(w, meta(7, 8), off, rows=meta(big, dtype=i32)),
+                 lambda: gsi.gsi_grouped_linear(meta(2, big + 3, 8), meta(7, 8), off),
+                 lambda: gsi.Q4(meta(big + 3, 16, dtype=u8), meta(big + 3, 1), None, group=32),
+                 lambda: gsi.Q4(meta(big, 8, 16, dtype=u8), meta(big, 8, 1), None, group=32),
+                 lambda: gsi.gsi_group_rows(meta(big, 1, dtype=i32), 4),
+                 lambda: gsi.gsi_group_rows(meta(3, big, dtype=i32), 4),
+                 lambda: gsi.gsi_group_rows(meta(3, 2, dtype=i32), big),
+                 lambda: gsi.gsi_group_combine(meta(7, 8), meta(big, 1, dtype=i32)),
+                 lambda: gsi.gsi_group_combine(meta(big, 8), meta(3, 2, dtype=i32)),
+                 lambda: gsi.gsi_group_combine(meta(7, big + 3), meta(3, 2, dtype=i32))):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+
+
 # ---- pins of the oracle ----
 
 
