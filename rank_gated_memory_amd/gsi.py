@@ -406,7 +406,8 @@ def _sizes(where: str, *sizes: int):
 
 
 def _rows2d(t: torch.Tensor, name: str, dtype, device, cols: int, n: int | None = None) -> int:
-    """The row stride of a [n][cols] tensor whose rows are contiguous."""
+    """The row stride of a [n][cols] tensor whose rows are contiguous; fewer than
+    two rows have none that counts."""
     shape = t.shape
     if len(shape) != 2 or shape[1] != cols or (n is not None and shape[0] != n):
         raise ValueError(f"{name} must be [{'n' if n is None else n}][{cols}], is {tuple(shape)}")
@@ -415,7 +416,7 @@ def _rows2d(t: torch.Tensor, name: str, dtype, device, cols: int, n: int | None 
     s0, s1 = t.stride()
     if s1 != 1 and cols > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return s0 if shape[0] > 1 or s0 > cols else cols
+    return s0 if shape[0] > 1 else cols
 
 
 def _ints(t: torch.Tensor, name: str, shape, device):

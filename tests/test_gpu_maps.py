@@ -167,6 +167,21 @@ def test_q4_one_token_vector_and_empty():
     assert gsi.gsi_q4_linear(w, x[None][:0]).shape == (0, 64)
 
 
+def test_one_row_of_a_matrix_with_an_odd_stride():
+    """A row sliced from rows that lie no multiple of 16 bytes apart, as x, y and base."""
+    g = gen(11)
+    w = make_q4(g, (64,), 256, 64, F32)
+    wide, out = torch.randn(3, 257, generator=g, device=DEV), torch.full((3, 67), 5.0, device=DEV)
+    x, y = wide[:1, :256], out[:1, :64]
+    assert gsi.gsi_q4_linear(w, x, y=y) is y
+    assert torch.equal(bits(y), bits(gsi.gsi_q4_linear(w, x.clone())))
+    base = torch.randn(2, 67, generator=g, device=DEV)[:1, :64]
+    want = base + y
+    assert gsi.gsi_group_combine(y, torch.zeros(1, 1, device=DEV, dtype=torch.int32), base=base, out=base) is base
+    assert torch.equal(bits(base), bits(want))
+    assert bool((out[1:] == 5).all()) and bool((out[:, 64:] == 5).all())
+
+
 # ---- grouped maps ----
 
 

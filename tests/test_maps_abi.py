@@ -236,6 +236,15 @@ def test_binding_refuses_sizes_past_32_bits():
             call()
 
 
+@pytest.mark.parametrize("rows", [0, 1])
+def test_one_row_has_no_stride(rows):
+    """The stride of a view of one row is never used, so it need not suit the library (257 columns apart here)."""
+    wide = torch.zeros(5, 257)
+    for view in (wide[2:2 + rows, :256], wide[2:2 + rows, :256].clone(), wide[None, 0, :256].expand(1, 256)[:rows]):
+        assert gsi._rows2d(view, "x", torch.float32, wide.device, 256) == 256
+    assert gsi._rows2d(wide[:2, :256], "x", torch.float32, wide.device, 256) == 257
+
+
 # ---- pins of the oracle ----
 
 
