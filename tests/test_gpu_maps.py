@@ -182,6 +182,20 @@ def test_one_row_of_a_matrix_with_an_odd_stride():
     assert bool((out[1:] == 5).all()) and bool((out[:, 64:] == 5).all())
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+def test_q4_most_rows_of_a_narrow_map(dtype):
+    """(T + 16)(d_out + 127) just below 2^32, the size up to which no call is refused."""
+    g = gen(17)
+    w = make_q4(g, (8,), 32, 32, dtype)
+    T = (2**32 - 1) // (8 + 127) - 16
+    x = torch.randn(T, 32, generator=g, device=DEV, dtype=dtype)
+    y = gsi.gsi_q4_linear(w, x)
+    at = torch.cat([torch.arange(0, T, 300007, device=DEV), torch.arange(T - 40, T, device=DEV)])
+    W, S = q4_64(w)
+    X = f64(x[at])
+    close(y[at], X @ W.T, np.abs(X) @ S.T, 32, dtype, "narrow")
+
+
 # ---- grouped maps ----
 
 
@@ -409,6 +423,88 @@ def test_grouped_many_rows_past_32_bits(kind, n, d, d_out, R):
         S = np.abs(W)
     X = f64(x[at])
     close(y[at][:, some], X @ W.T, np.abs(X) @ S.T, d, dtype, f"far tiles {kind}")
+
+
+# full tiles of 256 rows and rests of each of the four heights
+TURNS = [1300, 0, 257, 700, 64, 1, 193, 512, 130, 900, 0, 320, 15]
+
+
+@pytest.mark.parametrize("d,d_out", [(160, 8200), (416, 8200), (1048, 4104), (128, 4104)])
+def test_grouped_many_tiles_of_a_workgroup(d, d_out):
+    """bf16 tiles for several turns of every workgroup: 792 (d_out 8200) and 408
+    tiles on 256 workgroups, each turn another expert, height or column.  All of
+    y is compared, on the GPU, against products in 64 bits."""
+    g = gen(d + d_out)
+    n, R, T = len(TURNS), sum(TURNS), 1500
+    w = make_weights(g, "bf16", n, d_out, d)
+    x = torch.randn(T, d, generator=g, device=DEV).to(BF16)
+    x[0] = float("nan")  # row 0 stands in for no other row
+    offsets = to_offsets(TURNS, first=3)
+    rows = torch.randint(1, T, (R + 8,), generator=g, device=DEV, dtype=torch.int32)
+    rows[3], rows[5 + R // 2], rows[R + 2] = -1, T, 2**31 - 1
+    before = torch.full((R + 8, d_out), 7.0, device=DEV, dtype=BF16)
+    y, again = before.clone(), before.clone()
+    gsi.gsi_grouped_linear(w, x, offsets, rows, y=y)
+    gsi.gsi_grouped_linear(w, x, offsets, rows, y=again)
+    assert torch.equal(bits(y), bits(again))
+    assert bool((y[:3] == 7).all()) and bool((y[R + 3:] == 7).all())
+    at = ints(offsets)
+    for e in range(n):
+        src = rows[at[e]:at[e + 1]].long()
+        has = ((src >= 0) & (src < T))[:, None]
+        X = torch.where(has, x[src.clamp(0, T - 1)].double(), 0.0)
+        W = w[e].double()
+        ref, size = X @ W.T, X.abs() @ W.abs().T
+        # half a step of y and the fp32 sums, as in close()
+        tol = 2.0**-8 * ref.abs() * 1.001 + (1 + 2.0**-8) * (d / 16 + 64) * 2.0**-23 * size + 1e-30
+        off = (y[at[e]:at[e + 1]].double() - ref).abs()
+        assert bool((off <= tol).all()), f"expert {e}: {int((off > tol).sum())} off"
+        norm = ref.norm(dim=1)
+        rel = (off.norm(dim=1)[norm > 0] / norm[norm > 0])
+        assert rel.numel() == 0 or float(rel.max()) <= 2.0**-8 + 1e-5
+
+
+@pytest.mark.parametrize("n,d,d_out,R", [(34, 8192, 8192, 2400), (34, 131072, 768, 400)], ids=["large tiles", "small tiles"])
+def test_grouped_many_bf16_rows_past_32_bits(n, d, d_out, R):
+    """The bf16 tiles: the last expert's weights and the last rows of x and y lie
+    beyond 2^32 bytes, the rows beyond 2^31 elements."""
+    g = gen(16)
+    w = torch.zeros(n, d_out, d, device=DEV, dtype=BF16)
+    w[-1].normal_(0, d**-0.5, generator=g)
+    ld = (1 << 31) // (R - 1) // 8 * 8 + 64
+    x = torch.empty_strided((R, d), (ld, 1), device=DEV, dtype=BF16)
+    x.copy_(torch.randn(R, d, generator=g, device=DEV))
+    y = torch.empty_strided((R, d_out), (ld, 1), device=DEV, dtype=BF16)
+    gsi.gsi_grouped_linear(w, x, to_offsets([0] * (n - 1) + [R]), y=y)
+    some, at = torch.arange(0, d_out, 61, device=DEV), torch.arange(R - 1, 0, -57, device=DEV)
+    W, X = f64(w[-1][some]), f64(x[at])
+    close(y[at][:, some], X @ W.T, np.abs(X) @ np.abs(W).T, d, BF16, f"far bf16 tiles {d_out}")
+
+
+@pytest.mark.parametrize("zeros", [True, False], ids=["zeros", "eights"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("d,d_out,counts", [(96, 24, [1, 0, 2]), (1056, 264, [3, 0, 17, 1, 33]), (416, 1048, RAGGED)],
+                         ids=["few", "some", "many"])
+def test_grouped_q4_of_every_type(d, d_out, counts, dtype, group, zeros):
+    """Experts in 4 bits with bf16 and fp32 x, every group size, with zeros and without."""
+    g = gen(d + group + len(counts))
+    n, R, T = len(counts), sum(counts), 700
+    w = make_q4(g, (n, d_out), d, group, dtype, zeros=zeros)
+    x = torch.randn(T, d, generator=g, device=DEV).to(dtype)
+    x[:, d // 3] *= 30
+    x[0] = float("nan")  # row 0 stands in for no other row
+    offsets = to_offsets(counts, first=3)
+    rows = torch.randint(1, T, (R + 8,), generator=g, device=DEV, dtype=torch.int32)
+    rows[3], rows[R + 2] = -1, T
+    wide = torch.randn(R + 8, d_out + 16, generator=g, device=DEV).to(dtype)
+    before, y = wide.clone(), wide.clone()
+    gsi.gsi_grouped_linear(w, x, offsets, rows, y=y[:, 8:-8])
+    check_grouped(w, "q4", x, offsets, rows, y[:, 8:-8], before[:, 8:-8], f"q4 {dtype} {d}x{d_out} group {group}")
+    assert torch.equal(bits(y[:, :8]), bits(before[:, :8])) and torch.equal(bits(y[:, -8:]), bits(before[:, -8:]))
+    again = before.clone()
+    gsi.gsi_grouped_linear(w, x, offsets, rows, y=again[:, 8:-8])
+    assert torch.equal(bits(again), bits(y))
 
 
 @pytest.mark.parametrize("kind", ["bf16", "q4"])
