@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kStreamWaves * 64, 4) stream_kernel(MArgs a, S
   const Chunk ch = find_chunk(a, blockIdx.x / sh.strips, 16);
   if (ch.count <= 0) return;
   S s(a, lane);
-  // a workgroup's wavefronts: kStreamWaves / split blocks of weight rows, the
+  // a workgroup's wavefronts: sh.waves / sh.split blocks of weight rows, the
   // columns of each in `split` shares of whole batches
   const int side = wave / sh.split, share = wave % sh.split, sides = sh.waves / sh.split;
   const int blocks = (a.d_out + 15) / 16, groups = (blocks + sides - 1) / sides;
@@ -440,6 +440,11 @@ __global__ void __launch_bounds__(kStreamWaves * 64, 4) stream_kernel(MArgs a, S
     }
     // one output: token k / 16 and weight row k % 16 of block `b`
     const auto put = [&](int b, int k, float v) {
+      // here: the compiler would carry the addresses of every output through all
+      // blocks, in registers that the bf16 form of groups of 32 does not have (it
+      // spilled two; 5 tokens 4096 -> 50400, weights from HBM: 40.8 -> 39.9 us);
+      // the other forms keep them (bf16 without groups is 3 % faster so)
+      if constexpr (S::q4 && G == 32) asm volatile("" : "+v"(k));
       const int i = (g * sides + b) * 16 + k % 16, r = ch.row + k / 16;
       if (k / 16 >= ch.count || i >= a.d_out) return;
       if (a.rows) {

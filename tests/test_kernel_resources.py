@@ -81,3 +81,19 @@ def test_wide_maps_wait_for_their_stages(tmp_path):
         elif line.startswith((".LBB", "_Z")) or op.startswith(("s_cbranch", "s_branch")):
             loads, allowed = 0, None  # a step is straight-line code
     assert steps >= 4 * 4 + 4 * 6, steps  # four heights of bf16 tiles, two of each group size
+
+
+@pytest.mark.skipif(not os.path.exists("/opt/rocm/bin/hipcc"), reason="hipcc not installed")
+@pytest.mark.parametrize("source,pattern,count,waves", [
+    ("gsi_maps_stream.hip", r"stream_kernel", 8, 4),
+    ("gsi_maps_wide.hip", r"wide_kernel", 4, 2),
+    ("gsi_maps_wide.hip", r"small_kernel", 2, 4),
+], ids=["stream", "wide", "small"])
+def test_map_kernels_keep_their_occupancy(source, pattern, count, waves):
+    """Two workgroups of eight wavefronts of the streaming kernels on a CU (or
+    one of 16), one of the large tiles, four of the small ones; no spills."""
+    hits = {k: v for k, v in resource_usage(source).items() if re.search(pattern, k)}
+    assert len(hits) == count, sorted(hits)
+    for k, v in hits.items():
+        assert v.get("Occupancy", 0) >= waves, f"{k}: {v}"
+        assert v.get("VGPRs Spill") == 0 and v.get("ScratchSize") == 0, f"{k} spills registers: {v}"
