@@ -520,6 +520,56 @@ def test_grouped_over_thousands_of_experts(kind, R):
     check_grouped(w, kind, x, offsets, None, gsi.gsi_grouped_linear(w, x, offsets), before, f"{n} experts {kind}")
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dtype,T", [(BF16, 1), (BF16, 40), (BF16, 2560), (F32, 19)])
+def test_q4_reads_the_low_four_bits_of_a_zero(dtype, T, group):
+    g = gen(T + group)
+    w = make_q4(g, (1048,), 416, group, dtype)
+    x = torch.randn(T, 416, generator=g, device=DEV).to(dtype)
+    y = gsi.gsi_q4_linear(w, x)
+    high = w.zeros | (torch.randint(0, 16, w.zeros.shape, generator=g, device=DEV, dtype=torch.uint8) << 4)
+    assert torch.equal(bits(gsi.gsi_q4_linear(gsi.Q4(w.codes, w.scales, high, group=group), x)), bits(y))
+
+
+@pytest.mark.parametrize("kind,d_out", TILED)
+def test_many_rows_captured_and_replayed(kind, d_out):
+    """The tiles and the three launches of the ordering in one graph, on other
+    choices and values at every replay, with eager work between them."""
+    g = gen(d_out + 2)
+    n, d, T, top = 7, 160, 11000, 3
+    dtype = F32 if kind == "fp32" else BF16
+    w = make_weights(g, kind, n, d_out, d)
+    x, out = torch.empty(T, d, device=DEV, dtype=dtype), torch.empty(T, d_out, device=DEV, dtype=dtype)
+    ids = torch.zeros(T, top, device=DEV, dtype=torch.int32)
+    weights = torch.rand(T, top, generator=g, device=DEV)
+
+    def block(x, ids, out):
+        offsets, rows, pos = gsi.gsi_group_rows(ids, n)
+        y = gsi.gsi_grouped_linear(w, x, offsets, rows)
+        return gsi.gsi_group_combine(y, pos, weights, out=out)
+
+    def fill():
+        x.copy_(torch.randn(T, d, generator=g, device=DEV))
+        ids.copy_(torch.randint(-1, n, (T, top), generator=g, device=DEV))
+    fill()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        block(x, ids, out)
+    stream.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        block(x, ids, out)
+    for k in range(4):
+        fill()
+        want = block(x.clone(), ids.clone(), torch.empty_like(out))
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(bits(out), bits(want)), f"replay {k}"
+
+
 # ---- grouping and combining ----
 
 
