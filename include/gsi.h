@@ -308,8 +308,11 @@ gsi_status gsi_calibrate(const gsi_calib *c, void *ws, size_t ws_bytes, void *st
  * of 8, at most 2^24; W 16-byte aligned, stride a multiple of 16
  * bytes.  Products accumulate in fp32: codes and bf16 values multiply
  * exactly, a group's scale multiplies the group's fp32 sum, and y is
- * rounded once.  With 4-bit weights and |x| near the largest fp32 value the
- * sum 32 sum |x| of a group must itself stay finite. */
+ * rounded once.  With 4-bit weights calls of few rows sum (16 + code) x and
+ * take off (16 + zero) times the sum of x: their fp32 error goes by the size
+ * of these two (about 1e-6 of sum |w x| at most where x has one sign), and
+ * with |x| near the largest fp32 value the sum 32 sum |x| of a group must
+ * itself stay finite. */
 typedef struct gsi_weights {
   int32_t d;
   int32_t d_out;

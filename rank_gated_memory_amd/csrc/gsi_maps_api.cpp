@@ -32,27 +32,43 @@ gsi_status choose(const MArgs &a, const gsi_weights &w, hipStream_t st) {
   if (w.bits == 4) {
     // Large tiles once they beat streaming the weights for every 16 rows: as
     // many tiles as CUs, or fewer, take as long as about 9000 blocks of 16 x 16
-    // there (4096 -> 16384: 64 tokens 63 us in tiles, 39 us streamed; 128
-    // tokens 63 and 70; 512 tokens 86 and 243; 9120 -> 4608: 384 tokens 194 and
-    // 164, 512 tokens 192 and 210; 32 experts 2048 -> 2048: 1200 rows 70 and 63,
-    // 2400 rows 81 and 109).
+    // there (4096 -> 16384: 64 tokens 61 us in tiles, 31 us streamed; 160 tokens
+    // 77 and 79; 512 tokens 83 and 173; 4096 -> 4096: 512 tokens 74 and 50, 576
+    // tokens 75 and 77; 9120 -> 4608: 384 tokens 173 and 120, 640 tokens 171 and
+    // 177; 32 experts 2048 -> 2048: 1200 rows 68 and 48, 1600 rows 68 and 63,
+    // 2400 rows 69 and 86; weights called again and again).  Next to the limit
+    // the streaming kernel is up to a fifth faster on the tiles' side: 128 tokens
+    // 4096 -> 16384 61 and 51 us, 512 tokens 9120 -> 4608 172 and 153.
     const int64_t tiles = (a.R / 256 + experts) * ((a.d_out + 127) / 128);
     const int64_t blocks = (a.R / 16 + experts) * ((a.d_out + 15) / 16);
     if (!f32 && blocks >= 9000 && blocks / 9000. >= tiles / 256.) return launch_wide_q4(a, w.group, st);
     return launch_stream(a, f32 ? kQ4F32 : kQ4Bf16, w.group, st);
   }
-  // Streaming for few rows per expert (16 experts 2048 -> 2048, 8 and 12 rows
-  // each: bf16 23 and 36 us, 26 both in small tiles; fp32 51 and 65 us, 72 and
-  // 73), and as long as its blocks of 16 x 16 do not go round the chip twice:
-  // one small tile per CU or less is all latency (bf16 8 experts 4096 -> 256, 40
-  // rows each, 448 blocks: 21 us, 31 in small tiles; 4 experts 4096 -> 1024, 24
-  // rows, 640 blocks: 19 and 30 us, 40 rows, 896 blocks: 37 and 30 us).
+  // Streaming for few rows per expert, and as long as its blocks of 16 x 16 do
+  // not go round the chip twice: one small tile per CU or less is all latency.
+  // Streamed and in small tiles, on weights called again and again and in
+  // brackets from HBM:
+  //   16 bf16 experts 2048 -> 2048   8 rows each: 25 (29) and 23 (35) us
+  //                                 16 rows:      26 (30) and 24 (35)
+  //   64 bf16 experts 2048 -> 2816   8 rows each: 154 (153) and 165 (164)
+  //                                 16 rows:      161 (160) and 165 (165),
+  //                                               156 (159) in large tiles
+  //   16 fp32 experts 2048 -> 2048  12 rows each: 50 (64) and 51 (63)
+  //   bf16, 8 experts 4096 -> 256, 40 rows, 448 blocks: 16 (16) and 18 (45)
+  //         4 experts 4096 -> 1024, 24 rows, 640 blocks: 15 (16) and 28 (44)
+  //                                 40 rows, 896 blocks: 31 (32) and 30 (46)
+  //         8 experts 1024 -> 512, 33 rows, 768 blocks: 12 (12) and 8 (14)
+  //   fp32, 4 experts 4096 -> 1024, 40 rows, 896 blocks: 57 (60) and 74 (96)
+  // So the two are alike around the limits on repeated weights; on weights from
+  // HBM streaming would serve up to 16 rows of bf16 and some more blocks.
   const int64_t blocks = (a.R / 16 + experts) * ((a.d_out + 15) / 16);
   if (per <= (f32 ? 12 : 8) || blocks <= 800) return launch_stream(a, f32 ? kF32 : kBf16, 0, st);
   // Large tiles where there is at least one for every CU, or half as many full
-  // ones (64 experts 2048 -> 4096, 32 rows each: 139 us, 178 in small tiles;
-  // 16 experts 2048 -> 1024, 100 rows: 54 and 30 us; 8 experts 2048 -> 2048,
-  // 300 rows: 57 and 64 us).
+  // ones, as far as the rows and experts tell (large and small tiles: 64 experts
+  // 2048 -> 4096, 32 rows each: 197 and 248 us; 16 experts 2048 -> 1024, 100
+  // rows: 34 and 26 us; 8 experts 2048 -> 2048, 300 rows: 53 and 55 us, 512
+  // rows: 54 and 76; 256 rows each, counted as twice the tiles there are: 53 and
+  // 43; 2 experts 4096 -> 4096, 256 rows: 93 and 35).
   const int64_t tiles = (a.R / 256 + experts) * ((a.d_out + 255) / 256);
   if (!f32 && (tiles >= 256 || (tiles >= 128 && per >= 128))) return launch_wide(a, st);
   return launch_small(a, f32 ? kF32 : kBf16, st);

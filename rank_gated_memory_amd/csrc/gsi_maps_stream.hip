@@ -1,35 +1,45 @@
 // Plain linear maps with few rows per expert on gfx950 MFMA.
 //
 //   stream_kernel : the weights of an expert are read once for a chunk of up
-//                   to 16 rows.  Bound by HBM: at one token a weight is used
-//                   once, so the chunk's x is staged in LDS and the wavefronts
-//                   do nothing but stream weights into registers, a batch of
-//                   loads ahead of the products.  A wavefront owns 16 weight
-//                   rows; where there are fewer such blocks than the chip has
-//                   wavefronts, several split the columns of a block and are
-//                   joined through LDS in a fixed order.  Further chunks of an
-//                   expert read its weights again, out of the L2s.  (Chunks of
-//                   32 and 64 rows, with two blocks of weight rows per
-//                   wavefront, were slower at every number of rows: 28 and 69
-//                   us instead of 22 and 23 for 24 and 40 tokens of a 4-bit
-//                   4096 x 4096 map.)
-//                   24 tokens' 192 rows over 128 experts in 4 bits, 4096 ->
-//                   1536: 36 to 56 us for about 160 MB, by how uneven the
-//                   experts are.  8 experts' bf16 maps 2048 -> 2816 for one
-//                   token: 92 MB in 19 us.  A 4-bit 4096 x 4096 map for one
-//                   token, 8.8 MB: 6 us, most of it launch and latency; 5
-//                   tokens 4096 -> 50400, 113 MB: 32 us, where reading the
-//                   weights in this pattern alone takes 23.  With more tokens
-//                   the staging of x shows: 13 fp32 tokens 5120 -> 13824, 47
-//                   MB: 28 us.
+//                   to 16 rows.  At one token a weight is used once, so the
+//                   chunk's x is staged in LDS and the wavefronts do nothing
+//                   but stream weights into registers, a batch of loads ahead
+//                   of the products: many bytes at a few rows are bound by
+//                   HBM, few bytes by launch and latency, and from some ten
+//                   rows on the products, with the codes decoded again for
+//                   every 16 rows, count for more than the bytes.  A wavefront
+//                   owns 16 weight rows; where there are fewer such blocks
+//                   than the chip has wavefronts, several split the columns of
+//                   a block and are joined through LDS in a fixed order.
+//                   Further chunks of an expert read its weights again, out of
+//                   the L2s.  (Chunks of 32 and 64 rows, with two blocks of
+//                   weight rows per wavefront, were slower at every number of
+//                   rows when they were tried: 28 and 69 us against 22 and 23
+//                   for 24 and 40 tokens of a 4-bit 4096 x 4096 map, which
+//                   take 10.5 and 13 now.) Times on weights called again and
+//                   again, and in brackets on weights from HBM: 128 bf16
+//                   experts' maps 1024 -> 2048, a row each, 538 MB: 97 us (97:
+//                   5.5 TB/s).  8 experts' bf16 maps 2048 -> 2816 for one
+//                   token, 92 MB: 18.4 us (21.1: 4.4 TB/s).  24 tokens' 192
+//                   rows over 128 experts in 4 bits, 4096 -> 1536, 110 to 142
+//                   MB: 30 to 54 us (33 to 58), by how uneven the experts are.
+//                   A 4-bit 4096 x 4096 map for one token, 8.8 MB: 6.0 us
+//                   (6.3), most of it launch and latency; 5 tokens 4096 ->
+//                   50400, 113 MB: 30 us (33), where reading the weights in
+//                   this pattern alone took 23.  With more tokens the staging
+//                   of x shows: 13 fp32 tokens 5120 -> 13824, 47 MB: 28 us
+//                   (29.5).
 //
 // 4-bit weights.  With w = s (q - z) a group's share of y is
 //   s (sum q x - z sum x) = s (sum (16 + q) x - (16 + z) sum x).
 // 16 + q is the bf16 0x4180 | q << 3, so two codes decode with one shift and
 // one and-or, exactly, and the matrix core multiplies them with bf16 x
 // exactly; sum x of the group comes from the same instruction with ones for
-// weights.  fp32 x is split into three bf16 parts (8 + 8 + 8 bits, exact),
-// each its own product.  Only the group's fp32 sums are rounded.
+// weights.  The two sums cancel, so a group's fp32 error is one of sum (32 + q
+// + z) |x|: with x of one sign and groups of 128 up to 11 times that of a
+// plain fp32 product (1.0e-6 of sum |w x| at most, 2.2e-7 there).  fp32 x is
+// split into three bf16 parts (8 + 8 + 8 bits, exact), each its own product.
+// Only the group's fp32 sums are rounded.
 //
 // The matrix operand A holds tokens and B weight rows, so that a lane's
 // accumulators all belong to one weight row and take one scale.  Row m of A
@@ -483,15 +493,18 @@ gsi_status launch_as(const MArgs &a, hipStream_t st) {
   // until the last chunk is done: joining a split block costs about one, and
   // x that does not fit, one part after the other, two for each part.  Then a
   // workgroup may also have the CU for itself, with fewer and longer parts (16
-  // tokens through a 4-bit 16384 -> 4096 map: 64 us in parts of 1536 columns,
-  // two workgroups on a CU, and 40 us in parts of 4096, one on a CU; 300 tokens
-  // over 32 experts 4096 -> 1024: 68 and 78 us), of 8 wavefronts or of 16 (64
-  // tokens 4096 -> 16384: 37 and 33 us; 16 tokens 4096 -> 4096, whose blocks 16
-  // leave on half of the CUs: 10.3 and 11.6).
+  // tokens through a 4-bit 16384 -> 4096 map: 63 us in parts of 1536 columns,
+  // two workgroups on a CU, and 38 us in parts of 4096, one on a CU; 300 tokens
+  // over 32 experts 4096 -> 1024: 61 and 70 us), of 8 wavefronts or of 16 (64
+  // tokens 4096 -> 16384: 34 and 31 us; 48 tokens 16384 -> 4096: 53 and 41; 16
+  // tokens 4096 -> 4096, whose blocks 16 leave on half of the CUs: 10.2 and
+  // 10.4; the first map above, where 16 wavefronts would take 32 us, is one
+  // that this cost gets wrong).
   const int64_t busy = a.offsets ? std::max<int64_t>(experts, a.R / 16) : chunks;  // chunks with rows, about
   // Experts with more rows than others: more and smaller workgroups than run at
   // once even that out (100 tokens, six of 128 experts each, bf16 1024 -> 2048:
-  // 73 us with one round of workgroups, 54 with four).
+  // 63 us with one round of workgroups, 48 with two, 45 with four or eight; 24
+  // tokens, eight of 128 experts in 4 bits, 4096 -> 1536: 71, 45, 30 and 30).
   const int64_t uneven = a.offsets && a.R > a.n ? 4 : 1;
   const int tokens = a.R < 16 ? a.R : 16;
   const int unit = S::C * U, padded = (a.d + S::C - 1) / S::C * S::C, blocks = (a.d_out + 15) / 16;

@@ -152,8 +152,8 @@ __device__ __forceinline__ void landed() {
 // each 32 TM tokens x 64 weight rows.  The columns go by in stages of 32; four
 // stages lie in LDS, filled by direct loads in a stream that runs on from one
 // tile into the next.  Bound by the matrix cores and the clock they leave (one
-// 8192^3 product: 1140 TFLOP/s, MFMA busy 61 % of the cycles at 1.76 GHz).
-// 4096 tokens, four of 32 ragged experts each, 2048 -> 4096: 275 GFLOP in 330
+// 8192^3 product: 1140 to 1180 TFLOP/s, MFMA busy 61 % of the cycles at 1.76 GHz).
+// 4096 tokens, four of 32 ragged experts each, 2048 -> 4096: 275 GFLOP in 325
 // to 350 us; with as many rows for every expert 305 (before the order of the
 // tiles was tuned: two stages of 64 columns 3 % slower than four of 32, loads
 // through registers 11 %).
