@@ -375,6 +375,163 @@ gsi_status gsi_group_combine(const void *y, int64_t ldy, int32_t R, const int32_
                              int64_t ldo, int32_t T, int32_t top, int32_t d, int32_t dtype,
                              void *stream);
 
+/* ---- a key-value cache in pages, and attention of one new token over it ----
+ * What a decode step does between the map that gives q, k and v and the map
+ * that takes attention's output: rotary positions, appending to the cache,
+ * attention over it, and cutting it to a budget.
+ *
+ * The pool.  An entry (key, value and, where they are kept, its accumulated
+ * weight and its age) has a page, a key head and a slot of the page:
+ *   K, V : element e of an entry at page * page_stride + head * head_stride
+ *          + slot * slot_stride + e; K and V have the same strides
+ *   mass : [pages][heads][page] fp32, the attention weights that the entry has
+ *          been given (gsi_cache_attend adds, gsi_cache_evict goes by it), or NULL
+ *   age  : [pages][heads][page] int32, the entry's position, larger for newer
+ *          ones (gsi_cache_append writes, gsi_cache_evict goes by it), or NULL
+ * pages >= 1, page a power of two in 8..4096, heads 1..1024, d a multiple of 8
+ * in 8..256; strides of at least d, multiples of 16 bytes; K and V 16-byte
+ * aligned, mass and age 4-byte.  No two entries overlap.
+ *
+ * The tables.  Slot i of sequence s is slot i % page of the page
+ * table[s * ld + i / page].  A page number outside [0, pages) holds nothing:
+ * nothing is read from it or written to it, attention leaves its slots out.
+ * Table entries of slots that a call does not use are not read.
+ * 0 <= S < 2^24, 0 <= most, most * page <= 2^30, ld >= most.
+ *
+ * Conventions beside those at the top
+ *   - fp32 or bf16 for K, V and all rows of heads; sums, scores, softmax
+ *     statistics and weights are fp32, each result is rounded once.
+ *   - Lengths, slots and tables are read on the device; a length outside
+ *     [0, most * page] is clamped to it.
+ *   - Outputs overlap no input and no other output, but for the cases named.
+ *   - No atomics: equal calls give equal bits.
+ *   - A launch holds fewer than 2^32 threads: calls that would need more give
+ *     GSI_E_SHAPE and are cut by rows or sequences. */
+typedef struct gsi_cache {
+  int32_t pages;
+  int32_t page;    /* slots of a page                    */
+  int32_t heads;   /* key heads                          */
+  int32_t d;       /* elements of a key, and of a value  */
+  int32_t dtype;   /* gsi_dtype of K, V, q and outputs   */
+  int32_t reserved;
+  int64_t page_stride, head_stride, slot_stride;   /* elements */
+  void *K;
+  void *V;
+  float *mass;
+  int32_t *age;
+} gsi_cache;
+
+typedef struct gsi_table {
+  const int32_t *table;   /* device, S rows of `most` page numbers, `ld` apart */
+  int64_t ld;
+  int32_t S;
+  int32_t most;
+} gsi_table;
+
+/* T rows of n heads of d elements each: element e of head h of row t at
+ * t * row + h * head + e; p 16-byte aligned, strides multiples of 16 bytes and
+ * at least d (a stride over one row or one head does not count). n 1..4096. */
+typedef struct gsi_heads {
+  void *p;
+  int64_t row, head;   /* elements */
+  int32_t n;
+  int32_t reserved;
+} gsi_heads;
+
+/* Rotary positions.  Elements start .. start + d - 1 of a head are d / 2
+ * pairs; at position p pair i turns by the angle p * freq[i] and is multiplied
+ * by `amplitude`:
+ *   y0 = amplitude (x0 cos - x1 sin),  y1 = amplitude (x1 cos + x0 sin).
+ * The other elements stay as they are.  Angles are formed and reduced to one
+ * turn in 64 bits, the rest is fp32.  d even, at least 2, start >= 0,
+ * start + d at most the head's size.  (Frequencies for longer contexts are
+ * the caller's; positions may be negative, and with amplitude 1 the rotation
+ * by -p undoes that by p and is its transpose.) */
+typedef enum {
+  GSI_ROTARY_PAIRS = 0,    /* pair i: elements 2 i and 2 i + 1 */
+  GSI_ROTARY_HALVES = 1,   /* pair i: elements i and i + d / 2 */
+} gsi_rotary_layout;
+
+typedef struct gsi_rotation {
+  int32_t d;
+  int32_t start;
+  int32_t layout;   /* gsi_rotary_layout */
+  float amplitude;
+  const double *freq;   /* device, [d / 2] radians per position */
+} gsi_rotation;
+
+/* y = the rotated x: T rows of x->n heads of d elements (a multiple of 8, at
+ * most 256) in `dtype`; positions [T] int32 or int64 (pos_bytes 4 or 8).  y may
+ * be x itself (same address and strides).  T == 0 is a no-op. */
+gsi_status gsi_rotary(const gsi_rotation *r, const gsi_heads *x, const gsi_heads *y, int32_t T,
+                      int32_t d, int32_t dtype, const void *positions, int32_t pos_bytes,
+                      void *stream);
+
+/* Write T new entries: the (rotated) keys k and the values v, each of
+ * cache->heads heads, into slot slots[t] of sequence seq[t]; their mass becomes
+ * 0 and their age the position, clamped to int32 (without positions: the slot).
+ *   seq       : [T] int32, or NULL for t
+ *   slots     : [T] int32; a row whose sequence is outside [0, S), whose slot
+ *               is outside [0, most * page) or whose page is none writes nothing
+ *               into the cache; no two rows name one slot
+ *   r         : the rotation of keys and queries, or NULL for none
+ *   positions : [T] as in gsi_rotary; may be NULL without r
+ *   q, q_out  : queries rotated beside them, every row, as by gsi_rotary (q_out
+ *               may be q), or both NULL
+ * T == 0 is a no-op. */
+gsi_status gsi_cache_append(const gsi_cache *cache, const gsi_table *table, const int32_t *seq,
+                            const int32_t *slots, const gsi_heads *k, const gsi_heads *v, int32_t T,
+                            const gsi_rotation *r, const void *positions, int32_t pos_bytes,
+                            const gsi_heads *q, const gsi_heads *q_out, void *stream);
+
+/* Bytes of workspace that gsi_cache_attend needs for q_heads heads (0 for none,
+ * or for invalid arguments).  Unlike gsi_linear's it needs no initial contents
+ * and holds nothing between calls; calls that may overlap need their own. */
+size_t gsi_cache_attend_workspace(const gsi_cache *cache, const gsi_table *table, int32_t q_heads,
+                                  int32_t accumulate);
+
+/* Attention of one token of each of the S sequences over the sequence's slots
+ * [first, n), n = lengths[s] and first = max(0, n - window), or 0 where window
+ * is 0.  Query head h goes with key head h / (q->n / cache->heads):
+ *   score_i = scale q . k_i,  weight_i = exp(score_i) / sum exp(score),
+ *   out = sum weight_i v_i,   lse = log sum exp(score_i)
+ *   lengths    : [S] int32
+ *   q, out     : S rows of q->n heads, q->n a multiple of cache->heads
+ *   lse        : [S][q->n] fp32, or NULL
+ *   accumulate : not 0: mass of every slot in [first, n) += the sum of its
+ *                weights over the query heads of its key head; sequences then
+ *                share no page
+ * A sequence without slots (or with no page that there is, or whose scores all
+ * are -inf) gives zeros, and lse -inf.  What lies behind the n slots is never
+ * part of a result, whatever it holds.  Needs `ws` of at least
+ * gsi_cache_attend_workspace() bytes, 16-byte aligned. */
+gsi_status gsi_cache_attend(const gsi_cache *cache, const gsi_table *table, const int32_t *lengths,
+                            const gsi_heads *q, const gsi_heads *out, float scale, int32_t window,
+                            int32_t accumulate, float *lse, void *ws, size_t ws_bytes,
+                            void *stream);
+
+/* Cut every sequence of more than `budget` entries to `budget`, for each key
+ * head by itself: the `recent` entries of the largest age (without ages: of the
+ * highest slots) stay, and of the others those of the largest mass; ties go to
+ * the lowest slot, a mass that is NaN and an entry of no page count as the
+ * least.  Entries in slots below the budget stay where they are; the others
+ * that stay fill, in the order of their slots, the slots below the budget that
+ * were given up.  (Attention does not go by the order of slots.)
+ *   budget, recent : 1 <= budget <= 2^20, 0 <= recent <= budget
+ *   to          : NULL to move entries in place (only those that change slots;
+ *                 sequences then share no page), or the table of the S
+ *                 sequences in other pages of the same pool, into which all
+ *                 that stay are copied, from sequences of any length; none of
+ *                 its pages is a page of `table` or is named twice;
+ *                 to->most * page >= budget
+ *   lengths_out : [S] int32, min(length, budget), or NULL; not `lengths` itself
+ *   from        : [S][heads][budget] int32, for each slot the slot that its
+ *                 entry came from, -1 behind the last
+ * Needs cache->mass; table->most * page at most 2^19. */
+gsi_status gsi_cache_evict(const gsi_cache *cache, const gsi_table *table, const int32_t *lengths,
+                           int32_t budget, int32_t recent, const gsi_table *to,
+                           int32_t *lengths_out, int32_t *from, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

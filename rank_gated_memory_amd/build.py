@@ -11,7 +11,9 @@ SOURCES = [os.path.join(PKG, "csrc", "gsi_api.cpp"), os.path.join(PKG, "csrc", "
            os.path.join(PKG, "csrc", "gsi_batched.hip"), os.path.join(PKG, "csrc", "gsi_calib.hip"),
            os.path.join(PKG, "csrc", "gsi_noalloc.hip"), os.path.join(PKG, "csrc", "gsi_maps_api.cpp"),
            os.path.join(PKG, "csrc", "gsi_maps_stream.hip"), os.path.join(PKG, "csrc", "gsi_maps_wide.hip"),
-           os.path.join(PKG, "csrc", "gsi_rows.hip")]
+           os.path.join(PKG, "csrc", "gsi_rows.hip"), os.path.join(PKG, "csrc", "gsi_cache_api.cpp"),
+           os.path.join(PKG, "csrc", "gsi_rotary.hip"), os.path.join(PKG, "csrc", "gsi_attend.hip"),
+           os.path.join(PKG, "csrc", "gsi_evict.hip")]
 OUT = os.path.join(PKG, "libgsi.so")
 
 COMMON = [

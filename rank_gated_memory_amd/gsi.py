@@ -52,6 +52,26 @@ class GsiWeightsStruct(ctypes.Structure):
                 ("W", c_void_p), ("scales", c_void_p), ("zeros", c_void_p)]
 
 
+class GsiCacheStruct(ctypes.Structure):
+    _fields_ = [("pages", c_int32), ("page", c_int32), ("heads", c_int32), ("d", c_int32),
+                ("dtype", c_int32), ("reserved", c_int32), ("page_stride", c_int64),
+                ("head_stride", c_int64), ("slot_stride", c_int64), ("K", c_void_p), ("V", c_void_p),
+                ("mass", c_void_p), ("age", c_void_p)]
+
+
+class GsiTableStruct(ctypes.Structure):
+    _fields_ = [("table", c_void_p), ("ld", c_int64), ("S", c_int32), ("most", c_int32)]
+
+
+class GsiHeadsStruct(ctypes.Structure):
+    _fields_ = [("p", c_void_p), ("row", c_int64), ("head", c_int64), ("n", c_int32), ("reserved", c_int32)]
+
+
+class GsiRotationStruct(ctypes.Structure):
+    _fields_ = [("d", c_int32), ("start", c_int32), ("layout", c_int32), ("amplitude", c_float),
+                ("freq", c_void_p)]
+
+
 _lib = None
 
 
@@ -112,6 +132,20 @@ def lib() -> ctypes.CDLL:
         L.gsi_group_combine.restype = c_int32
         L.gsi_group_combine.argtypes = [c_void_p, c_int64, c_int32, c_void_p, c_void_p, c_void_p, c_int64,
                                         c_void_p, c_int64, c_int32, c_int32, c_int32, c_int32, c_void_p]
+        rotation, heads = POINTER(GsiRotationStruct), POINTER(GsiHeadsStruct)
+        cache, table = POINTER(GsiCacheStruct), POINTER(GsiTableStruct)
+        L.gsi_rotary.restype = c_int32
+        L.gsi_rotary.argtypes = [rotation, heads, heads, c_int32, c_int32, c_int32, c_void_p, c_int32, c_void_p]
+        L.gsi_cache_append.restype = c_int32
+        L.gsi_cache_append.argtypes = [cache, table, c_void_p, c_void_p, heads, heads, c_int32, rotation, c_void_p,
+                                       c_int32, heads, heads, c_void_p]
+        L.gsi_cache_attend_workspace.restype = c_size_t
+        L.gsi_cache_attend_workspace.argtypes = [cache, table, c_int32, c_int32]
+        L.gsi_cache_attend.restype = c_int32
+        L.gsi_cache_attend.argtypes = [cache, table, c_void_p, heads, heads, c_float, c_int32, c_int32, c_void_p,
+                                       c_void_p, c_size_t, c_void_p]
+        L.gsi_cache_evict.restype = c_int32
+        L.gsi_cache_evict.argtypes = [cache, table, c_void_p, c_int32, c_int32, table, c_void_p, c_void_p, c_void_p]
         _lib = L
     return _lib
 
@@ -555,3 +589,250 @@ def gsi_group_combine(y: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor 
     _call("gsi_group_combine", lib().gsi_group_combine, dev, stream, y.data_ptr(), ldy, y.shape[0], pos.data_ptr(),
           _ptr(weights), _ptr(base), ldb, out.data_ptr(), ldo, T, top, d, _dtype_code(y))
     return out
+
+
+# ---- a key-value cache in pages: rotary positions, appending, attention, eviction ----
+
+_LAYOUTS = {"pairs": 0, "halves": 1}
+
+
+def rotary_freqs(d: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                 original: int = 0, low: float = 1.0, high: float = 32.0) -> torch.Tensor:
+    """Radians per position of the d / 2 pairs, f_i = base^(-2 i / d), in 64 bits;
+    for contexts `factor` times as long as the weights were made for:
+
+    scaling "linear" : f_i / factor, positions pressed together
+            "base"   : the base times factor^(d / (d - 2)), so that the slowest
+                       pair alone goes `factor` times slower (d > 2)
+            "bands"  : pairs that turn at least `high` times within `original`
+                       positions as they are, those that turn at most `low`
+                       times `factor` times slower, in between in between
+                       (usually with an amplitude of 0.1 ln(factor) + 1)"""
+    if d < 2 or d % 2:
+        raise ValueError(f"d must be even and at least 2, is {d}")
+    if scaling not in (None, "linear", "base", "bands"):
+        raise ValueError(f"scaling must be linear, base or bands, is {scaling!r}")
+    if not factor > 0 or not base > 0:
+        raise ValueError("base and factor must be positive")
+    if scaling == "base":
+        if d == 2:
+            raise ValueError("scaling of the base needs d > 2")
+        base = base * factor ** (d / (d - 2))
+    f = float(base) ** (-torch.arange(0, d, 2, dtype=torch.float64) / d)
+    if scaling == "linear":
+        return f / factor
+    if scaling == "bands":
+        if original < 1 or not low < high:
+            raise ValueError("scaling by bands needs original >= 1 and low < high")
+        turns = original * f / (2.0 * torch.pi)
+        keep = ((turns - low) / (high - low)).clamp(0.0, 1.0)
+        return f * (keep + (1.0 - keep) / factor)
+    return f
+
+
+class Rotary:
+    """Rotary positions: the frequencies of d / 2 pairs (radians per position, as
+    rotary_freqs gives them), their layout in a head ("pairs": elements 2 i and
+    2 i + 1; "halves": i and i + d / 2, from element `start` on) and the factor
+    of the turned elements.  Elements outside stay as they are."""
+
+    def __init__(self, freqs: torch.Tensor, layout: str = "halves", start: int = 0, amplitude: float = 1.0,
+                 device=None):
+        if layout not in _LAYOUTS:
+            raise ValueError(f"layout must be pairs or halves, is {layout!r}")
+        if freqs.dim() != 1 or freqs.numel() < 1:
+            raise ValueError("freqs must hold a frequency for each pair")
+        self.freqs = freqs.to(device=device, dtype=torch.float64).contiguous()
+        self.d, self.layout, self.start, self.amplitude = 2 * freqs.numel(), layout, int(start), float(amplitude)
+        self.device = self.freqs.device
+        _sizes("Rotary", self.d, abs(self.start))
+        self.struct = GsiRotationStruct(self.d, self.start, _LAYOUTS[layout], self.amplitude, _ptr(self.freqs))
+
+
+class Cache:
+    """A pool of pages of keys and values, K and V [pages][heads][page][d] with
+    the elements of an entry contiguous and the same strides (a pool stored as
+    [pages][page][heads][d] is passed as its transpose(1, 2)); mass fp32 and age
+    int32 [pages][heads][page], contiguous, or None.  The tensors are used where
+    they lie and must stay alive as long as this."""
+
+    def __init__(self, K: torch.Tensor, V: torch.Tensor, mass: torch.Tensor | None = None,
+                 age: torch.Tensor | None = None):
+        if K.dim() != 4 or K.shape != V.shape:
+            raise ValueError(f"K and V must be [pages][heads][page][d], are {tuple(K.shape)} and {tuple(V.shape)}")
+        if K.dtype != V.dtype or K.device != V.device:
+            raise ValueError("K and V must share a dtype and a device")
+        self.K, self.V, self.mass, self.age = K, V, mass, age
+        self.pages, self.heads, self.page, self.d = K.shape
+        _sizes("Cache", *K.shape)
+        self.dtype, self.device = K.dtype, K.device
+        for t, name, dtype in ((mass, "mass", torch.float32), (age, "age", torch.int32)):
+            if t is not None and (t.shape != K.shape[:3] or t.dtype != dtype or t.device != K.device
+                                  or not t.is_contiguous()):
+                raise ValueError(f"{name} must be contiguous {dtype} {tuple(K.shape[:3])} on {K.device}")
+        strides = []  # those of a single page, head or slot do not count
+        for n, k, v in zip(K.shape, K.stride(), V.stride()):
+            if n > 1 and k != v:
+                raise ValueError("K and V must have the same strides")
+            strides.append(k if n > 1 else self.d)
+        if K.stride(3) != 1 or V.stride(3) != 1:
+            raise ValueError("the elements of an entry must be contiguous")
+        self.struct = GsiCacheStruct(self.pages, self.page, self.heads, self.d, _dtype_code(K), 0, *strides[:3],
+                                     _ptr(K), _ptr(V), _ptr(mass), _ptr(age))
+
+
+def _heads(t: torch.Tensor, name: str, dtype, device, d: int, T: int | None = None, n: int | None = None):
+    """A [T][n][d] tensor whose heads are contiguous."""
+    if t.dim() != 3 or t.shape[2] != d or (T is not None and t.shape[0] != T) or (n is not None and t.shape[1] != n):
+        raise ValueError(f"{name} must be [{'T' if T is None else T}][{'heads' if n is None else n}][{d}], "
+                         f"is {tuple(t.shape)}")
+    if t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} on {device}, is {t.dtype} on {t.device}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    return GsiHeadsStruct(t.data_ptr(), s0, s1, t.shape[1], 0)
+
+
+def _table(t: torch.Tensor, name: str, device, S: int | None = None):
+    """Page numbers [S][most], int32, rows contiguous."""
+    if t.dim() != 2 or t.dtype is not torch.int32 or t.device != device or (S is not None and t.shape[0] != S):
+        raise ValueError(f"{name} must be int32 [{'S' if S is None else S}][most] on {device}, "
+                         f"is {t.dtype} {tuple(t.shape)} on {t.device}")
+    rows, most = t.shape
+    _sizes(name, rows, most)
+    if most > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the page numbers of a sequence must be contiguous")
+    return GsiTableStruct(t.data_ptr(), t.stride(0) if rows > 1 else most, rows, most)
+
+
+def _positions(t: torch.Tensor, T: int, device):
+    if t.dtype not in (torch.int32, torch.int64) or t.device != device or t.shape != (T,) or not t.is_contiguous():
+        raise ValueError(f"positions must be contiguous int32 or int64 ({T},) on {device}, "
+                         f"is {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def gsi_rotary(r: Rotary, x: torch.Tensor, positions: torch.Tensor, y: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """y = x [T][heads][d] with every head turned by its token's position
+    ([T], int32 or int64, may be negative); y may be x."""
+    if x.dim() != 3:
+        raise ValueError(f"x must be [T][heads][d], is {tuple(x.shape)}")
+    T, n, d = x.shape
+    dtype, dev = x.dtype, x.device
+    _sizes("gsi_rotary", T, n, d)
+    hx = _heads(x, "x", dtype, dev, d)
+    _positions(positions, T, dev)
+    if r.device != dev:
+        raise ValueError(f"the frequencies must be on {dev}, are on {r.device}")
+    if y is None:
+        y = _empty((T, n, d), dtype, dev, stream)
+    _call("gsi_rotary", lib().gsi_rotary, dev, stream, r.struct, hx, _heads(y, "y", dtype, dev, d, T, n), T, d,
+          _dtype_code(x), positions.data_ptr(), positions.element_size())
+    return y
+
+
+def gsi_cache_append(c: Cache, table: torch.Tensor, slots: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     seq: torch.Tensor | None = None, rotary: Rotary | None = None,
+                     positions: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                     q_out: torch.Tensor | None = None, stream=None):
+    """Write the keys k and values v [T][heads][d] into slot slots[t] of sequence
+    seq[t] (None: t) of the table [S][most]; keys, and queries q [T][heads'][d],
+    are turned by `rotary` at `positions`.  Rows whose slot has no page write
+    nothing.  Returns the turned queries (q_out, which may be q), or None."""
+    dtype, dev, d = c.dtype, c.device, c.d
+    T = k.shape[0]
+    _sizes("gsi_cache_append", T)
+    hk, hv = _heads(k, "k", dtype, dev, d, None, c.heads), _heads(v, "v", dtype, dev, d, T, c.heads)
+    pages = _table(table, "table", dev)
+    _ints(slots, "slots", (T,), dev)
+    if seq is not None:
+        _ints(seq, "seq", (T,), dev)
+    if positions is not None:
+        _positions(positions, T, dev)
+    if rotary is not None and rotary.device != dev:
+        raise ValueError(f"the frequencies must be on {dev}, are on {rotary.device}")
+    hq = ho = None
+    if q is not None:
+        hq = _heads(q, "q", dtype, dev, d, T)
+        _sizes("gsi_cache_append", q.shape[1])
+        if q_out is None:
+            q_out = _empty(q.shape, dtype, dev, stream)
+        ho = _heads(q_out, "q_out", dtype, dev, d, T, q.shape[1])
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    _call("gsi_cache_append", lib().gsi_cache_append, dev, stream, c.struct, pages, _ptr(seq), slots.data_ptr(), hk, hv,
+          T, None if rotary is None else rotary.struct, _ptr(positions),
+          4 if positions is None else positions.element_size(), hq, ho)
+    return q_out
+
+
+def gsi_cache_attend_workspace(c: Cache, table: torch.Tensor, q_heads: int, accumulate: bool = False) -> int:
+    return int(lib().gsi_cache_attend_workspace(c.struct, _table(table, "table", c.device), int(q_heads),
+                                                int(accumulate)))
+
+
+def gsi_cache_attend(c: Cache, table: torch.Tensor, lengths: torch.Tensor, q: torch.Tensor,
+                     scale: float | None = None, window: int = 0, accumulate: bool = False,
+                     out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                     ws: torch.Tensor | None = None, stream=None):
+    """Attention of one token q [S][q heads][d] of each sequence over the first
+    lengths[s] slots of its pages, or the last `window` of them: (out like q,
+    lse [S][q heads] fp32).  scale None is d^-0.5.  accumulate adds each slot's
+    weights to the cache's mass.  ws: device memory of
+    gsi_cache_attend_workspace() bytes with any contents."""
+    dtype, dev, d = c.dtype, c.device, c.d
+    hq = _heads(q, "q", dtype, dev, d)
+    S, n = q.shape[:2]
+    _sizes("gsi_cache_attend", S, n, window)
+    pages = _table(table, "table", dev, S)
+    _ints(lengths, "lengths", (S,), dev)
+    if accumulate and c.mass is None:
+        raise ValueError("accumulate needs a cache with mass")
+    if out is None:
+        out = _empty((S, n, d), dtype, dev, stream)
+    ho = _heads(out, "out", dtype, dev, d, S, n)
+    if lse is None:
+        lse = _empty((S, n), torch.float32, dev, stream)
+    elif lse.dtype is not torch.float32 or lse.device != dev or lse.shape != (S, n) or not lse.is_contiguous():
+        raise ValueError(f"lse must be contiguous fp32 ({S}, {n}) on {dev}")
+    if ws is None:
+        need = int(lib().gsi_cache_attend_workspace(c.struct, pages, n, int(accumulate)))
+        if need:
+            ws = _empty(need, torch.uint8, dev, stream)
+    elif ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous on {dev}")
+    _call("gsi_cache_attend", lib().gsi_cache_attend, dev, stream, c.struct, pages, lengths.data_ptr(), hq, ho,
+          d**-0.5 if scale is None else float(scale), int(window), int(accumulate), lse.data_ptr(), _ptr(ws),
+          0 if ws is None else ws.numel() * ws.element_size())
+    return out, lse
+
+
+def gsi_cache_evict(c: Cache, table: torch.Tensor, lengths: torch.Tensor, budget: int, recent: int = 0,
+                    to: torch.Tensor | None = None, lengths_out: torch.Tensor | None = None,
+                    moved: torch.Tensor | None = None, stream=None):
+    """Cut every sequence of more than `budget` entries to it: each key head keeps
+    its `recent` newest entries and those of the largest mass, in place or, with
+    `to` [S][most'], copied into other pages of the pool.  Returns (lengths_out
+    [S], moved [S][heads][budget]: the slot each slot's entry came from, or -1)."""
+    dev = c.device
+    pages = _table(table, "table", dev)
+    S = table.shape[0]
+    _sizes("gsi_cache_evict", budget, recent)
+    _ints(lengths, "lengths", (S,), dev)
+    if c.mass is None:
+        raise ValueError("eviction needs a cache with mass")
+    if budget < 1:
+        raise ValueError(f"budget must be at least 1, is {budget}")
+    target = None if to is None else _table(to, "to", dev, S)
+    if lengths_out is None:
+        lengths_out = _empty(S, torch.int32, dev, stream)
+    else:
+        _ints(lengths_out, "lengths_out", (S,), dev)
+    if moved is None:
+        moved = _empty((S, c.heads, budget), torch.int32, dev, stream)
+    else:
+        _ints(moved, "moved", (S, c.heads, budget), dev)
+    _call("gsi_cache_evict", lib().gsi_cache_evict, dev, stream, c.struct, pages, lengths.data_ptr(), int(budget),
+          int(recent), target, lengths_out.data_ptr(), moved.data_ptr())
+    return lengths_out, moved
