@@ -389,8 +389,8 @@ gsi_status gsi_group_combine(const void *y, int64_t ldy, int32_t R, const int32_
  *   age  : [pages][heads][page] int32, the entry's position, larger for newer
  *          ones (gsi_cache_append writes, gsi_cache_evict goes by it), or NULL
  * pages >= 1, page a power of two in 8..4096, heads 1..1024, d a multiple of 8
- * in 8..256; strides of at least d, multiples of 16 bytes; K and V 16-byte
- * aligned, mass and age 4-byte.  No two entries overlap.
+ * in 8..256; strides of at least d, multiples of 16 bytes, slot_stride below
+ * 2^24; K and V 16-byte aligned, mass and age 4-byte.  No two entries overlap.
  *
  * The tables.  Slot i of sequence s is slot i % page of the page
  * table[s * ld + i / page].  A page number outside [0, pages) holds nothing:

@@ -18,7 +18,7 @@ gsi_status check_cache(const gsi_cache *c) {
       c->d < 8 || c->d > 256 || c->d % 8)
     return GSI_E_SHAPE;
   if (!stride_ok(c->page_stride, c->pages, c->d) || !stride_ok(c->head_stride, c->heads, c->d) ||
-      !stride_ok(c->slot_stride, c->page, c->d))
+      !stride_ok(c->slot_stride, c->page, c->d) || c->slot_stride >= (1 << 24))
     return GSI_E_SHAPE;
   if (!c->K || !c->V) return GSI_E_NULL;
   const int vec = 16 / size_of(c->dtype);

@@ -65,7 +65,7 @@ BAD_CACHES = [
     (dict(page=8192), E_SHAPE), (dict(heads=0), E_SHAPE), (dict(heads=1025), E_SHAPE), (dict(d=0), E_SHAPE),
     (dict(d=12), E_SHAPE), (dict(d=264), E_SHAPE), (dict(dtype=2), E_DTYPE), (dict(ss=56), E_SHAPE), (dict(hs=56), E_SHAPE),
     (dict(ps=0), E_SHAPE), (dict(ps=-2048), E_SHAPE), (dict(ps=1 << 60), E_SHAPE), (dict(hs=1 << 60), E_SHAPE),
-    (dict(ss=1 << 60), E_SHAPE), (dict(K=None), E_NULL), (dict(V=None), E_NULL), (dict(K=FAKE + 8), E_ALIGN),
+    (dict(ss=1 << 60), E_SHAPE), (dict(ss=1 << 24), E_SHAPE), (dict(K=None), E_NULL), (dict(V=None), E_NULL), (dict(K=FAKE + 8), E_ALIGN),
     (dict(V=FAKE + 2), E_ALIGN), (dict(ss=68), E_ALIGN), (dict(hs=1028), E_ALIGN), (dict(ps=4100), E_ALIGN),
     (dict(mass=FAKE + 2), E_ALIGN), (dict(age=FAKE + 1), E_ALIGN),
 ]

@@ -277,11 +277,13 @@ def check_attend(c, table, lengths, q, scale=None, window=0, accumulate=False, w
 
 
 @DTYPES
-@pytest.mark.parametrize("d", [8, 24, 40, 64, 72, 80, 96, 104, 128, 136, 160, 192, 200, 256])
-def test_attend_head_sizes(d, dtype):
+@pytest.mark.parametrize("page", [8, 16, 32])
+@pytest.mark.parametrize("d", [8, 24, 32, 40, 64, 72, 80, 96, 104, 128, 136, 160, 192, 200, 248, 256])
+def test_attend_head_sizes(d, page, dtype):
+    """Every size of a head in units of 32, in pages shorter and longer than a step."""
     g = gen(d)
-    lengths = torch.tensor([1, 33, 0, 200], device=DEV, dtype=torch.int32)
-    c, table = make_pool(g, 4, lengths.tolist(), 2, 16, d, dtype)
+    lengths = torch.tensor([1, 33, 0, 700], device=DEV, dtype=torch.int32)
+    c, table = make_pool(g, 4, lengths.tolist(), 2, page, d, dtype)
     q = 2 * torch.randn(4, 6, d, generator=g, device=DEV).to(dtype)
     check_attend(c, table, lengths, q, accumulate=True, what=f"d={d}")
 
