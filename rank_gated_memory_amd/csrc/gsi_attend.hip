@@ -1,16 +1,19 @@
 // Attention of one new token of every sequence over the paged cache on gfx950
 // MFMA (gsi_cache_attend).
 //
-//   attend_kernel : the slots of a sequence and key head are cut into pieces, a
-//                   workgroup each; its four wavefronts take the piece's steps
-//                   of 32 slots (bf16; 16 in fp32) in turn.  A step's keys and
-//                   values are read once, straight into the registers that the
-//                   matrix instructions take them from, for up to 16 query
-//                   heads of the key head.  One pass with the running maximum
-//                   and sum of the softmax; the wavefronts are joined through
-//                   LDS, pieces through the workspace.
-//   join_kernel   : the pieces of a row, and the weights added to the mass from
-//                   the scores that attend_kernel has left in the workspace.
+//   attend_kernel : the slots of a sequence, key head and up to 16 query heads of
+//                   it (a row) are counted in units, four steps of 32 slots
+//                   (bf16; 16 in fp32), one for each wavefront of a workgroup.
+//                   All rows' units, one after the other, are dealt to as many
+//                   workgroups as the chip holds at once in equal shares, from
+//                   the lengths as they are: no workgroup is idle however the
+//                   lengths differ.  A step's keys and values are read once,
+//                   straight into the registers that the matrix instructions
+//                   take them from.  One pass with the running maximum and sum
+//                   of the softmax; wavefronts are joined through LDS.
+//   join_kernel   : rows that a share's end cuts, from the workspace.
+//   mass_kernel   : the weights added to the mass, from the scores that
+//                   attend_kernel has left in the workspace.
 //
 // The products.  S^T = K Q^T has slots as rows and query heads as columns, so
 // accumulator i of a lane belongs to head l % 16, and the rows of K's tiles are
@@ -42,37 +45,117 @@ typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kMostPieces = 256;
 
-// How a launch splits its work, and its workspace.
+// How a launch splits its work, and its workspace.  A workgroup leaves at most
+// two rows unfinished: 2 b for one that an earlier workgroup has begun, 2 b + 1
+// for one that it begins.
 struct Plan {
-  int pieces;   // of a row at most
-  int least;    // steps of a piece at least
-  int tiles;    // of 16 query heads of a key head
-  int row;      // scores of a row
-  float *stats;    // [S * heads][pieces]: maximum (times log2 e) and sum
-  float *partial;  // [S * heads][pieces][d], sums at that maximum
-  float *scores;   // [S * heads][row], times log2 e
+  int tiles;   // rows of a key head
+  int shares;  // workgroups
+  int scores_row;
+  float *stats;    // [2 shares][16]: maximum (times log2 e) and sum
+  float *partial;  // [2 shares][16][d], sums at that maximum
+  float *level;    // [S * heads]: log2 of the sum of all weights, infinity for none
+  float *scores;   // [S * heads][scores_row], times log2 e
 };
 
 template <typename E>
 constexpr int kStep = sizeof(E) == 2 ? 32 : 16;
 
-// The steps of a sequence and its pieces.
+// The slots [first, n) of a sequence in steps [lo, lo + steps), and in units.
 struct Span {
-  int n, first, lo, steps, per, pieces;  // slots [first, n); steps [lo, lo + steps), `per` a piece
+  int n, first, lo, steps, units;
 };
 
 template <typename E>
-__device__ __forceinline__ Span span_of(const AttendArgs &a, const Plan &p, int s) {
+__device__ __forceinline__ Span span_of(const AttendArgs &a, int n) {
   Span r;
-  r.n = clamped_length(a.c, a.lengths, s);
-  r.first = a.window > 0 ? max(0, r.n - a.window) : 0;
+  r.n = n;
+  r.first = a.window > 0 ? max(0, n - a.window) : 0;
   r.lo = r.first / kStep<E>;
-  r.steps = (r.n + kStep<E> - 1) / kStep<E> - r.lo;
-  r.per = max(p.least, (r.steps + p.pieces - 1) / p.pieces);
-  r.pieces = (r.steps + r.per - 1) / r.per;
+  r.steps = (n + kStep<E> - 1) / kStep<E> - r.lo;
+  r.units = max(1, (r.steps + kWaves - 1) / kWaves);  // no slots: a unit that writes zeros
   return r;
+}
+
+// Sums over the lanes up to and with this one, in registers (a row's lanes by
+// shifts, then the rows' last lanes to the rows behind).
+__device__ __forceinline__ int sums_to(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr 1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast 15, rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast 31, rows 2 and 3
+  return v;
+}
+
+// A sequence, its length, and the things of those before it.
+struct Sequence {
+  int s, n, before;
+};
+
+// The sequences one after the other, count(n) things each for n slots: all
+// things, and where a thing or a sequence is.  By every wavefront; the lengths
+// of the first 64 sequences are read once.
+template <typename Count>
+struct Counted {
+  const AttendArgs &a;
+  const Count &count;
+  int length, first, first_to, sum;
+
+  __device__ __forceinline__ Counted(const AttendArgs &args, const Count &c) : a(args), count(c) {
+    const int lane = threadIdx.x & 63, S = a.c.S;
+    length = clamped_length(a.c, a.lengths, min(lane, S - 1));
+    first = lane < S ? count(length) : 0;
+    first_to = sums_to(first);
+    int more = 0;
+    for (int s = lane + 64; s < S; s += 64) more += count(clamped_length(a.c, a.lengths, s));
+    sum = __builtin_amdgcn_readlane(first_to, 63);
+    if (S > 64) sum += __builtin_amdgcn_readlane(sums_to(more), 63);
+  }
+  // the first sequence that `is` holds for, of its number and the things up to and with it
+  template <typename Is>
+  __device__ __forceinline__ Sequence search(const Is &is) const {
+    const int lane = threadIdx.x & 63, S = a.c.S;
+    int run = 0;
+    for (int s0 = 0; s0 < S; s0 += 64) {
+      const int n = s0 == 0 ? length : clamped_length(a.c, a.lengths, min(s0 + lane, S - 1));
+      const int mine = s0 == 0 ? first : s0 + lane < S ? count(n) : 0;
+      const int incl = s0 == 0 ? first_to : sums_to(mine);
+      const uint64_t over = __ballot(is(s0 + lane, run + incl));
+      if (over) {
+        const int l = __ffsll((unsigned long long)over) - 1;
+        return {s0 + l, __builtin_amdgcn_readlane(n, l), run + __builtin_amdgcn_readlane(incl - mine, l)};
+      }
+      run += __builtin_amdgcn_readlane(incl, 63);
+    }
+    return {S - 1, 0, run};
+  }
+  __device__ __forceinline__ Sequence of_thing(int v) const {
+    return search([&](int, int to) { return to > v; });
+  }
+  __device__ __forceinline__ Sequence number(int s) const {
+    return search([&](int i, int) { return i == s; });
+  }
+};
+
+// A quotient of wave-uniform numbers, in 32 bits where they are: a division of
+// 64 bits takes a good part of a microsecond.
+__device__ __forceinline__ int64_t over(int64_t n, int64_t by) {
+  return (uint64_t)(n | by) >> 32 ? n / by : (int64_t)((uint32_t)n / (uint32_t)by);
+}
+
+// Shares of `all` units: share b begins at unit b all / shares.
+struct Shares {
+  int64_t all;
+  int of;
+  __device__ __forceinline__ int64_t begin(int b) const { return over(b * all, of); }
+  __device__ __forceinline__ int owner(int64_t unit) const { return (int)over((unit + 1) * of - 1, all); }
+};
+__device__ __forceinline__ Shares shares_of(const AttendArgs &a, const Plan &p, int units) {
+  const int64_t all = (int64_t)units * (a.c.heads * p.tiles);
+  return {all, (int)min((int64_t)p.shares, all)};
 }
 
 // The largest (the sum) of a value over the four lanes l % 16 + 16 k.
@@ -96,10 +179,16 @@ __device__ __forceinline__ float log2_of(float v) { return __builtin_amdgcn_logf
 // for it in the exponent.
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
 
+__device__ __forceinline__ void finish_row(const AttendArgs &a, const Plan &p, int64_t row, float top, float total) {
+  const float level = top + log2_of(total);
+  if (a.lse) a.lse[row] = total == 0.f ? -INFINITY : level * 0.69314718055994531f;
+  if (p.level) p.level[row] = total == 0.f ? INFINITY : level;
+}
+
 // KS: the head's size in units of 32, rounded up.  Uniform: a page holds whole
 // steps, so that a step has one page; otherwise each 8 slots have one.
 template <typename E, int KS, bool Uniform>
-__global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) attend_kernel(AttendArgs a, Plan p) {
+__global__ void __launch_bounds__(kThreads, KS <= 3 ? 3 : KS <= 4 ? 2 : 1) attend_kernel(AttendArgs a, Plan p) {
   constexpr bool f32 = sizeof(E) == 4;
   constexpr int es = sizeof(E), step = kStep<E>;
   constexpr int KT = f32 ? 1 : 2;          // tiles of keys of a step
@@ -114,16 +203,36 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) attend_kernel(Atten
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int quad = lane >> 4, l16 = lane & 15, d = a.c.d;
-  int b = blockIdx.x;
-  const int piece = b % p.pieces;
-  b /= p.pieces;
-  const int tile = b % p.tiles;
-  b /= p.tiles;
-  const int kh = b % a.c.heads, s = b / a.c.heads;
-  const Span sp = span_of<E>(a, p, s);
+  const int share = blockIdx.x, rows = a.c.heads * p.tiles;  // of a sequence
+  const auto units_of = [&](int n) { return span_of<E>(a, n).units; };
+  const Counted counted(a, units_of);
+  const Shares sh = shares_of(a, p, counted.sum);
+  if (share >= sh.of) return;
+  int64_t unit = sh.begin(share);
+  const int64_t unit_end = sh.begin(share + 1);
+  const Sequence at = counted.of_thing((int)over(unit, rows));
+  int s = at.s, before = at.before;
+  Span sp = span_of<E>(a, at.n);
+
+  // this lane's first column, and its offsets from the start of a step (of a
+  // block of 8 slots): the last run of columns ends with the value
+  const int col0 = min(l16 * NC, d - NC);
+  const int ktoken = f32 ? (Uniform ? l16 : l16 & 7) : (Uniform ? 8 * (l16 >> 2) : 0) + (l16 & 3);
+  const int vtoken = f32 ? (Uniform ? 4 * quad : 4 * (quad & 1)) : (Uniform ? 8 * quad : 0);
+  const int kblock = f32 ? l16 >> 3 : l16 >> 2, vblock = f32 ? quad >> 1 : quad;
+  const uint32_t ss = (uint32_t)a.c.slot_stride;
+  const uint32_t ko = ktoken * ss + 16 * quad, vo = vtoken * ss + col0 * es;
+  const float scale2 = a.scale * 1.4426950408889634f;
+
+  for (;;) {
+  const int64_t in_rows = unit - (int64_t)before * rows;
+  const int row_at = (int)over(in_rows, sp.units);
+  const int skip = (int)(in_rows - (int64_t)row_at * sp.units);  // units of the row that earlier workgroups have
+  const int mine = (int)min((int64_t)(sp.units - skip), unit_end - unit);
+  const bool whole = mine == sp.units;
+  const int kh = row_at / p.tiles, tile = row_at - kh * p.tiles;
   const int live = min(16, a.group - tile * 16);  // query heads of this tile
   const int head0 = kh * a.group + tile * 16;
-  if (piece >= sp.pieces && !(piece == 0 && sp.pieces == 0)) return;
 
   // this lane's query head as the operand B of S^T
   u32x4_t q[CH];
@@ -134,39 +243,32 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) attend_kernel(Atten
     if (l16 < live && e < d)
       q[c] = *reinterpret_cast<const u32x4_t *>(a.q.p + s * a.q.row + (head0 + l16) * a.q.head + e * es);
   }
-
-  // this lane's first column, and its offsets from the start of a step (of a
-  // block of 8 slots): the last run of columns ends with the value
-  const int col0 = min(l16 * NC, d - NC);
-  const int ktoken = f32 ? (Uniform ? l16 : l16 & 7) : (Uniform ? 8 * (l16 >> 2) : 0) + (l16 & 3);
-  const int vtoken = f32 ? (Uniform ? 4 * quad : 4 * (quad & 1)) : (Uniform ? 8 * quad : 0);
-  const int kblock = f32 ? l16 >> 3 : l16 >> 2, vblock = f32 ? quad >> 1 : quad;
-  const uint32_t ss = (uint32_t)a.c.slot_stride;
-  const uint32_t ko = ktoken * ss + 16 * quad, vo = vtoken * ss + col0 * es;
   const int32_t *const table = a.c.table + s * a.c.ld;
 
+  // The page numbers of this lane's keys and values, as the table has them: they
+  // are checked where they are used, a step later, so that nothing waits for
+  // them here.  Slots behind the last read the last one's and are masked.
   struct Where {
-    int k, v;  // pages of this lane's keys and values, -1 for none
+    uint32_t k, v;
   };
   const auto pages_of = [&](int st) {
-    const auto page = [&](int t) {
-      if (t >= sp.n) return -1;
-      const int g = table[t >> a.c.shift];
-      return (uint32_t)g < (uint32_t)a.c.pages ? g : -1;
-    };
-    Where w;
+    const auto page = [&](int t) { return (uint32_t)table[min(t, sp.n - 1) >> a.c.shift]; };
     if constexpr (Uniform) {
-      w.k = w.v = __builtin_amdgcn_readfirstlane(page(st * step));
+      const uint32_t g = page(st * step);
+      return Where{g, g};
     } else {
-      w.k = page(st * step + 8 * kblock);
-      w.v = page(st * step + 8 * vblock);
+      return Where{page(st * step + 8 * kblock), page(st * step + 8 * vblock)};
     }
-    return w;
+  };
+  const uint32_t pages = a.c.pages;
+  const auto start_of = [&](uint32_t g, int t) {
+    if constexpr (Uniform) g = __builtin_amdgcn_readfirstlane(g);
+    return entry_at(a.c, g < pages ? g : 0, kh, t);
   };
   u32x4_t k[KT][CH];
   uint32_t v[VT][VD];
   const auto load_k = [&](const Where &w, int st) {
-    const uint8_t *const at = a.c.K + entry_at(a.c, max(w.k, 0), kh, st * step + (Uniform ? 0 : 8 * kblock));
+    const uint8_t *const at = a.c.K + start_of(w.k, st * step + (Uniform ? 0 : 8 * kblock));
 #pragma unroll
     for (int u = 0; u < KT; ++u)
 #pragma unroll
@@ -176,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) attend_kernel(Atten
       }
   };
   const auto load_v = [&](const Where &w, int st) {
-    const uint8_t *const at = a.c.V + entry_at(a.c, max(w.v, 0), kh, st * step + (Uniform ? 0 : 8 * vblock));
+    const uint8_t *const at = a.c.V + start_of(w.v, st * step + (Uniform ? 0 : 8 * vblock));
     struct Run {
       uint32_t w[VD];
     };
@@ -184,18 +286,18 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) attend_kernel(Atten
     for (int e = 0; e < VT; ++e) __builtin_memcpy(v[e], at + e * (uint64_t)ss + vo, sizeof(Run));
   };
 
-  const float scale2 = a.scale * 1.4426950408889634f;
   f32x4_t acc[NC];
 #pragma unroll
   for (int j = 0; j < NC; ++j) acc[j] = f32x4_t{0, 0, 0, 0};
   float m = -INFINITY, sum = 0.f;  // of head l16; the sum over this lane's slots
-  const int end = sp.lo + min(sp.steps, (piece + 1) * sp.per);
-  int st = sp.lo + piece * sp.per + wave;
-  Where now = pages_of(st < end ? st : 0), next = now;
+  const int end = sp.lo + min(sp.steps, (skip + mine) * kWaves);
+  int st = sp.lo + skip * kWaves + wave;
+  Where now{}, next{};
   if (st < end) {
+    now = pages_of(st);
+    next = pages_of(st + kWaves);
     load_k(now, st);
     load_v(now, st);
-    if (st + kWaves < end) next = pages_of(st + kWaves);
   }
   for (; st < end; st += kWaves) {
     f32x4_t sc[KT];
@@ -218,11 +320,8 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) attend_kernel(Atten
     }
     // the next step's keys into the registers that have just been read
     const bool more = st + kWaves < end;
-    Where after = next;
-    if (more) {
-      load_k(next, st + kWaves);
-      if (st + 2 * kWaves < end) after = pages_of(st + 2 * kWaves);
-    }
+    const Where after = pages_of(st + 2 * kWaves);
+    if (more) load_k(next, st + kWaves);
     float w[VT];
 #pragma unroll
     for (int i = 0; i < VT; ++i) w[i] = sc[i / 4][i % 4] * scale2;
@@ -232,11 +331,11 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) attend_kernel(Atten
 #pragma unroll
     for (int i = 0; i < VT; ++i) {
       const int t = t0 + VT * quad + i;
-      in[i] = t >= sp.first && t < sp.n && now.v >= 0 ? ~0u : 0u;
+      in[i] = t >= sp.first && t < sp.n && now.v < pages ? ~0u : 0u;
       w[i] = in[i] ? w[i] : -INFINITY;
     }
     if (p.scores && l16 < live) {
-      float *const to = p.scores + ((int64_t)s * a.q.n + head0 + l16) * p.row + t0 + VT * quad;
+      float *const to = p.scores + ((int64_t)s * a.q.n + head0 + l16) * p.scores_row + t0 + VT * quad;
 #pragma unroll
       for (int i = 0; i < VT; i += 4) *reinterpret_cast<f32x4_t *>(to + i) = f32x4_t{w[i], w[i + 1], w[i + 2], w[i + 3]};
     }
@@ -311,15 +410,17 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) attend_kernel(Atten
       for (int j = 0; j < NC; ++j) red[wave][h][col0 + j] = acc[j][i] * f;
   }
   __syncthreads();
-  const bool whole = sp.pieces <= 1;
+  const int64_t slot = 2 * (int64_t)share + (skip == 0);
   for (int h = wave; h < live; h += kWaves) {
     float top = red_m[0][h], total = 0.f;
     for (int w = 1; w < kWaves; ++w) top = fmaxf(top, red_m[w][h]);
     for (int w = 0; w < kWaves; ++w) total += red_l[w][h] * exp2_of(red_m[w][h] - base_of(top));
-    const int64_t row = (int64_t)s * a.q.n + head0 + h, at = row * p.pieces + piece;
+    const int64_t row = (int64_t)s * a.q.n + head0 + h;
     if (lane == 0) {
-      if (p.stats) p.stats[2 * at] = top, p.stats[2 * at + 1] = total;
-      if (whole && a.lse) a.lse[row] = total == 0.f ? -INFINITY : (top + log2_of(total)) * 0.69314718055994531f;
+      if (whole)
+        finish_row(a, p, row, top, total);
+      else
+        p.stats[2 * (slot * 16 + h)] = top, p.stats[2 * (slot * 16 + h) + 1] = total;
     }
     const float inv = total == 0.f ? 0.f : 1.f / total;
     for (int c = lane; c < d; c += 64) {
@@ -329,110 +430,190 @@ __global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) attend_kernel(Atten
       if (whole)
         reinterpret_cast<E *>(a.out.p + s * a.out.row + (head0 + h) * a.out.head)[c] = (E)(total == 0.f ? 0.f : o * inv);
       else
-        p.partial[at * d + c] = o;
+        p.partial[(slot * 16 + h) * d + c] = o;
     }
+  }
+  unit += mine;
+  if (unit >= unit_end) return;
+  if (row_at == rows - 1) {  // the row is done, and was the sequence's last
+    before += sp.units;
+    sp = span_of<E>(a, clamped_length(a.c, a.lengths, ++s));
+  }
+  __syncthreads();  // the sums have been read
   }
 }
 
-// log2 of the sum of a row's weights, from its pieces' statistics; by a wavefront.
-__device__ __forceinline__ float joined(const float *stats, int pieces, float *top_out) {
-  const int lane = threadIdx.x & 63;
-  float top = -INFINITY, total = 0.f;
-  for (int i = lane; i < pieces; i += 64) top = fmaxf(top, stats[2 * i]);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-  for (int i = lane; i < pieces; i += 64) total += stats[2 * i + 1] * exp2_of(stats[2 * i] - base_of(top));
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o, 64);
-  *top_out = top;
-  return total;
-}
+// A maximum and the sum of weights at it.
+struct Stat {
+  float m, l;
+};
 
-constexpr int kMassSlots = 1024;  // of a workgroup
+// Query heads that a workgroup of join_kernel takes: four columns a thread.
+inline __host__ __device__ int heads_at_once(int d) { return max(1, 4 * kThreads / d); }
 
-// Workgroups below `rows` join a row each, those behind add the weights of
-// kMassSlots slots of a sequence and key head.
+// Joins the rows that are cut.  By `cuts`, `sets` workgroups for each share's end
+// join the row that this end cuts, if no earlier one cuts it, heads_at_once()
+// query heads each; otherwise a workgroup takes a query head of a sequence.
+// All latency: the lengths, and then all pieces' statistics and sums at once.
+// (A first round for the statistics and second ones for eight pieces at a time
+// took 5 us more for 65 pieces; workgroups of 1024 threads took 10 us alone to
+// start and end.)
 template <typename E>
-__global__ void __launch_bounds__(kThreads) join_kernel(AttendArgs a, Plan p, int rows, int strips) {
-  __shared__ float red[kWaves][256];
-  __shared__ float level[4096];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, d = a.c.d;
-  if ((int)blockIdx.x < rows) {
-    const int row = blockIdx.x, s = row / a.q.n, h = row - s * a.q.n;
-    const Span sp = span_of<E>(a, p, s);
-    if (sp.pieces <= 1) return;
-    const float *const stats = p.stats + (int64_t)row * p.pieces * 2;
-    float top;
-    const float total = joined(stats, sp.pieces, &top), base = base_of(top);
-    float o[4] = {};
-    if (4 * lane < d) {
-      for (int i = wave; i < sp.pieces; i += kWaves) {
-        const float f = exp2_of(stats[2 * i] - base);
-        const f32x4_t u = *reinterpret_cast<const f32x4_t *>(p.partial + ((int64_t)row * p.pieces + i) * d + 4 * lane);
+__global__ void __launch_bounds__(kThreads) join_kernel(AttendArgs a, Plan p, bool cuts, int sets) {
+  __shared__ __attribute__((aligned(16))) float red[kThreads * 4];
+  __shared__ float red_m[kThreads], red_l[kThreads];
+  const int tid = threadIdx.x, d = a.c.d, rows = a.c.heads * p.tiles;
+  const auto units_of = [&](int n) { return span_of<E>(a, n).units; };
+  const Counted counted(a, units_of);
+  const Shares sh = shares_of(a, p, counted.sum);
+  int64_t start;
+  int s, first, units, kh, tile, in_tile, live;
+  if (cuts) {
+    const int share = blockIdx.x / sets + 1, most = heads_at_once(d);
+    if (share >= sh.of) return;
+    const int64_t cut = sh.begin(share);
+    const Sequence at = counted.of_thing((int)over(cut, rows));
+    s = at.s;
+    units = units_of(at.n);
+    const int row_at = (int)over(cut - (int64_t)at.before * rows, units);
+    start = (int64_t)at.before * rows + (int64_t)row_at * units;
+    first = sh.owner(start);
+    if (cut == start || share != first + 1) return;
+    kh = row_at / p.tiles, tile = row_at - kh * p.tiles;
+    in_tile = (blockIdx.x - (share - 1) * sets) * most;
+    live = min(min(16, a.group - tile * 16) - in_tile, most);
+    if (live <= 0) return;
+  } else {
+    s = blockIdx.x / a.q.n;
+    const int h = blockIdx.x - s * a.q.n;
+    kh = h / a.group, tile = (h - kh * a.group) / 16, in_tile = (h - kh * a.group) % 16, live = 1;
+    const Sequence at = counted.number(s);
+    units = units_of(at.n);
+    start = (int64_t)at.before * rows + (int64_t)(kh * p.tiles + tile) * units;
+    first = sh.owner(start);
+  }
+  const int pieces = sh.owner(start + units - 1) - first + 1;
+  if (pieces <= 1) return;
+  const int head0 = kh * a.group + tile * 16 + in_tile;
+  // `sides` threads share four columns of a head, each takes every sides-th piece
+  const int items = live * d / 4, sides = kThreads / items, side = tid / items, item = tid - side * items;
+  const int h = 4 * item / d, c = 4 * item - h * d;
+  if (side < sides) {
+    constexpr int kAhead = 12;
+    f32x4_t o = {0, 0, 0, 0};
+    Stat all{-INFINITY, 0.f};
+    for (int i0 = side; i0 < pieces; i0 += kAhead * sides) {
+      f32x4_t u[kAhead];
+      Stat t[kAhead];
+      float top = all.m;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] += u[j] * f;
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = min(i0 + k * sides, pieces - 1);
+        const int64_t at = (2 * (int64_t)(first + i) + (i == 0)) * 16 + in_tile + h;
+        u[k] = *reinterpret_cast<const f32x4_t *>(p.partial + at * d + c);
+        t[k] = *reinterpret_cast<const Stat *>(p.stats + 2 * at);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) red[wave][4 * lane + j] = o[j];
-    }
-    __syncthreads();
-    if ((int)threadIdx.x < d) {
-      float v = 0.f;
+      for (int k = 0; k < kAhead; ++k)
+        if (i0 + k * sides < pieces) top = fmaxf(top, t[k].m);
+      const float base = base_of(top), fade = exp2_of(all.m - base);
+      all = {top, all.l * fade};
+      o *= fade;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) v += red[w][threadIdx.x];
-      reinterpret_cast<E *>(a.out.p + s * a.out.row + h * a.out.head)[threadIdx.x] = (E)(total == 0.f ? 0.f : v / total);
+      for (int k = 0; k < kAhead; ++k) {
+        if (i0 + k * sides >= pieces) continue;
+        const float f = exp2_of(t[k].m - base);
+        all.l += t[k].l * f;
+        o += u[k] * f;
+      }
     }
-    if (threadIdx.x == 0 && a.lse)
-      a.lse[row] = total == 0.f ? -INFINITY : (top + log2_of(total)) * 0.69314718055994531f;
-    return;
-  }
-  const int b = blockIdx.x - rows, strip = b % strips, kh = b / strips % a.c.heads, s = b / strips / a.c.heads;
-  const Span sp = span_of<E>(a, p, s);
-  const int lo = max(sp.first, strip * kMassSlots), hi = min(sp.n, (strip + 1) * kMassSlots);
-  if (lo >= hi) return;
-  const int64_t row0 = (int64_t)s * a.q.n + kh * a.group;
-  for (int h = wave; h < a.group; h += kWaves) {
-    float top;
-    const float total = joined(p.stats + (row0 + h) * p.pieces * 2, sp.pieces, &top);
-    if (lane == 0) level[h] = total == 0.f ? INFINITY : top + log2_of(total);
+    *reinterpret_cast<f32x4_t *>(red + 4 * tid) = o;
+    red_m[tid] = all.m, red_l[tid] = all.l;
   }
   __syncthreads();
-  for (int i = lo + threadIdx.x; i < hi; i += kThreads) {
-    const int page = page_of(a.c, s, i);
-    if (page < 0) continue;
-    float add = 0.f;
-    for (int h = 0; h < a.group; ++h) add += exp2_of(p.scores[(row0 + h) * p.row + i] - level[h]);
-    a.c.mass[number_at(a.c, page, kh, i)] += add;
+  if (side != 0) return;
+  float top = red_m[item], total = 0.f;
+  for (int w = 1; w < sides; ++w) top = fmaxf(top, red_m[w * items + item]);
+  f32x4_t v = {0, 0, 0, 0};
+  for (int w = 0; w < sides; ++w) {
+    const float f = exp2_of(red_m[w * items + item] - base_of(top));
+    total += red_l[w * items + item] * f;
+    v += *reinterpret_cast<const f32x4_t *>(red + 4 * (w * items + item)) * f;
+  }
+  if (c == 0) finish_row(a, p, (int64_t)s * a.q.n + head0 + h, top, total);
+  E *const out = reinterpret_cast<E *>(a.out.p + s * a.out.row + (head0 + h) * a.out.head) + c;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) out[k] = (E)(total == 0.f ? 0.f : v[k] / total);
+}
+
+constexpr int kMassSlots = 256;  // of a workgroup at a time
+constexpr int kMassGrid = 2048;
+
+// Workgroups walk the strips of kMassSlots slots of all sequences and key heads;
+// a strip's query heads are dealt to the wavefronts, four slots a lane, and a
+// thread adds up a slot.
+__global__ void __launch_bounds__(kThreads) mass_kernel(AttendArgs a, Plan p) {
+  __shared__ float sums[kWaves][kMassSlots];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const auto first_of = [&](int n) { return a.window > 0 ? max(0, n - a.window) : 0; };
+  const auto strips = [&](int n) { return (n + kMassSlots - 1) / kMassSlots - first_of(n) / kMassSlots; };
+  const Counted counted(a, strips);
+  const int64_t all = (int64_t)counted.sum * a.c.heads;
+  for (int64_t at = blockIdx.x; at < all; at += gridDim.x) {
+    const Sequence seq = counted.of_thing((int)over(at, a.c.heads));
+    const int s = seq.s, n = seq.n, first = first_of(n);
+    const int in = (int)(at - (int64_t)seq.before * a.c.heads), of = strips(n), kh = in / of, strip = in - kh * of;
+    const int lo = (first / kMassSlots + strip) * kMassSlots, i = lo + tid;
+    const int64_t row0 = (int64_t)s * a.q.n + kh * a.group;
+    const int page = i >= first && i < n ? page_of(a.c, s, i) : -1;
+    const int64_t number = number_at(a.c, max(page, 0), kh, i);
+    const float mass = a.c.mass[number];
+    f32x4_t add = {0, 0, 0, 0};
+    const int mine = min(lo + 4 * lane, p.scores_row - 4);  // what lies behind the row's slots is not used
+#pragma unroll 4
+    for (int h = wave; h < a.group; h += kWaves) {
+      const float level = p.level[row0 + h];
+      const f32x4_t score = *reinterpret_cast<const f32x4_t *>(p.scores + (row0 + h) * p.scores_row + mine);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) add[k] += exp2_of(score[k] - level);
+    }
+    *reinterpret_cast<f32x4_t *>(&sums[wave][4 * lane]) = add;
+    __syncthreads();
+    if (page >= 0) {
+      float v = 0.f;  // what is added first: the mass is rounded once
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) v += sums[w][tid];
+      a.c.mass[number] = mass + v;
+    }
+    __syncthreads();
   }
 }
+
+// Workgroups that the chip holds at once, by the registers of the kernel.
+inline int shares_for(int d) { return 256 * (d <= 96 ? 3 : d <= 128 ? 2 : 1); }
 
 template <typename E>
 Plan plan_of(const Pool &c, int q_heads, bool accumulate, uint8_t *ws, size_t *bytes) {
   Plan p{};
-  const int64_t slots = (int64_t)c.most << c.shift, steps = (slots + kStep<E> - 1) / kStep<E>;
+  const int64_t slots = (int64_t)c.most << c.shift;
+  const int64_t units = std::max<int64_t>(1, (slots + kWaves * kStep<E> - 1) / (kWaves * kStep<E>));
   p.tiles = (q_heads / c.heads + 15) / 16;
-  const int64_t rows = std::max<int64_t>(1, (int64_t)c.S * c.heads * p.tiles);
-  // Pieces enough that the chip has four rounds of workgroups, two to a CU, of
-  // at least 128 slots; where rows alone do, of 1024 slots, so that no long
-  // sequence is left at the end.
-  int64_t want = 1024 / rows, least = kWaves;
-  const int64_t longest = 1024 / kStep<E>;
-  want = std::max<int64_t>(want, (steps + longest - 1) / longest);
-  if (rows >= 1024) least = longest;
-  want = std::min<int64_t>({want, kMostPieces, (steps + least - 1) / least});
-  p.pieces = (int)std::max<int64_t>(1, want);
-  p.least = (int)least;
-  p.row = (int)((slots + 31) / 32 * 32);
-  const size_t all = (size_t)c.S * q_heads;
+  p.shares = (int)std::min<int64_t>(shares_for(c.d), c.S * units * c.heads * p.tiles);
+  p.scores_row = (int)((slots + 31) / 32 * 32);
   size_t at = 0;
   const auto take = [&](size_t floats) {
     float *const r = ws ? reinterpret_cast<float *>(ws + at) : nullptr;
     at += (floats * 4 + 15) / 16 * 16;
     return r;
   };
-  if (p.pieces > 1 || accumulate) p.stats = take(all * p.pieces * 2);
-  if (p.pieces > 1) p.partial = take(all * p.pieces * c.d);
-  if (accumulate) p.scores = take(all * p.row);
+  if (units > 1) {
+    p.stats = take((size_t)p.shares * 2 * 16 * 2);
+    p.partial = take((size_t)p.shares * 2 * 16 * c.d);
+  }
+  if (accumulate) {
+    p.level = take((size_t)c.S * q_heads);
+    p.scores = take((size_t)c.S * q_heads * p.scores_row);
+  }
   if (bytes) *bytes = at;
   return p;
 }
@@ -440,18 +621,16 @@ Plan plan_of(const Pool &c, int q_heads, bool accumulate, uint8_t *ws, size_t *b
 template <typename E>
 gsi_status launch_as(const AttendArgs &a, hipStream_t st) {
   const Plan p = plan_of<E>(a.c, a.q.n, a.accumulate, a.ws, nullptr);
-  const int64_t grid = (int64_t)a.c.S * a.c.heads * p.tiles * p.pieces;
-  const int64_t rows = p.pieces > 1 ? (int64_t)a.c.S * a.q.n : 0;
-  const int64_t strips = ((int64_t)a.c.most << a.c.shift) / kMassSlots + 1;
-  const int64_t second = rows + (a.accumulate ? (int64_t)a.c.S * a.c.heads * strips : 0);
-  if (grid * kThreads > kMostLaunch || second * kThreads > kMostLaunch) return GSI_E_SHAPE;
+  // units of all sequences, a unit each at least, are counted in 32 bits
+  if ((((int64_t)a.c.most << a.c.shift) / 64 + 1) * a.c.S > INT32_MAX) return GSI_E_SHAPE;
+  const unsigned grid = p.shares;
   const bool uniform = 1 << a.c.shift >= kStep<E>;
   const auto go = [&](auto ks) {
     constexpr int KS = decltype(ks)::value;
     if (uniform)
-      attend_kernel<E, KS, true><<<(unsigned)grid, kThreads, 0, st>>>(a, p);
+      attend_kernel<E, KS, true><<<grid, kThreads, 0, st>>>(a, p);
     else
-      attend_kernel<E, KS, false><<<(unsigned)grid, kThreads, 0, st>>>(a, p);
+      attend_kernel<E, KS, false><<<grid, kThreads, 0, st>>>(a, p);
   };
   const int ks = (a.c.d + 31) / 32;
   if (ks == 1)
@@ -467,9 +646,19 @@ gsi_status launch_as(const AttendArgs &a, hipStream_t st) {
   else
     go(std::integral_constant<int, 8>{});
   if (hipGetLastError() != hipSuccess) return GSI_E_HIP;
-  if (second == 0) return GSI_OK;
-  join_kernel<E><<<(unsigned)second, kThreads, 0, st>>>(a, p, (int)rows, (int)strips);
-  return hipGetLastError() == hipSuccess ? GSI_OK : GSI_E_HIP;
+  if (p.stats && p.shares > 1) {
+    const int most = heads_at_once(a.c.d), sets = (std::min(16, a.group) + most - 1) / most;
+    const int64_t by_cuts = (int64_t)(p.shares - 1) * sets, by_heads = (int64_t)a.c.S * a.q.n;
+    const bool cuts = by_cuts < by_heads;
+    join_kernel<E><<<(unsigned)(cuts ? by_cuts : by_heads), kThreads, 0, st>>>(a, p, cuts, sets);
+    if (hipGetLastError() != hipSuccess) return GSI_E_HIP;
+  }
+  if (a.accumulate && a.c.most > 0) {
+    const int64_t strips = (((int64_t)a.c.most << a.c.shift) + kMassSlots - 1) / kMassSlots * a.c.S * a.c.heads;
+    mass_kernel<<<(unsigned)std::min<int64_t>(strips, kMassGrid), kThreads, 0, st>>>(a, p);
+    if (hipGetLastError() != hipSuccess) return GSI_E_HIP;
+  }
+  return GSI_OK;
 }
 
 }  // namespace

@@ -165,11 +165,9 @@ def test_attend_refuses():
     assert gsi.lib().gsi_cache_attend_workspace(REF(cache()), None, 4, 1) == 0
 
 
-def test_attend_refuses_what_a_launch_cannot_hold():
-    t = table(S=(1 << 24) - 1, most=1, ld=1)
-    c = cache(heads=1024, ps=16 * 1024 * 64)
-    q = heads(n=4096, row=4096 * 64)
-    assert attend(c=c, t=t, q=q, out=q, ws_bytes=2**63) == E_SHAPE
+def test_attend_refuses_more_slots_than_it_counts():
+    assert attend(t=table(S=(1 << 24) - 1, most=1 << 10, ld=1 << 10), ws_bytes=2**63) == E_SHAPE
+    assert attend(t=table(S=1 << 20, most=1 << 13, ld=1 << 13), ws_bytes=2**63) == E_SHAPE
 
 
 def test_evict_refuses():
