@@ -9,10 +9,11 @@
 // The newest entries and those of the largest mass are each found as all
 // entries above a threshold, the key of the wanted rank, and the first ones at
 // it.  The threshold comes eight bits at a time: entries that agree with it so
-// far are counted by their next eight bits in LDS.  Keys lie in registers (up to
-// 4096 slots) or LDS (up to 32768), so an entry's mass and age are read once; a
-// call for a few thousand slots is bound by the latency of these reads and of
-// the dozen barriers behind them, one for long sequences by the counting.
+// far are counted by their next eight bits in LDS.  A lane holds the keys of four
+// slots one after the other, which lie in one page, so that a load of 16 bytes
+// reads them; up to 32768 slots stay in registers and are read once.  A call for
+// a few thousand slots is bound by the latency of these reads and of the dozen
+// barriers behind them, one for long sequences by the counting in LDS.
 #include <utility>
 
 #include "gsi_cache.h"
@@ -32,7 +33,11 @@ __device__ __forceinline__ uint32_t mass_key(float v) {
 }
 __device__ __forceinline__ uint32_t age_key(int32_t v) { return (uint32_t)v ^ 0x80000000u; }
 
-// LDS of a workgroup.  words: as many 64-bit words as the slots need.
+struct Four {
+  uint32_t v[4];
+};
+
+// LDS of a workgroup.
 struct Shared {
   int hist[2][4][256];  // of the two selections' passes, zero at first
   uint32_t all[2][kWaves], any[2][kWaves];
@@ -40,13 +45,13 @@ struct Shared {
   int2 moves[kFewMoves];
 };
 
-// words[w] becomes the sum of the words before it; returns after a barrier.
-__device__ void sums_before(int *words, int nw, Shared &sh) {
+// counts[b] becomes the sum of the counts before it; returns after a barrier.
+__device__ void sums_before(int *counts, int nb, Shared &sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int per = (nw + kThreads - 1) / kThreads, lo = min(tid * per, nw), hi = min(lo + per, nw);
+  const int per = (nb + kThreads - 1) / kThreads, lo = min(tid * per, nb), hi = min(lo + per, nb);
   __syncthreads();
   int sum = 0;
-  for (int w = lo; w < hi; ++w) sum += words[w];
+  for (int b = lo; b < hi; ++b) sum += counts[b];
   int incl = sum;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
@@ -57,71 +62,81 @@ __device__ void sums_before(int *words, int nw, Shared &sh) {
   __syncthreads();
   int run = incl - sum;
   for (int w = 0; w < wave; ++w) run += sh.part[w];
-  for (int w = lo; w < hi; ++w) {
-    const int c = words[w];
-    words[w] = run;
+  for (int b = lo; b < hi; ++b) {
+    const int c = counts[b];
+    counts[b] = run;
     run += c;
   }
   __syncthreads();
 }
 
-// Where a selection's keys lie: four words of slots per wavefront in registers,
-// LDS, or where they came from, read again each time.
-enum Keys { kInRegisters, kInLds, kInMemory };
-constexpr int kWords = 4;
-constexpr int kMostInRegisters = kWords * kThreads, kMostInLds = 32 * 1024;
+__device__ __forceinline__ uint64_t below(int lane) { return (1ull << lane) - 1; }
 
-// The slots of a workgroup: slot 64 w + lane of word w, words dealt to the
-// wavefronts in turn.
-template <Keys K>
+// The slots of a workgroup in blocks of 256: slot 256 b + 4 lane + e of a block,
+// blocks dealt to the wavefronts in turn.  NB blocks at most of a wavefront, with
+// their keys in registers; 0: any number, keys are read again each time.
+constexpr int kBlock = 256;
+template <int NB>
 struct Slots {
   int n, lane, wave;
-  uint64_t *keep;     // a bit per slot (from registers: written at the end)
-  uint32_t kept = 0;  // in registers: bit r for this lane's slot of word r
+  uint64_t *keep;     // [block][e]: a bit per lane (for NB > 0 written at the end)
+  uint32_t kept = 0;  // NB > 0: bit 4 k + e
 
-  // f(r, w) for each of the wavefront's words; r is a constant, or the arrays
+  // f(k, b) for each of the wavefront's blocks; k is a constant, or the arrays
   // that it indexes would not stay in registers
   template <typename F>
   __device__ __forceinline__ void each(const F &f) const {
-    if constexpr (K == kInRegisters) {
-      unrolled(f, std::make_integer_sequence<int, kWords>());
+    if constexpr (NB > 0)
+      unrolled(f, std::make_integer_sequence<int, NB>());
+    else
+      for (int b = wave; b * kBlock < n; b += kWaves) f(std::integral_constant<int, 0>{}, b);
+  }
+  template <typename F, int... K>
+  __device__ __forceinline__ void unrolled(const F &f, std::integer_sequence<int, K...>) const {
+    (((wave + kWaves * K) * kBlock < n ? f(std::integral_constant<int, K>{}, wave + kWaves * K) : void()), ...);
+  }
+  // bit e: slot e of this lane is there and not kept yet
+  __device__ __forceinline__ uint32_t is_free(int k, int b) const {
+    uint32_t mine;
+    if constexpr (NB > 0) {
+      mine = kept >> (4 * k);
     } else {
-      for (int w = wave; w * 64 < n; w += kWaves) f(std::integral_constant<int, 0>{}, w);
+      mine = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mine |= (uint32_t)(keep[4 * b + e] >> lane & 1) << e;
     }
+    const int left = n - (b * kBlock + 4 * lane);
+    return ~mine & (left >= 4 ? 15u : left <= 0 ? 0u : (1u << left) - 1);
   }
-  template <typename F, int... R>
-  __device__ __forceinline__ void unrolled(const F &f, std::integer_sequence<int, R...>) const {
-    ((wave * 64 + kWaves * 64 * R < n ? f(std::integral_constant<int, R>{}, wave + kWaves * R) : void()), ...);
-  }
-  __device__ __forceinline__ bool is_free(int r, int w) const {
-    if (w * 64 + lane >= n) return false;
-    if constexpr (K == kInRegisters) return !(kept >> r & 1);
-    return !(keep[w] >> lane & 1);
-  }
-  // every lane of the wavefront
-  __device__ __forceinline__ void take(int r, int w, bool mine) {
-    if constexpr (K == kInRegisters) {
-      kept |= (uint32_t)mine << r;
+  __device__ __forceinline__ void take(int k, int b, uint32_t mine) {  // every lane of the wavefront
+    if constexpr (NB > 0) {
+      kept |= mine << (4 * k);
     } else {
-      const uint64_t m = __ballot(mine);
-      if (lane == 0) keep[w] |= m;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint64_t m = __ballot(mine >> e & 1);
+        if (lane == 0) keep[4 * b + e] |= m;
+      }
     }
   }
 };
 
 // Keeps the `count` free slots of the largest key, ties to the lowest slot;
-// there are at least `count`.  which: 0 or 1, the selection's LDS.
-template <Keys K, typename Key>
-__device__ __forceinline__ void take_largest(Slots<K> &sl, int count, const Key &key, int which, int *words, Shared &sh) {
-  if (count <= 0) return;
+// there are at least `count`.  keys(k, b): this lane's four keys; which: 0 or 1,
+// the selection's LDS; counts: LDS for a number per block.
+template <int NB, typename Keys>
+__device__ __forceinline__ void take_largest(Slots<NB> &sl, int count, const Keys &keys, int which, int *counts,
+                                             Shared &sh) {
   const int lane = sl.lane;
   // what all keys agree in, from the top, needs no counting
   uint32_t all = ~0u, any = 0;
-  sl.each([&](auto r, int w) {
-    if (sl.is_free(r, w)) {
-      const uint32_t k = key(r, w);
-      all &= k;
-      any |= k;
+  sl.each([&](auto k, int b) {
+    const uint32_t is_free = sl.is_free(k, b);
+    const Four key = keys(k, b);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      all &= is_free >> e & 1 ? key.v[e] : ~0u;
+      any |= is_free >> e & 1 ? key.v[e] : 0u;
     }
   });
 #pragma unroll
@@ -141,10 +156,13 @@ __device__ __forceinline__ void take_largest(Slots<K> &sl, int count, const Key 
     const int low = max(shift - 8, 0);
     const uint32_t mask = (1u << (shift - low)) - 1;
     int *const hist = sh.hist[which][pass];
-    sl.each([&](auto r, int w) {
-      if (!sl.is_free(r, w)) return;
-      const uint32_t k = key(r, w);
-      if ((uint64_t)k >> shift == prefix) atomicAdd(&hist[k >> low & mask], 1);  // integers: any order
+    sl.each([&](auto k, int b) {
+      const uint32_t is_free = sl.is_free(k, b);
+      const Four key = keys(k, b);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((is_free >> e & 1) && (uint64_t)key.v[e] >> shift == prefix)
+          atomicAdd(&hist[key.v[e] >> low & mask], 1);  // integers: any order
     });
     __syncthreads();
     // from the top, four bins a lane: the bin where the running count reaches
@@ -173,18 +191,42 @@ __device__ __forceinline__ void take_largest(Slots<K> &sl, int count, const Key 
     shift = low;
   }
   if (!tied) {
-    sl.each([&](auto r, int w) { sl.take(r, w, sl.is_free(r, w) && (uint64_t)key(r, w) >> shift >= prefix); });
-  } else {  // the first `need` slots with this very key
-    sl.each([&](auto r, int w) {
-      const int same = __popcll(__ballot(sl.is_free(r, w) && key(r, w) == prefix));
-      if (lane == 0) words[w] = same;
+    sl.each([&](auto k, int b) {
+      const Four key = keys(k, b);
+      uint32_t mine = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mine |= (uint32_t)((uint64_t)key.v[e] >> shift >= prefix) << e;
+      sl.take(k, b, mine & sl.is_free(k, b));
     });
-    sums_before(words, (sl.n + 63) / 64, sh);
-    sl.each([&](auto r, int w) {
-      const bool is_free = sl.is_free(r, w);
-      const uint32_t k = is_free ? key(r, w) : 0;
-      const int rank = words[w] + __popcll(__ballot(is_free && k == prefix) & ((1ull << lane) - 1));
-      sl.take(r, w, is_free && (k > prefix || (k == prefix && rank < need)));
+  } else {  // the first `need` slots with this very key
+    const auto same_of = [&](const Four &key, uint32_t is_free) {
+      uint32_t same = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) same |= (uint32_t)(key.v[e] == prefix) << e;
+      return same & is_free;
+    };
+    sl.each([&](auto k, int b) {
+      const uint32_t same = same_of(keys(k, b), sl.is_free(k, b));
+      int c = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c += __popcll(__ballot(same >> e & 1));
+      if (lane == 0) counts[b] = c;
+    });
+    sums_before(counts, (sl.n + kBlock - 1) / kBlock, sh);
+    sl.each([&](auto k, int b) {
+      const uint32_t is_free = sl.is_free(k, b);
+      const Four key = keys(k, b);
+      const uint32_t same = same_of(key, is_free);
+      int rank = counts[b];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) rank += __popcll(__ballot(same >> e & 1) & below(lane));
+      uint32_t mine = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (key.v[e] > prefix || ((same >> e & 1) && rank < need)) mine |= 1u << e;
+        rank += same >> e & 1;
+      }
+      sl.take(k, b, mine & is_free);
     });
   }
   __syncthreads();
@@ -203,9 +245,9 @@ __device__ __forceinline__ void move_numbers(const EvictArgs &a, int64_t from, i
   if (a.c.age) a.c.age[to] = a.c.age[from];
 }
 
-// words: 64-bit words of LDS for the slots; pieces: of 16 bytes of a key.
-template <Keys K>
-__global__ void __launch_bounds__(kThreads) select_kernel(EvictArgs a, int words, int pieces) {
+// blocks: for which there is LDS; pieces: of 16 bytes of a key.
+template <int NB>
+__global__ void __launch_bounds__(kThreads) select_kernel(EvictArgs a, int blocks, int pieces) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ __attribute__((aligned(16))) Shared sh;
   const int s = blockIdx.x / a.c.heads, h = blockIdx.x - s * a.c.heads, tid = threadIdx.x;
@@ -216,96 +258,114 @@ __global__ void __launch_bounds__(kThreads) select_kernel(EvictArgs a, int words
     for (int j = tid; j < budget; j += kThreads) from[j] = j < n ? j : -1;
     return;
   }
-  const int nw = (n + 63) / 64;
-  int *const count = reinterpret_cast<int *>(lds + 8 * words);
-  uint32_t *const keys = reinterpret_cast<uint32_t *>(lds + 12 * words);
-  Slots<K> sl{n, tid & 63, tid >> 6, reinterpret_cast<uint64_t *>(lds)};
-  const bool by_age = a.c.age && a.recent > 0;
-  // An entry without a page reads page 0 and counts as the least.
-  const auto raw_page = [&](int i) { return a.c.table[s * a.c.ld + (i >> a.c.shift)]; };
+  const int nb = (n + kBlock - 1) / kBlock;
+  int *const count = reinterpret_cast<int *>(lds + 32 * blocks);
+  Slots<NB> sl{n, tid & 63, tid >> 6, reinterpret_cast<uint64_t *>(lds)};
+  const bool by_age = a.c.age && a.recent > 0, by_mass = budget > a.recent;
+  // This lane's four slots of a block: one page.  What lies behind the last slot
+  // reads the last page's; an entry without a page reads page 0 and counts as
+  // the least.
+  const auto raw_page = [&](int b) {
+    return a.c.table[s * a.c.ld + (min(b * kBlock + 4 * sl.lane, n - 1) >> a.c.shift)];
+  };
   const auto is_page = [&](int p) { return (uint32_t)p < (uint32_t)a.c.pages; };
-  const auto read_age = [&](int p, int i) { return a.c.age[number_at(a.c, is_page(p) ? p : 0, h, i)]; };
-  const auto read_mass = [&](int p, int i) { return a.c.mass[number_at(a.c, is_page(p) ? p : 0, h, i)]; };
+  const auto read = [&](const void *from_pool, int p, int b) {
+    Four r;
+    __builtin_memcpy(&r, static_cast<const uint32_t *>(from_pool) +
+                             number_at(a.c, is_page(p) ? p : 0, h, b * kBlock + 4 * sl.lane), 16);
+    return r;
+  };
+  const auto mass_keys = [&](int p, Four r) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r.v[e] = is_page(p) ? mass_key(__uint_as_float(r.v[e])) : 0;
+    return r;
+  };
+  const auto age_keys = [&](int p, Four r) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r.v[e] = is_page(p) ? age_key((int32_t)r.v[e]) : 0;
+    return r;
+  };
   for (int k = tid; k < 2 * 4 * 256; k += kThreads) (&sh.hist[0][0][0])[k] = 0;
-  uint32_t age[kWords] = {}, mass[kWords] = {};
-  if constexpr (K == kInRegisters) {  // all reads at once: pages, then masses and ages
-    int p[kWords];
-    float m[kWords];
-    int32_t t[kWords] = {};
-    sl.each([&](auto r, int w) { p[r] = raw_page(min(w * 64 + sl.lane, n - 1)); });
-    sl.each([&](auto r, int w) {
-      const int i = min(w * 64 + sl.lane, n - 1);
-      m[r] = read_mass(p[r], i);
-      if (by_age) t[r] = read_age(p[r], i);
-    });
-    sl.each([&](auto r, int) {
-      mass[r] = is_page(p[r]) ? mass_key(m[r]) : 0;
-      age[r] = is_page(p[r]) ? age_key(t[r]) : 0;
-    });
+  // All reads of a selection at once, those of both where there are registers.
+  constexpr bool kBoth = NB <= 1;
+  int p[NB > 0 ? NB : 1];
+  Four age[NB > 0 ? NB : 1], mass[NB > 0 ? NB : 1];
+  const auto read_masses = [&] {
+    sl.each([&](auto k, int b) { mass[k] = read(a.c.mass, p[k], b); });
+  };
+  if constexpr (NB > 0) {
+    sl.each([&](auto k, int b) { p[k] = raw_page(b); });
+    if (by_age) sl.each([&](auto k, int b) { age[k] = read(a.c.age, p[k], b); });
+    if (kBoth && by_mass) read_masses();
+    if (by_age) sl.each([&](auto k, int) { age[k] = age_keys(p[k], age[k]); });
   } else {
-    for (int w = tid; w < nw; w += kThreads) sl.keep[w] = 0;
+    for (int k = tid; k < 4 * nb; k += kThreads) sl.keep[k] = 0;
   }
-  // into LDS, eight reads of a thread at once
-  const auto stage = [&](const auto &read, const auto &key_of) {
-    constexpr int kAhead = 8;
-    for (int i0 = tid; i0 < n; i0 += kAhead * kThreads) {
-      int p[kAhead];
-      decltype(read(0, 0)) v[kAhead];
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) p[j] = raw_page(min(i0 + j * kThreads, n - 1));
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) v[j] = read(p[j], min(i0 + j * kThreads, n - 1));
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j)
-        if (i0 + j * kThreads < n) keys[i0 + j * kThreads] = is_page(p[j]) ? key_of(v[j]) : 0;
-    }
-    __syncthreads();
-  };
-  const auto select = [&](int which, int wanted, const uint32_t *own, const auto &read, const auto &key_of) {
-    if (wanted <= 0) return;
-    if constexpr (K == kInLds) stage(read, key_of);
-    take_largest(sl, wanted, [&](auto r, int w) {
-      if constexpr (K == kInRegisters) return own[r];
-      const int i = w * 64 + sl.lane;
-      if constexpr (K == kInLds) return keys[i];
-      const int p = raw_page(i);
-      return is_page(p) ? key_of(read(p, i)) : 0;
-    }, which, count, sh);
-  };
   __syncthreads();
   if (by_age) {
-    select(0, a.recent, age, read_age, age_key);
+    take_largest(sl, a.recent, [&](auto k, int b) {
+      if constexpr (NB > 0) return age[k];
+      const int page = raw_page(b);
+      return age_keys(page, read(a.c.age, page, b));
+    }, 0, count, sh);
   } else if (a.recent > 0) {
-    sl.each([&](auto r, int w) {
-      const int i = w * 64 + sl.lane;
-      sl.take(r, w, i < n && i >= n - a.recent);
+    sl.each([&](auto k, int b) {
+      const int before = n - a.recent - (b * kBlock + 4 * sl.lane);  // slots of this lane before the newest
+      sl.take(k, b, sl.is_free(k, b) & (before <= 0 ? 15u : before >= 4 ? 0u : 15u << before & 15u));
     });
     __syncthreads();
   }
-  select(1, budget - a.recent, mass, read_mass, mass_key);
-  // kept slots before each word
-  sl.each([&](auto r, int w) {
-    uint64_t m;
-    if constexpr (K == kInRegisters) {
-      m = __ballot(sl.kept >> r & 1);
-      if (sl.lane == 0) sl.keep[w] = m;
-    } else {
-      m = sl.keep[w];
+  if (by_mass) {
+    if constexpr (NB > 0) {
+      if (!kBoth) read_masses();
+      sl.each([&](auto k, int) { mass[k] = mass_keys(p[k], mass[k]); });
     }
-    if (sl.lane == 0) count[w] = __popcll(m);
+    take_largest(sl, budget - a.recent, [&](auto k, int b) {
+      if constexpr (NB > 0) return mass[k];
+      const int page = raw_page(b);
+      return mass_keys(page, read(a.c.mass, page, b));
+    }, 1, count, sh);
+  }
+  // kept slots before each block
+  sl.each([&](auto k, int b) {
+    int c = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint64_t m;
+      if constexpr (NB > 0) {
+        m = __ballot(sl.kept >> (4 * k + e) & 1);
+        if (sl.lane == 0) sl.keep[4 * b + e] = m;
+      } else {
+        m = sl.keep[4 * b + e];
+      }
+      c += __popcll(m);
+    }
+    if (sl.lane == 0) count[b] = c;
   });
-  sums_before(count, nw, sh);
-  const auto before = [&](int i) { return count[i >> 6] + __popcll(sl.keep[i >> 6] & ((1ull << (i & 63)) - 1)); };
+  sums_before(count, nb, sh);
+  const auto is_kept = [&](int i) { return sl.keep[4 * (i / kBlock) + (i & 3)] >> (i / 4 % 64) & 1; };
+  // kept slots of a block's lanes before `lane`
+  const auto lanes_before = [&](int b, int lane) {
+    int c = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c += __popcll(sl.keep[4 * b + e] & below(lane));
+    return c;
+  };
+  const auto before = [&](int i) {
+    int c = count[i / kBlock] + lanes_before(i / kBlock, i / 4 % 64);
+    for (int e = 0; e < (i & 3); ++e) c += is_kept((i & ~3) + e);
+    return c;
+  };
   const int low = before(budget);  // budget < n
   const bool few = budget - low <= kFewMoves && !a.to;
   for (int j = tid; j < budget; j += kThreads) {
-    if (sl.keep[j >> 6] >> (j & 63) & 1) {
+    if (is_kept(j)) {
       from[j] = j;
       continue;
     }
     // the hole's rank among the holes is that of its filler among the kept slots behind
-    const int hole = j - before(j), rank = low + hole;
-    int lo = budget >> 6, hi = nw - 1;  // the last word with at most `rank` kept slots before it
+    const int hole = j - before(j);
+    int rank = low + hole, lo = budget / kBlock, hi = nb - 1;  // the last block with at most `rank` kept slots before it
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
       if (count[mid] <= rank)
@@ -313,9 +373,14 @@ __global__ void __launch_bounds__(kThreads) select_kernel(EvictArgs a, int words
       else
         hi = mid - 1;
     }
-    uint64_t bits = sl.keep[lo];
-    for (int k = rank - count[lo]; k > 0; --k) bits &= bits - 1;
-    const int src = lo * 64 + __ffsll((unsigned long long)bits) - 1;
+    rank -= count[lo];
+    int lane = 0;  // the last lane with at most `rank` before it
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+      if (lanes_before(lo, lane + o) <= rank) lane += o;
+    rank -= lanes_before(lo, lane);
+    int src = lo * kBlock + 4 * lane;
+    for (; rank > 0 || !is_kept(src); ++src) rank -= (int)is_kept(src);
     from[j] = src;
     if (few) sh.moves[hole] = make_int2(src, j);
   }
@@ -374,17 +439,17 @@ __global__ void __launch_bounds__(256) move_kernel(EvictArgs a, int strips, Div 
 }  // namespace
 
 gsi_status launch_evict(const EvictArgs &a, int dtype, hipStream_t st) {
-  const int slots = a.c.most << a.c.shift, words = slots / 64 + 1;
+  const int slots = a.c.most << a.c.shift, blocks = slots / kBlock + 1;
   const int pieces = a.c.d * (dtype == GSI_FP32 ? 4 : 2) / 16, per = 256 / pieces * kMoveRows;
   const int64_t rows = (int64_t)a.c.S * a.c.heads, strips = (a.budget + per - 1) / per;
   if (rows * kThreads > kMostLaunch || rows * strips * 256 > kMostLaunch) return GSI_E_SHAPE;
-  const auto lds = ((size_t)words * 12 + 15) / 16 * 16;
-  if (slots <= kMostInRegisters)
-    select_kernel<kInRegisters><<<(unsigned)rows, kThreads, lds, st>>>(a, words, pieces);
-  else if (slots <= kMostInLds)
-    select_kernel<kInLds><<<(unsigned)rows, kThreads, lds + (size_t)slots * 4, st>>>(a, words, pieces);
+  const size_t lds = (size_t)blocks * 36;
+  if (slots <= kWaves * kBlock)
+    select_kernel<1><<<(unsigned)rows, kThreads, lds, st>>>(a, blocks, pieces);
+  else if (slots <= 8 * kWaves * kBlock)
+    select_kernel<8><<<(unsigned)rows, kThreads, lds, st>>>(a, blocks, pieces);
   else
-    select_kernel<kInMemory><<<(unsigned)rows, kThreads, lds, st>>>(a, words, pieces);
+    select_kernel<0><<<(unsigned)rows, kThreads, lds, st>>>(a, blocks, pieces);
   if (hipGetLastError() != hipSuccess) return GSI_E_HIP;
   // In place no more move than there are slots behind the budget; select_kernel
   // has made few (and made again they change nothing: nothing is moved from

@@ -401,6 +401,7 @@ def gsi_calibrate(A: torch.Tensor, V0: torch.Tensor, iters: int, V=None, ws=None
 # (a microsecond and a half of a call's five), where this torch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(where: str, fn, device: torch.device, stream, *args):
@@ -408,7 +409,7 @@ def _call(where: str, fn, device: torch.device, stream, *args):
     whatever device is current."""
     if device.type != "cuda":
         raise ValueError(f"{where}: tensors must be on the GPU")
-    index, current = device.index, torch.cuda.current_device()
+    index, current = device.index, _current_device()
     if stream is None:
         raw = _raw_stream(current if index is None else index)
     else:
@@ -679,37 +680,63 @@ class Cache:
             raise ValueError("the elements of an entry must be contiguous")
         self.struct = GsiCacheStruct(self.pages, self.page, self.heads, self.d, _dtype_code(K), 0, *strides[:3],
                                      _ptr(K), _ptr(V), _ptr(mass), _ptr(age))
+        self.needs = {}  # bytes of workspace by the sizes of a gsi_cache_attend call
+
+
+_INT = (1 << 31) - 1  # the library's sizes are int32, and ctypes drops the bits above without a word
 
 
 def _heads(t: torch.Tensor, name: str, dtype, device, d: int, T: int | None = None, n: int | None = None):
     """A [T][n][d] tensor whose heads are contiguous."""
-    if t.dim() != 3 or t.shape[2] != d or (T is not None and t.shape[0] != T) or (n is not None and t.shape[1] != n):
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != d or (T is not None and shape[0] != T) or (n is not None and shape[1] != n):
         raise ValueError(f"{name} must be [{'T' if T is None else T}][{'heads' if n is None else n}][{d}], "
-                         f"is {tuple(t.shape)}")
+                         f"is {tuple(shape)}")
     if t.dtype is not dtype or t.device != device:
         raise ValueError(f"{name} must be {dtype} on {device}, is {t.dtype} on {t.device}")
     s0, s1, s2 = t.stride()
     if s2 != 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
-    return GsiHeadsStruct(t.data_ptr(), s0, s1, t.shape[1], 0)
+    heads = shape[1]
+    if heads > _INT or shape[0] > _INT:
+        raise ValueError(f"{name}: sizes must be below 2^31, are {tuple(shape)}")
+    return GsiHeadsStruct(t.data_ptr(), s0, s1, heads)
+
+
+def _new_heads(like: torch.Tensor, T: int, n: int, d: int, stream):
+    """A new contiguous [T][n][d] tensor and its description."""
+    if stream is not None:
+        t = _empty((T, n, d), like.dtype, like.device, stream)
+    elif like.is_contiguous():
+        t = torch.empty_like(like)
+    else:
+        t = like.new_empty((T, n, d))
+    return t, GsiHeadsStruct(t.data_ptr(), n * d, d, n)
 
 
 def _table(t: torch.Tensor, name: str, device, S: int | None = None):
     """Page numbers [S][most], int32, rows contiguous."""
-    if t.dim() != 2 or t.dtype is not torch.int32 or t.device != device or (S is not None and t.shape[0] != S):
+    shape = t.shape
+    if len(shape) != 2 or t.dtype is not torch.int32 or t.device != device or (S is not None and shape[0] != S):
         raise ValueError(f"{name} must be int32 [{'S' if S is None else S}][most] on {device}, "
-                         f"is {t.dtype} {tuple(t.shape)} on {t.device}")
-    rows, most = t.shape
-    _sizes(name, rows, most)
-    if most > 1 and t.stride(1) != 1:
+                         f"is {t.dtype} {tuple(shape)} on {t.device}")
+    rows, most = shape
+    s0, s1 = t.stride()
+    if rows > _INT or most > _INT:
+        raise ValueError(f"{name}: sizes must be below 2^31, are {tuple(shape)}")
+    if s1 != 1 and most > 1:
         raise ValueError(f"{name}: the page numbers of a sequence must be contiguous")
-    return GsiTableStruct(t.data_ptr(), t.stride(0) if rows > 1 else most, rows, most)
+    return GsiTableStruct(t.data_ptr(), s0 if rows > 1 else most, rows, most)
 
 
-def _positions(t: torch.Tensor, T: int, device):
-    if t.dtype not in (torch.int32, torch.int64) or t.device != device or t.shape != (T,) or not t.is_contiguous():
+def _positions(t: torch.Tensor, T: int, device) -> int:
+    """The bytes of a position."""
+    dtype = t.dtype
+    if (dtype is not torch.int64 and dtype is not torch.int32) or t.device != device or t.shape != (T,) \
+            or not t.is_contiguous():
         raise ValueError(f"positions must be contiguous int32 or int64 ({T},) on {device}, "
                          f"is {t.dtype} {tuple(t.shape)} on {t.device}")
+    return 8 if dtype is torch.int64 else 4
 
 
 def gsi_rotary(r: Rotary, x: torch.Tensor, positions: torch.Tensor, y: torch.Tensor | None = None,
@@ -720,15 +747,16 @@ def gsi_rotary(r: Rotary, x: torch.Tensor, positions: torch.Tensor, y: torch.Ten
         raise ValueError(f"x must be [T][heads][d], is {tuple(x.shape)}")
     T, n, d = x.shape
     dtype, dev = x.dtype, x.device
-    _sizes("gsi_rotary", T, n, d)
     hx = _heads(x, "x", dtype, dev, d)
-    _positions(positions, T, dev)
+    pos_bytes = _positions(positions, T, dev)
     if r.device != dev:
         raise ValueError(f"the frequencies must be on {dev}, are on {r.device}")
+    code = _dtype_code(x)
     if y is None:
-        y = _empty((T, n, d), dtype, dev, stream)
-    _call("gsi_rotary", lib().gsi_rotary, dev, stream, r.struct, hx, _heads(y, "y", dtype, dev, d, T, n), T, d,
-          _dtype_code(x), positions.data_ptr(), positions.element_size())
+        y, hy = _new_heads(x, T, n, d, stream)
+    else:
+        hy = _heads(y, "y", dtype, dev, d, T, n)
+    _call("gsi_rotary", lib().gsi_rotary, dev, stream, r.struct, hx, hy, T, d, code, positions.data_ptr(), pos_bytes)
     return y
 
 
@@ -740,30 +768,28 @@ def gsi_cache_append(c: Cache, table: torch.Tensor, slots: torch.Tensor, k: torc
     seq[t] (None: t) of the table [S][most]; keys, and queries q [T][heads'][d],
     are turned by `rotary` at `positions`.  Rows whose slot has no page write
     nothing.  Returns the turned queries (q_out, which may be q), or None."""
-    dtype, dev, d = c.dtype, c.device, c.d
+    dtype, dev, d, heads = c.dtype, c.device, c.d, c.heads
+    hk = _heads(k, "k", dtype, dev, d, None, heads)
     T = k.shape[0]
-    _sizes("gsi_cache_append", T)
-    hk, hv = _heads(k, "k", dtype, dev, d, None, c.heads), _heads(v, "v", dtype, dev, d, T, c.heads)
+    hv = _heads(v, "v", dtype, dev, d, T, heads)
     pages = _table(table, "table", dev)
     _ints(slots, "slots", (T,), dev)
     if seq is not None:
         _ints(seq, "seq", (T,), dev)
-    if positions is not None:
-        _positions(positions, T, dev)
+    pos_bytes = 4 if positions is None else _positions(positions, T, dev)
     if rotary is not None and rotary.device != dev:
         raise ValueError(f"the frequencies must be on {dev}, are on {rotary.device}")
     hq = ho = None
     if q is not None:
         hq = _heads(q, "q", dtype, dev, d, T)
-        _sizes("gsi_cache_append", q.shape[1])
         if q_out is None:
-            q_out = _empty(q.shape, dtype, dev, stream)
-        ho = _heads(q_out, "q_out", dtype, dev, d, T, q.shape[1])
+            q_out, ho = _new_heads(q, T, hq.n, d, stream)
+        else:
+            ho = _heads(q_out, "q_out", dtype, dev, d, T, hq.n)
     elif q_out is not None:
         raise ValueError("q_out needs q")
     _call("gsi_cache_append", lib().gsi_cache_append, dev, stream, c.struct, pages, _ptr(seq), slots.data_ptr(), hk, hv,
-          T, None if rotary is None else rotary.struct, _ptr(positions),
-          4 if positions is None else positions.element_size(), hq, ho)
+          T, None if rotary is None else rotary.struct, _ptr(positions), pos_bytes, hq, ho)
     return q_out
 
 
@@ -783,28 +809,37 @@ def gsi_cache_attend(c: Cache, table: torch.Tensor, lengths: torch.Tensor, q: to
     gsi_cache_attend_workspace() bytes with any contents."""
     dtype, dev, d = c.dtype, c.device, c.d
     hq = _heads(q, "q", dtype, dev, d)
-    S, n = q.shape[:2]
-    _sizes("gsi_cache_attend", S, n, window)
+    S, n = q.shape[0], hq.n
+    if not 0 <= window <= _INT:
+        raise ValueError(f"window must be in 0..2^31 - 1, is {window}")
     pages = _table(table, "table", dev, S)
     _ints(lengths, "lengths", (S,), dev)
+    accumulate = bool(accumulate)
     if accumulate and c.mass is None:
         raise ValueError("accumulate needs a cache with mass")
     if out is None:
-        out = _empty((S, n, d), dtype, dev, stream)
-    ho = _heads(out, "out", dtype, dev, d, S, n)
+        out, ho = _new_heads(q, S, n, d, stream)
+    else:
+        ho = _heads(out, "out", dtype, dev, d, S, n)
     if lse is None:
-        lse = _empty((S, n), torch.float32, dev, stream)
+        lse = q.new_empty((S, n), dtype=torch.float32) if stream is None else _empty((S, n), torch.float32, dev, stream)
     elif lse.dtype is not torch.float32 or lse.device != dev or lse.shape != (S, n) or not lse.is_contiguous():
         raise ValueError(f"lse must be contiguous fp32 ({S}, {n}) on {dev}")
     if ws is None:
-        need = int(lib().gsi_cache_attend_workspace(c.struct, pages, n, int(accumulate)))
+        sizes = (S, pages.most, n, accumulate)
+        need = c.needs.get(sizes)
+        if need is None:
+            if len(c.needs) >= 256:
+                c.needs.clear()
+            need = c.needs[sizes] = int(lib().gsi_cache_attend_workspace(c.struct, pages, n, accumulate))
         if need:
             ws = _empty(need, torch.uint8, dev, stream)
-    elif ws.device != dev or not ws.is_contiguous():
-        raise ValueError(f"ws must be contiguous on {dev}")
+    else:
+        if ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be contiguous on {dev}")
+        need = ws.numel() * ws.element_size()
     _call("gsi_cache_attend", lib().gsi_cache_attend, dev, stream, c.struct, pages, lengths.data_ptr(), hq, ho,
-          d**-0.5 if scale is None else float(scale), int(window), int(accumulate), lse.data_ptr(), _ptr(ws),
-          0 if ws is None else ws.numel() * ws.element_size())
+          d**-0.5 if scale is None else float(scale), int(window), accumulate, lse.data_ptr(), _ptr(ws), need)
     return out, lse
 
 
@@ -817,13 +852,12 @@ def gsi_cache_evict(c: Cache, table: torch.Tensor, lengths: torch.Tensor, budget
     [S], moved [S][heads][budget]: the slot each slot's entry came from, or -1)."""
     dev = c.device
     pages = _table(table, "table", dev)
-    S = table.shape[0]
-    _sizes("gsi_cache_evict", budget, recent)
+    S = pages.S
     _ints(lengths, "lengths", (S,), dev)
     if c.mass is None:
         raise ValueError("eviction needs a cache with mass")
-    if budget < 1:
-        raise ValueError(f"budget must be at least 1, is {budget}")
+    if not 1 <= budget <= _INT or not 0 <= recent <= budget:
+        raise ValueError(f"budget must be in 1..2^31 - 1 and recent in 0..budget, are {budget} and {recent}")
     target = None if to is None else _table(to, "to", dev, S)
     if lengths_out is None:
         lengths_out = _empty(S, torch.int32, dev, stream)
