@@ -78,18 +78,6 @@ __device__ __forceinline__ Span span_of(const AttendArgs &a, int n) {
   return r;
 }
 
-// Sums over the lanes up to and with this one, in registers (a row's lanes by
-// shifts, then the rows' last lanes to the rows behind).
-__device__ __forceinline__ int sums_to(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr 1
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast 15, rows 1 and 3
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast 31, rows 2 and 3
-  return v;
-}
-
 // A sequence, its length, and the things of those before it.
 struct Sequence {
   int s, n, before;

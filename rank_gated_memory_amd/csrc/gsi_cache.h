@@ -93,5 +93,21 @@ __device__ __forceinline__ int64_t number_at(const Pool &c, int p, int h, int i)
   return (((int64_t)p * c.heads + h) << c.shift) + (i & ((1 << c.shift) - 1));
 }
 
+// Sums over the lanes up to and with this one, in registers (a row's lanes by
+// shifts, then the rows' last lanes to the rows behind).
+template <int None, typename F>
+__device__ __forceinline__ int joined_to(int v, const F &f) {  // of any f with f(None, x) = x
+  v = f(v, __builtin_amdgcn_update_dpp(None, v, 0x111, 0xf, 0xf, false));  // row_shr 1
+  v = f(v, __builtin_amdgcn_update_dpp(None, v, 0x112, 0xf, 0xf, false));
+  v = f(v, __builtin_amdgcn_update_dpp(None, v, 0x114, 0xf, 0xf, false));
+  v = f(v, __builtin_amdgcn_update_dpp(None, v, 0x118, 0xf, 0xf, false));
+  v = f(v, __builtin_amdgcn_update_dpp(None, v, 0x142, 0xa, 0xf, false));  // row_bcast 15, rows 1 and 3
+  v = f(v, __builtin_amdgcn_update_dpp(None, v, 0x143, 0xc, 0xf, false));  // row_bcast 31, rows 2 and 3
+  return v;
+}
+__device__ __forceinline__ int sums_to(int v) {
+  return joined_to<0>(v, [](int a, int b) { return a + b; });
+}
+
 }  // namespace
 }  // namespace gsi

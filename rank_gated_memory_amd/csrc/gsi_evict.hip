@@ -14,6 +14,7 @@
 // reads them; up to 32768 slots stay in registers and are read once.  A call for
 // a few thousand slots is bound by the latency of these reads and of the dozen
 // barriers behind them, one for long sequences by the counting in LDS.
+#include <algorithm>
 #include <utility>
 
 #include "gsi_cache.h"
@@ -52,12 +53,7 @@ __device__ void sums_before(int *counts, int nb, Shared &sh) {
   __syncthreads();
   int sum = 0;
   for (int b = lo; b < hi; ++b) sum += counts[b];
-  int incl = sum;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(incl, o, 64);
-    if (lane >= o) incl += u;
-  }
+  const int incl = sums_to(sum);
   if (lane == 63) sh.part[wave] = incl;
   __syncthreads();
   int run = incl - sum;
@@ -139,42 +135,56 @@ __device__ __forceinline__ void take_largest(Slots<NB> &sl, int count, const Key
       any |= is_free >> e & 1 ? key.v[e] : 0u;
     }
   });
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    all &= __shfl_xor(all, o, 64);
-    any |= __shfl_xor(any, o, 64);
-  }
-  if (lane == 0) sh.all[which][sl.wave] = all, sh.any[which][sl.wave] = any;
+  all = joined_to<-1>(all, [](int x, int y) { return x & y; });
+  any = joined_to<0>(any, [](int x, int y) { return x | y; });
+  if (lane == 63) sh.all[which][sl.wave] = all, sh.any[which][sl.wave] = any;
   __syncthreads();
+  all = sh.all[which][0], any = sh.any[which][0];
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) all &= sh.all[which][w], any |= sh.any[which][w];
+  for (int w = 1; w < kWaves; ++w) all &= sh.all[which][w], any |= sh.any[which][w];
   const uint32_t differ = all ^ any;
-  int shift = 32 - __clz(differ), need = count;  // bits from `shift` on are known: those of prefix
-  uint64_t prefix = (uint64_t)all >> shift;
+  int shift = 32 - __clz(differ), need = count;
+  // keys from `base` on to base + span agree with the threshold so far
+  uint32_t span = shift == 32 ? ~0u : (1u << shift) - 1, base = all & ~span;
   bool tied = true;  // more slots at the threshold than are taken
   for (int pass = 0; shift > 0 && tied; ++pass) {
     const int low = max(shift - 8, 0);
-    const uint32_t mask = (1u << (shift - low)) - 1;
     int *const hist = sh.hist[which][pass];
     sl.each([&](auto k, int b) {
       const uint32_t is_free = sl.is_free(k, b);
       const Four key = keys(k, b);
+      // Neighbours often agree in these bits (ages are slots at first), and lanes
+      // at one bin take their turns: a lane's run of one bin is counted at once,
+      // and of the lanes' last runs those of the first lane's bin.
+      int bin = 0, c = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if ((is_free >> e & 1) && (uint64_t)key.v[e] >> shift == prefix)
-          atomicAdd(&hist[key.v[e] >> low & mask], 1);  // integers: any order
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t off = key.v[e] - base;
+        const bool in = (is_free >> e & 1) && off <= span;
+        if (in && c > 0 && (int)(off >> low) != bin) {
+          atomicAdd(&hist[bin], c);  // integers: any order
+          c = 0;
+        }
+        bin = in ? off >> low : bin;
+        c += in;
+      }
+      const uint64_t last = __ballot(c > 0);
+      if (last == 0) return;
+      const int first = __ffsll((unsigned long long)last) - 1, common = __builtin_amdgcn_readlane(bin, first);
+      const uint64_t same = last & __ballot(bin == common);
+      const int sum = __popcll(same & __ballot(c & 1)) + 2 * __popcll(same & __ballot(c & 2)) +
+                      4 * __popcll(same & __ballot(c & 4));
+      if (lane == first)
+        atomicAdd(&hist[common], sum);
+      else if (c > 0 && bin != common)
+        atomicAdd(&hist[bin], c);
     });
     __syncthreads();
     // from the top, four bins a lane: the bin where the running count reaches
     // `need`; every wavefront by itself
     const int4 h = *reinterpret_cast<const int4 *>(hist + 252 - 4 * lane);
     const int sum = h.x + h.y + h.z + h.w;
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int u = __shfl_up(incl, o, 64);
-      if (lane >= o) incl += u;
-    }
+    const int incl = sums_to(sum);
     const int at = __ffsll((unsigned long long)__ballot(incl >= need)) - 1;
     int above = __builtin_amdgcn_readlane(incl - sum, at), bin = 255 - 4 * at;
     int c = __builtin_amdgcn_readlane(h.w, at);
@@ -187,7 +197,8 @@ __device__ __forceinline__ void take_largest(Slots<NB> &sl, int count, const Key
     }
     need -= above;
     tied = c > need;
-    prefix = prefix << (shift - low) | (uint32_t)bin;
+    base += (uint32_t)bin << low;
+    span = (1u << low) - 1;
     shift = low;
   }
   if (!tied) {
@@ -195,14 +206,14 @@ __device__ __forceinline__ void take_largest(Slots<NB> &sl, int count, const Key
       const Four key = keys(k, b);
       uint32_t mine = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) mine |= (uint32_t)((uint64_t)key.v[e] >> shift >= prefix) << e;
+      for (int e = 0; e < 4; ++e) mine |= (uint32_t)(key.v[e] >= base) << e;
       sl.take(k, b, mine & sl.is_free(k, b));
     });
   } else {  // the first `need` slots with this very key
     const auto same_of = [&](const Four &key, uint32_t is_free) {
       uint32_t same = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) same |= (uint32_t)(key.v[e] == prefix) << e;
+      for (int e = 0; e < 4; ++e) same |= (uint32_t)(key.v[e] == base) << e;
       return same & is_free;
     };
     sl.each([&](auto k, int b) {
@@ -223,7 +234,7 @@ __device__ __forceinline__ void take_largest(Slots<NB> &sl, int count, const Key
       uint32_t mine = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if (key.v[e] > prefix || ((same >> e & 1) && rank < need)) mine |= 1u << e;
+        if (key.v[e] > base || ((same >> e & 1) && rank < need)) mine |= 1u << e;
         rank += same >> e & 1;
       }
       sl.take(k, b, mine & is_free);
@@ -245,9 +256,10 @@ __device__ __forceinline__ void move_numbers(const EvictArgs &a, int64_t from, i
   if (a.c.age) a.c.age[to] = a.c.age[from];
 }
 
-// blocks: for which there is LDS; pieces: of 16 bytes of a key.
+// blocks: for which there is LDS; holes: for which there is; pieces: of 16 bytes
+// of a key.
 template <int NB>
-__global__ void __launch_bounds__(kThreads) select_kernel(EvictArgs a, int blocks, int pieces) {
+__global__ void __launch_bounds__(kThreads) select_kernel(EvictArgs a, int blocks, int holes, int pieces) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ __attribute__((aligned(16))) Shared sh;
   const int s = blockIdx.x / a.c.heads, h = blockIdx.x - s * a.c.heads, tid = threadIdx.x;
@@ -287,7 +299,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(EvictArgs a, int block
   };
   for (int k = tid; k < 2 * 4 * 256; k += kThreads) (&sh.hist[0][0][0])[k] = 0;
   // All reads of a selection at once, those of both where there are registers.
-  constexpr bool kBoth = NB <= 1;
+  constexpr bool kBoth = NB <= 8;
   int p[NB > 0 ? NB : 1];
   Four age[NB > 0 ? NB : 1], mass[NB > 0 ? NB : 1];
   const auto read_masses = [&] {
@@ -343,49 +355,62 @@ __global__ void __launch_bounds__(kThreads) select_kernel(EvictArgs a, int block
     if (sl.lane == 0) count[b] = c;
   });
   sums_before(count, nb, sh);
-  const auto is_kept = [&](int i) { return sl.keep[4 * (i / kBlock) + (i & 3)] >> (i / 4 % 64) & 1; };
-  // kept slots of a block's lanes before `lane`
-  const auto lanes_before = [&](int b, int lane) {
-    int c = 0;
+  // of a lane's four slots, the kept ones and how many are kept before them
+  const auto kept_of = [&](int b, int lane, uint32_t *kept) {
+    int c = count[b];
+    *kept = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) c += __popcll(sl.keep[4 * b + e] & below(lane));
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t w = sl.keep[4 * b + e];
+      c += __popcll(w & below(lane));
+      *kept |= (uint32_t)(w >> lane & 1) << e;
+    }
     return c;
   };
-  const auto before = [&](int i) {
-    int c = count[i / kBlock] + lanes_before(i / kBlock, i / 4 % 64);
-    for (int e = 0; e < (i & 3); ++e) c += is_kept((i & ~3) + e);
-    return c;
-  };
-  const int low = before(budget);  // budget < n
+  uint32_t kept;
+  int low = kept_of(budget / kBlock, budget / 4 % 64, &kept);  // kept below the budget; budget < n
+  low += __popc(kept & ((1u << (budget & 3)) - 1));
   const bool few = budget - low <= kFewMoves && !a.to;
-  for (int j = tid; j < budget; j += kThreads) {
-    if (is_kept(j)) {
-      from[j] = j;
-      continue;
-    }
-    // the hole's rank among the holes is that of its filler among the kept slots behind
-    const int hole = j - before(j);
-    int rank = low + hole, lo = budget / kBlock, hi = nb - 1;  // the last block with at most `rank` kept slots before it
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (count[mid] <= rank)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    rank -= count[lo];
-    int lane = 0;  // the last lane with at most `rank` before it
+  // The holes below the budget and the kept slots behind it, both in order, go
+  // together: through a list of the holes in LDS, `holes` at a time.
+  int *const list = count + blocks;
+  for (int first = 0; first == 0 || first < budget - low; first += holes) {
+    sl.each([&](auto, int b) {
+      const int i0 = b * kBlock + 4 * sl.lane;
+      if (b * kBlock >= budget) return;
+      uint32_t mine;
+      int hole = i0 - kept_of(b, sl.lane, &mine) - first;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-      if (lanes_before(lo, lane + o) <= rank) lane += o;
-    rank -= lanes_before(lo, lane);
-    int src = lo * kBlock + 4 * lane;
-    for (; rank > 0 || !is_kept(src); ++src) rank -= (int)is_kept(src);
-    from[j] = src;
-    if (few) sh.moves[hole] = make_int2(src, j);
+      for (int e = 0; e < 4; ++e) {
+        if (i0 + e >= budget) continue;
+        if (mine >> e & 1) {
+          if (first == 0) from[i0 + e] = i0 + e;
+        } else {
+          if (hole >= 0 && hole < holes) list[hole] = i0 + e;
+          ++hole;
+        }
+      }
+    });
+    __syncthreads();
+    sl.each([&](auto, int b) {
+      if ((b + 1) * kBlock <= budget) return;
+      const int i0 = b * kBlock + 4 * sl.lane;
+      uint32_t mine;
+      int rank = kept_of(b, sl.lane, &mine) - low;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (!(mine >> e & 1)) continue;
+        const int hole = rank - first;
+        if (i0 + e >= budget && hole >= 0 && hole < holes) {
+          from[list[hole]] = i0 + e;
+          if (few) sh.moves[rank] = make_int2(i0 + e, list[hole]);
+        }
+        ++rank;
+      }
+    });
+    __syncthreads();
   }
   if (!few) return;
-  __syncthreads();
   for (int k = sl.wave; k < budget - low; k += kWaves) {
     const int src = sh.moves[k].x, j = sh.moves[k].y, p = page_of(a.c, s, src), t = page_of(a.c, s, j);
     if (p < 0 || t < 0) continue;
@@ -394,7 +419,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(EvictArgs a, int block
   }
 }
 
-constexpr int kMoveRows = 4;  // of a thread
+constexpr int kMoveRows = 2;  // of a thread
 
 // 16 bytes of a key and of a value per thread and row; `side` rows at a time.
 __global__ void __launch_bounds__(256) move_kernel(EvictArgs a, int strips, Div pieces) {
@@ -443,13 +468,14 @@ gsi_status launch_evict(const EvictArgs &a, int dtype, hipStream_t st) {
   const int pieces = a.c.d * (dtype == GSI_FP32 ? 4 : 2) / 16, per = 256 / pieces * kMoveRows;
   const int64_t rows = (int64_t)a.c.S * a.c.heads, strips = (a.budget + per - 1) / per;
   if (rows * kThreads > kMostLaunch || rows * strips * 256 > kMostLaunch) return GSI_E_SHAPE;
-  const size_t lds = (size_t)blocks * 36;
+  const int holes = std::max(1, std::min({a.budget, slots - a.budget, 8192}));
+  const size_t lds = (size_t)blocks * 36 + (size_t)holes * 4;
   if (slots <= kWaves * kBlock)
-    select_kernel<1><<<(unsigned)rows, kThreads, lds, st>>>(a, blocks, pieces);
+    select_kernel<1><<<(unsigned)rows, kThreads, lds, st>>>(a, blocks, holes, pieces);
   else if (slots <= 8 * kWaves * kBlock)
-    select_kernel<8><<<(unsigned)rows, kThreads, lds, st>>>(a, blocks, pieces);
+    select_kernel<8><<<(unsigned)rows, kThreads, lds, st>>>(a, blocks, holes, pieces);
   else
-    select_kernel<0><<<(unsigned)rows, kThreads, lds, st>>>(a, blocks, pieces);
+    select_kernel<0><<<(unsigned)rows, kThreads, lds, st>>>(a, blocks, holes, pieces);
   if (hipGetLastError() != hipSuccess) return GSI_E_HIP;
   // In place no more move than there are slots behind the budget; select_kernel
   // has made few (and made again they change nothing: nothing is moved from
