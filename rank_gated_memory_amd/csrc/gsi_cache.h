@@ -21,7 +21,7 @@ struct Pool {
   int32_t pages, shift, heads, d, S, most;  // a page has 1 << shift slots
 };
 
-// Quotients of numbers below 2^24 by a divisor of at most 256.
+// Quotients n / by, exact where n * by stays below 2^32.
 struct Div {
   uint32_t by, magic;
 };
