@@ -131,7 +131,10 @@ struct Counted {
 // A quotient of wave-uniform numbers, in 32 bits where they are: a division of
 // 64 bits takes a good part of a microsecond.
 __device__ __forceinline__ int64_t over(int64_t n, int64_t by) {
-  return (uint64_t)(n | by) >> 32 ? n / by : (int64_t)((uint32_t)n / (uint32_t)by);
+  const int64_t q = (uint64_t)(n | by) >> 32 ? n / by : (int64_t)((uint32_t)n / (uint32_t)by);
+  // a division's steps are vector instructions: back to scalar registers
+  return (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)q) |
+         (int64_t)__builtin_amdgcn_readfirstlane((int)(q >> 32)) << 32;
 }
 
 // Shares of `all` units: share b begins at unit b all / shares.
@@ -176,7 +179,7 @@ __device__ __forceinline__ void finish_row(const AttendArgs &a, const Plan &p, i
 // KS: the head's size in units of 32, rounded up.  Uniform: a page holds whole
 // steps, so that a step has one page; otherwise each 8 slots have one.
 template <typename E, int KS, bool Uniform>
-__global__ void __launch_bounds__(kThreads, KS <= 3 ? 3 : KS <= 4 ? 2 : 1) attend_kernel(AttendArgs a, Plan p) {
+__global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) attend_kernel(AttendArgs a, Plan p) {
   constexpr bool f32 = sizeof(E) == 4;
   constexpr int es = sizeof(E), step = kStep<E>;
   constexpr int KT = f32 ? 1 : 2;          // tiles of keys of a step
@@ -185,6 +188,9 @@ __global__ void __launch_bounds__(kThreads, KS <= 3 ? 3 : KS <= 4 ? 2 : 1) atten
   constexpr int VT = f32 ? 4 : 8;          // slots whose scores and values a lane holds
   constexpr int NC = 2 * KS;               // columns of a value that a lane holds
   constexpr int VD = NC * es / 4;          // dwords
+  // whether the next segment's first loads go out before the present one is done:
+  // for large fp32 heads there are no registers for it
+  constexpr bool kAhead = !f32 || KS <= 3;
   constexpr int GC = CH - (f32 ? 2 : 1) * (KS > 4 ? 2 : 1);  // pieces from here on may lie behind the key
   __shared__ float red[kWaves][16][32 * KS];
   __shared__ float red_m[kWaves][16], red_l[kWaves][16];
@@ -196,11 +202,34 @@ __global__ void __launch_bounds__(kThreads, KS <= 3 ? 3 : KS <= 4 ? 2 : 1) atten
   const Counted counted(a, units_of);
   const Shares sh = shares_of(a, p, counted.sum);
   if (share >= sh.of) return;
-  int64_t unit = sh.begin(share);
-  const int64_t unit_end = sh.begin(share + 1);
-  const Sequence at = counted.of_thing((int)over(unit, rows));
-  int s = at.s, before = at.before;
-  Span sp = span_of<E>(a, at.n);
+  int64_t left = sh.begin(share + 1);  // units of the share behind the present segment
+
+  // A row's part in this share: its units from `skip` on, `mine` of them, and of
+  // this wavefront the steps st, st + kWaves, .. below end.
+  struct Segment {
+    int s, row_at, kh, tile, skip, mine, st, end;
+    Span sp;
+  };
+  const auto place = [&](Segment &g) {
+    g.kh = p.tiles == 1 ? g.row_at : (int)over(g.row_at, p.tiles);
+    g.tile = g.row_at - g.kh * p.tiles;
+    g.mine = (int)min((int64_t)(g.sp.units - g.skip), left);
+    g.st = g.sp.lo + g.skip * kWaves + wave;
+    g.end = g.sp.lo + min(g.sp.steps, (g.skip + g.mine) * kWaves);
+    left -= g.mine;
+  };
+  Segment seg;
+  {
+    const int64_t unit = sh.begin(share);
+    const Sequence at = counted.of_thing((int)over(unit, rows));
+    const int64_t in_rows = unit - (int64_t)at.before * rows;
+    seg.s = at.s;
+    seg.sp = span_of<E>(a, at.n);
+    seg.row_at = (int)over(in_rows, seg.sp.units);
+    seg.skip = (int)(in_rows - (int64_t)seg.row_at * seg.sp.units);
+    left -= unit;
+    place(seg);
+  }
 
   // this lane's first column, and its offsets from the start of a step (of a
   // block of 8 slots): the last run of columns ends with the value
@@ -208,30 +237,9 @@ __global__ void __launch_bounds__(kThreads, KS <= 3 ? 3 : KS <= 4 ? 2 : 1) atten
   const int ktoken = f32 ? (Uniform ? l16 : l16 & 7) : (Uniform ? 8 * (l16 >> 2) : 0) + (l16 & 3);
   const int vtoken = f32 ? (Uniform ? 4 * quad : 4 * (quad & 1)) : (Uniform ? 8 * quad : 0);
   const int kblock = f32 ? l16 >> 3 : l16 >> 2, vblock = f32 ? quad >> 1 : quad;
-  const uint32_t ss = (uint32_t)a.c.slot_stride;
+  const uint32_t ss = (uint32_t)a.c.slot_stride, pages = a.c.pages;
   const uint32_t ko = ktoken * ss + 16 * quad, vo = vtoken * ss + col0 * es;
   const float scale2 = a.scale * 1.4426950408889634f;
-
-  for (;;) {
-  const int64_t in_rows = unit - (int64_t)before * rows;
-  const int row_at = (int)over(in_rows, sp.units);
-  const int skip = (int)(in_rows - (int64_t)row_at * sp.units);  // units of the row that earlier workgroups have
-  const int mine = (int)min((int64_t)(sp.units - skip), unit_end - unit);
-  const bool whole = mine == sp.units;
-  const int kh = row_at / p.tiles, tile = row_at - kh * p.tiles;
-  const int live = min(16, a.group - tile * 16);  // query heads of this tile
-  const int head0 = kh * a.group + tile * 16;
-
-  // this lane's query head as the operand B of S^T
-  u32x4_t q[CH];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int e = c * CE + 16 / es * quad;
-    q[c] = u32x4_t{0, 0, 0, 0};
-    if (l16 < live && e < d)
-      q[c] = *reinterpret_cast<const u32x4_t *>(a.q.p + s * a.q.row + (head0 + l16) * a.q.head + e * es);
-  }
-  const int32_t *const table = a.c.table + s * a.c.ld;
 
   // The page numbers of this lane's keys and values, as the table has them: they
   // are checked where they are used, a step later, so that nothing waits for
@@ -239,55 +247,115 @@ __global__ void __launch_bounds__(kThreads, KS <= 3 ? 3 : KS <= 4 ? 2 : 1) atten
   struct Where {
     uint32_t k, v;
   };
-  const auto pages_of = [&](int st) {
-    const auto page = [&](int t) { return (uint32_t)table[min(t, sp.n - 1) >> a.c.shift]; };
+  const auto pages_of = [&](const Segment &g, int st) {
+    const int32_t *const table = a.c.table + g.s * a.c.ld;
+    const auto page = [&](int t) { return (uint32_t)table[min(t, g.sp.n - 1) >> a.c.shift]; };
     if constexpr (Uniform) {
-      const uint32_t g = page(st * step);
-      return Where{g, g};
+      const uint32_t w = page(st * step);
+      return Where{w, w};
     } else {
       return Where{page(st * step + 8 * kblock), page(st * step + 8 * vblock)};
     }
   };
-  const uint32_t pages = a.c.pages;
-  const auto start_of = [&](uint32_t g, int t) {
-    if constexpr (Uniform) g = __builtin_amdgcn_readfirstlane(g);
-    return entry_at(a.c, g < pages ? g : 0, kh, t);
+  const auto start_of = [&](const Segment &g, uint32_t page, int t) {
+    if constexpr (Uniform) page = __builtin_amdgcn_readfirstlane(page);
+    return entry_at(a.c, page < pages ? page : 0, g.kh, t);
   };
+  u32x4_t q[CH];  // this lane's query head as the operand B of S^T
   u32x4_t k[KT][CH];
   uint32_t v[VT][VD];
-  const auto load_k = [&](const Where &w, int st) {
-    const uint8_t *const at = a.c.K + start_of(w.k, st * step + (Uniform ? 0 : 8 * kblock));
+  const auto load_q = [&](const Segment &g) {
+    const int live = a.group - g.tile * 16;
+    const uint8_t *const at = a.q.p + g.s * a.q.row + (g.kh * a.group + g.tile * 16 + l16) * a.q.head;
 #pragma unroll
-    for (int u = 0; u < KT; ++u)
+    for (int c = 0; c < CH; ++c) {
+      const int e = c * CE + 16 / es * quad;
+      q[c] = u32x4_t{0, 0, 0, 0};
+      if (l16 < live && e < d) q[c] = *reinterpret_cast<const u32x4_t *>(at + e * es);
+    }
+  };
+  // The addresses are formed one after the other: all at once they would take as
+  // many registers as what they load.
+  const auto here = [](const uint8_t *at) {
+    if constexpr (Uniform) {
+      const uint64_t p = reinterpret_cast<uint64_t>(at);
+      return reinterpret_cast<const uint8_t *>((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)p) |
+                                               (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(p >> 32)) << 32);
+    } else {
+      asm volatile("" : "+v"(at));
+      return at;
+    }
+  };
+  const auto load_k = [&](const Segment &g, const Where &w, int st) {
+    const uint8_t *at = here(a.c.K + start_of(g, w.k, st * step + (Uniform ? 0 : 8 * kblock)));
+#pragma unroll
+    for (int u = 0; u < KT; ++u) {
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const uint32_t in = c < GC || c * CE + 16 / es * quad < d ? c * 64 : 0;
-        k[u][c] = *reinterpret_cast<const u32x4_t *>(at + 4 * u * (uint64_t)ss + (ko + in));
+        k[u][c] = *reinterpret_cast<const u32x4_t *>(at + (ko + in));
       }
+      if (u + 1 < KT) at = Uniform ? at + 4 * (uint64_t)ss : here(at + 4 * (uint64_t)ss);
+    }
   };
-  const auto load_v = [&](const Where &w, int st) {
-    const uint8_t *const at = a.c.V + start_of(w.v, st * step + (Uniform ? 0 : 8 * vblock));
+  const auto load_v = [&](const Segment &g, const Where &w, int st) {
+    const uint8_t *at = here(a.c.V + start_of(g, w.v, st * step + (Uniform ? 0 : 8 * vblock)));
     struct Run {
       uint32_t w[VD];
     };
 #pragma unroll
-    for (int e = 0; e < VT; ++e) __builtin_memcpy(v[e], at + e * (uint64_t)ss + vo, sizeof(Run));
+    for (int e = 0; e < VT; ++e) {
+      __builtin_memcpy(v[e], at + vo, sizeof(Run));
+      at = Uniform ? at + ss : here(at + ss);
+    }
   };
+
+  Where now{}, next{};
+  if (seg.st < seg.end) {
+    now = pages_of(seg, seg.st);
+    next = pages_of(seg, seg.st + kWaves);
+  }
+  load_q(seg);
+  if (seg.st < seg.end) {
+    load_k(seg, now, seg.st);
+    load_v(seg, now, seg.st);
+  }
+  for (;;) {
+  // The next segment, whose first loads go out as this one's last are used: while
+  // the wavefronts are joined nothing has to be waited for.
+  const bool last = left == 0;
+  Segment then = seg;
+  Where then_now{}, then_next{};
+  if (!last) {  // then this segment ends its row
+    if (++then.row_at == rows) {
+      then.row_at = 0;
+      then.sp = span_of<E>(a, __builtin_amdgcn_readfirstlane(clamped_length(a.c, a.lengths, ++then.s)));
+    }
+    then.skip = 0;
+    place(then);
+    if (then.st < then.end) {
+      then_now = pages_of(then, then.st);
+      then_next = pages_of(then, then.st + kWaves);
+    }
+  }
+  const bool ahead = !last && then.st < then.end;
+  const bool whole = seg.mine == seg.sp.units;
+  const int s = seg.s, live = min(16, a.group - seg.tile * 16);  // query heads of this tile
+  const int head0 = seg.kh * a.group + seg.tile * 16;
+  const Span &sp = seg.sp;
 
   f32x4_t acc[NC];
 #pragma unroll
   for (int j = 0; j < NC; ++j) acc[j] = f32x4_t{0, 0, 0, 0};
   float m = -INFINITY, sum = 0.f;  // of head l16; the sum over this lane's slots
-  const int end = sp.lo + min(sp.steps, (skip + mine) * kWaves);
-  int st = sp.lo + skip * kWaves + wave;
-  Where now{}, next{};
-  if (st < end) {
-    now = pages_of(st);
-    next = pages_of(st + kWaves);
-    load_k(now, st);
-    load_v(now, st);
+  if (kAhead && seg.st >= seg.end && !last) {  // no step of this wavefront
+    load_q(then);
+    if (ahead) {
+      load_k(then, then_now, then.st);
+      load_v(then, then_now, then.st);
+    }
   }
-  for (; st < end; st += kWaves) {
+  for (int st = seg.st; st < seg.end; st += kWaves) {
     f32x4_t sc[KT];
 #pragma unroll
     for (int u = 0; u < KT; ++u) {
@@ -307,9 +375,14 @@ __global__ void __launch_bounds__(kThreads, KS <= 3 ? 3 : KS <= 4 ? 2 : 1) atten
       }
     }
     // the next step's keys into the registers that have just been read
-    const bool more = st + kWaves < end;
-    const Where after = pages_of(st + 2 * kWaves);
-    if (more) load_k(next, st + kWaves);
+    const bool more = st + kWaves < seg.end;
+    const Where after = pages_of(seg, st + 2 * kWaves);
+    if (more) {
+      load_k(seg, next, st + kWaves);
+    } else if (kAhead && !last) {
+      load_q(then);
+      if (ahead) load_k(then, then_now, then.st);
+    }
     float w[VT];
 #pragma unroll
     for (int i = 0; i < VT; ++i) w[i] = sc[i / 4][i % 4] * scale2;
@@ -378,7 +451,10 @@ __global__ void __launch_bounds__(kThreads, KS <= 3 ? 3 : KS <= 4 ? 2 : 1) atten
         acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, __builtin_bit_cast(bf16x8_t, o), acc[j], 0, 0, 0);
       }
     }
-    if (more) load_v(next, st + kWaves);
+    if (more)
+      load_v(seg, next, st + kWaves);
+    else if (kAhead && ahead)
+      load_v(then, then_now, then.st);
     now = next;
     next = after;
   }
@@ -398,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, KS <= 3 ? 3 : KS <= 4 ? 2 : 1) atten
       for (int j = 0; j < NC; ++j) red[wave][h][col0 + j] = acc[j][i] * f;
   }
   __syncthreads();
-  const int64_t slot = 2 * (int64_t)share + (skip == 0);
+  const int64_t slot = 2 * (int64_t)share + (seg.skip == 0);
   for (int h = wave; h < live; h += kWaves) {
     float top = red_m[0][h], total = 0.f;
     for (int w = 1; w < kWaves; ++w) top = fmaxf(top, red_m[w][h]);
@@ -421,11 +497,15 @@ __global__ void __launch_bounds__(kThreads, KS <= 3 ? 3 : KS <= 4 ? 2 : 1) atten
         p.partial[(slot * 16 + h) * d + c] = o;
     }
   }
-  unit += mine;
-  if (unit >= unit_end) return;
-  if (row_at == rows - 1) {  // the row is done, and was the sequence's last
-    before += sp.units;
-    sp = span_of<E>(a, clamped_length(a.c, a.lengths, ++s));
+  if (last) return;
+  seg = then;
+  now = then_now, next = then_next;
+  if (!kAhead) {
+    load_q(seg);
+    if (ahead) {
+      load_k(seg, now, seg.st);
+      load_v(seg, now, seg.st);
+    }
   }
   __syncthreads();  // the sums have been read
   }
@@ -534,51 +614,71 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttendArgs a, Plan p, bo
   for (int k = 0; k < 4; ++k) out[k] = (E)(total == 0.f ? 0.f : v[k] / total);
 }
 
-constexpr int kMassSlots = 256;  // of a workgroup at a time
+constexpr int kMassSlots = 256;  // of a strip
 constexpr int kMassGrid = 2048;
 
-// Workgroups walk the strips of kMassSlots slots of all sequences and key heads;
-// a strip's query heads are dealt to the wavefronts, four slots a lane, and a
-// thread adds up a slot.
-__global__ void __launch_bounds__(kThreads) mass_kernel(AttendArgs a, Plan p) {
-  __shared__ float sums[kWaves][kMassSlots];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+// The strips of kMassSlots slots of all sequences and key heads, four slots a
+// lane, which lie in one page.  `sharers` wavefronts (1, 2 or 4) divide a strip's
+// query heads.  Bound by latency: lengths, pages, then masses and scores.  (A
+// strip for a whole workgroup, one slot a thread: 14.5 us for 64 ragged
+// sequences of 40 heads, 4.0 us for 24 of 2 heads of 32.)
+__global__ void __launch_bounds__(kThreads) mass_kernel(AttendArgs a, Plan p, int sharers) {
+  __shared__ __attribute__((aligned(16))) float sums[kWaves][kMassSlots];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int own = wave & (sharers - 1), at_once = kWaves / sharers;
   const auto first_of = [&](int n) { return a.window > 0 ? max(0, n - a.window) : 0; };
   const auto strips = [&](int n) { return (n + kMassSlots - 1) / kMassSlots - first_of(n) / kMassSlots; };
   const Counted counted(a, strips);
   const int64_t all = (int64_t)counted.sum * a.c.heads;
-  for (int64_t at = blockIdx.x; at < all; at += gridDim.x) {
-    const Sequence seq = counted.of_thing((int)over(at, a.c.heads));
+  for (int64_t at0 = (int64_t)blockIdx.x * at_once; at0 < all; at0 += (int64_t)gridDim.x * at_once) {
+    const int64_t at = at0 + wave / sharers;
+    const bool has = at < all;
+    const Sequence seq = counted.of_thing((int)over(has ? at : 0, a.c.heads));
     const int s = seq.s, n = seq.n, first = first_of(n);
-    const int in = (int)(at - (int64_t)seq.before * a.c.heads), of = strips(n), kh = in / of, strip = in - kh * of;
-    const int lo = (first / kMassSlots + strip) * kMassSlots, i = lo + tid;
+    const int in = (int)((has ? at : 0) - (int64_t)seq.before * a.c.heads), of = strips(n);
+    const int kh = (int)over(in, of), strip = in - kh * of;
+    const int i = (first / kMassSlots + strip) * kMassSlots + 4 * lane;
     const int64_t row0 = (int64_t)s * a.q.n + kh * a.group;
-    const int page = i >= first && i < n ? page_of(a.c, s, i) : -1;
-    const int64_t number = number_at(a.c, max(page, 0), kh, i);
-    const float mass = a.c.mass[number];
-    f32x4_t add = {0, 0, 0, 0};
-    const int mine = min(lo + 4 * lane, p.scores_row - 4);  // what lies behind the row's slots is not used
-#pragma unroll 4
-    for (int h = wave; h < a.group; h += kWaves) {
-      const float level = p.level[row0 + h];
-      const f32x4_t score = *reinterpret_cast<const f32x4_t *>(p.scores + (row0 + h) * p.scores_row + mine);
+    const int page = page_of(a.c, s, min(i, n - 1));
+    float *const number = a.c.mass + number_at(a.c, max(page, 0), kh, i);
+    f32x4_t mass = {0, 0, 0, 0}, add = {0, 0, 0, 0};
+    if (own == 0) __builtin_memcpy(&mass, number, 16);
+    const float *const score = p.scores + row0 * p.scores_row + min(i, p.scores_row - 4);
+    for (int h0 = own; h0 < a.group; h0 += 8 * sharers) {
+      f32x4_t u[8];
+      float level[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) add[k] += exp2_of(score[k] - level);
-    }
-    *reinterpret_cast<f32x4_t *>(&sums[wave][4 * lane]) = add;
-    __syncthreads();
-    if (page >= 0) {
-      float v = 0.f;  // what is added first: the mass is rounded once
+      for (int j = 0; j < 8; ++j) {
+        const int h = min(h0 + j * sharers, a.group - 1);
+        level[j] = p.level[row0 + h];
+        u[j] = *reinterpret_cast<const f32x4_t *>(score + (int64_t)h * p.scores_row);
+      }
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) v += sums[w][tid];
-      a.c.mass[number] = mass + v;
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) add[e] += h0 + j * sharers < a.group ? exp2_of(u[j][e] - level[j]) : 0.f;
     }
-    __syncthreads();
+    if (sharers > 1) {
+      *reinterpret_cast<f32x4_t *>(&sums[wave][4 * lane]) = add;
+      __syncthreads();
+      if (own == 0)
+        for (int w = 1; w < sharers; ++w) add += *reinterpret_cast<const f32x4_t *>(&sums[wave + w][4 * lane]);
+      __syncthreads();
+    }
+    if (own != 0 || !has || page < 0) continue;
+    mass += add;  // rounded once
+    if (i >= first && i + 4 <= n) {
+      __builtin_memcpy(number, &mass, 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i + e >= first && i + e < n) number[e] = mass[e];
+    }
   }
 }
 
 // Workgroups that the chip holds at once, by the registers of the kernel.
-inline int shares_for(int d) { return 256 * (d <= 96 ? 3 : d <= 128 ? 2 : 1); }
+inline int shares_for(int d) { return 256 * (d <= 64 ? 3 : d <= 128 ? 2 : 1); }
 
 template <typename E>
 Plan plan_of(const Pool &c, int q_heads, bool accumulate, uint8_t *ws, size_t *bytes) {
@@ -643,7 +743,9 @@ gsi_status launch_as(const AttendArgs &a, hipStream_t st) {
   }
   if (a.accumulate && a.c.most > 0) {
     const int64_t strips = (((int64_t)a.c.most << a.c.shift) + kMassSlots - 1) / kMassSlots * a.c.S * a.c.heads;
-    mass_kernel<<<(unsigned)std::min<int64_t>(strips, kMassGrid), kThreads, 0, st>>>(a, p);
+    const int sharers = a.group >= 4 ? 4 : a.group >= 2 ? 2 : 1, at_once = kWaves / sharers;
+    const int64_t grid = std::min<int64_t>((strips + at_once - 1) / at_once, kMassGrid);
+    mass_kernel<<<(unsigned)grid, kThreads, 0, st>>>(a, p, sharers);
     if (hipGetLastError() != hipSuccess) return GSI_E_HIP;
   }
   return GSI_OK;
