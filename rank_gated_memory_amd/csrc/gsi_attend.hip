@@ -737,7 +737,7 @@ gsi_status launch_as(const AttendArgs &a, hipStream_t st) {
   if (p.stats && p.shares > 1) {
     const int most = heads_at_once(a.c.d), sets = (std::min(16, a.group) + most - 1) / most;
     const int64_t by_cuts = (int64_t)(p.shares - 1) * sets, by_heads = (int64_t)a.c.S * a.q.n;
-    const bool cuts = by_cuts < by_heads;
+    const bool cuts = by_heads > 2048 && by_cuts < by_heads;  // a head for each workgroup has more threads for many pieces
     join_kernel<E><<<(unsigned)(cuts ? by_cuts : by_heads), kThreads, 0, st>>>(a, p, cuts, sets);
     if (hipGetLastError() != hipSuccess) return GSI_E_HIP;
   }

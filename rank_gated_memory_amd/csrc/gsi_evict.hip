@@ -41,7 +41,7 @@ struct Four {
 // LDS of a workgroup.
 struct Shared {
   int hist[2][4][256];  // of the two selections' passes, zero at first
-  uint32_t all[2][kWaves], any[2][kWaves];
+  uint32_t all[kWaves], any[kWaves];
   int part[kWaves];
   int2 moves[kFewMoves];
 };
@@ -118,49 +118,57 @@ struct Slots {
 };
 
 // Keeps the `count` free slots of the largest key, ties to the lowest slot;
-// there are at least `count`.  keys(k, b): this lane's four keys; which: 0 or 1,
-// the selection's LDS; counts: LDS for a number per block.
-template <int NB, typename Keys>
-__device__ __forceinline__ void take_largest(Slots<NB> &sl, int count, const Keys &keys, int which, int *counts,
+// there are at least `count`.  keys(k, b): this lane's four keys; Common: they may
+// agree in their upper bits, as ages do; hists: the selection's bins, zero; counts:
+// LDS for a number per block.
+template <bool Common, int NB, typename Keys>
+__device__ __forceinline__ void take_largest(Slots<NB> &sl, int count, const Keys &keys, int (*hists)[256], int *counts,
                                              Shared &sh) {
   const int lane = sl.lane;
-  // what all keys agree in, from the top, needs no counting
-  uint32_t all = ~0u, any = 0;
-  sl.each([&](auto k, int b) {
-    const uint32_t is_free = sl.is_free(k, b);
-    const Four key = keys(k, b);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      all &= is_free >> e & 1 ? key.v[e] : ~0u;
-      any |= is_free >> e & 1 ? key.v[e] : 0u;
-    }
-  });
-  all = joined_to<-1>(all, [](int x, int y) { return x & y; });
-  any = joined_to<0>(any, [](int x, int y) { return x | y; });
-  if (lane == 63) sh.all[which][sl.wave] = all, sh.any[which][sl.wave] = any;
-  __syncthreads();
-  all = sh.all[which][0], any = sh.any[which][0];
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w) all &= sh.all[which][w], any |= sh.any[which][w];
-  const uint32_t differ = all ^ any;
-  int shift = 32 - __clz(differ), need = count;
+  int shift = 32, need = count;
   // keys from `base` on to base + span agree with the threshold so far
-  uint32_t span = shift == 32 ? ~0u : (1u << shift) - 1, base = all & ~span;
+  uint32_t base = 0, span = ~0u;
+  if constexpr (Common) {  // what all keys agree in, from the top, needs no counting
+    uint32_t all = ~0u, any = 0;
+    sl.each([&](auto k, int b) {
+      const uint32_t is_free = sl.is_free(k, b);
+      const Four key = keys(k, b);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        all &= is_free >> e & 1 ? key.v[e] : ~0u;
+        any |= is_free >> e & 1 ? key.v[e] : 0u;
+      }
+    });
+    all = joined_to<-1>(all, [](int x, int y) { return x & y; });
+    any = joined_to<0>(any, [](int x, int y) { return x | y; });
+    if (lane == 63) sh.all[sl.wave] = all, sh.any[sl.wave] = any;
+    __syncthreads();
+    all = sh.all[0], any = sh.any[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) all &= sh.all[w], any |= sh.any[w];
+    shift = 32 - __clz(all ^ any);
+    if (shift < 32) span = (1u << shift) - 1, base = all & ~span;
+  }
   bool tied = true;  // more slots at the threshold than are taken
   for (int pass = 0; shift > 0 && tied; ++pass) {
     const int low = max(shift - 8, 0);
-    int *const hist = sh.hist[which][pass];
+    int *const hist = hists[pass];
     sl.each([&](auto k, int b) {
       const uint32_t is_free = sl.is_free(k, b);
       const Four key = keys(k, b);
       // Neighbours often agree in these bits (ages are slots at first), and lanes
       // at one bin take their turns: a lane's run of one bin is counted at once,
       // and of the lanes' last runs those of the first lane's bin.
+      uint32_t among = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) among |= (uint32_t)(key.v[e] - base <= span) << e;
+      among &= is_free;
+      if (__ballot(among != 0) == 0) return;  // few are left after a pass or two
       int bin = 0, c = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint32_t off = key.v[e] - base;
-        const bool in = (is_free >> e & 1) && off <= span;
+        const bool in = among >> e & 1;
         if (in && c > 0 && (int)(off >> low) != bin) {
           atomicAdd(&hist[bin], c);  // integers: any order
           c = 0;
@@ -315,11 +323,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(EvictArgs a, int block
   }
   __syncthreads();
   if (by_age) {
-    take_largest(sl, a.recent, [&](auto k, int b) {
+    take_largest<true>(sl, a.recent, [&](auto k, int b) {
       if constexpr (NB > 0) return age[k];
       const int page = raw_page(b);
       return age_keys(page, read(a.c.age, page, b));
-    }, 0, count, sh);
+    }, sh.hist[0], count, sh);
   } else if (a.recent > 0) {
     sl.each([&](auto k, int b) {
       const int before = n - a.recent - (b * kBlock + 4 * sl.lane);  // slots of this lane before the newest
@@ -332,11 +340,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(EvictArgs a, int block
       if (!kBoth) read_masses();
       sl.each([&](auto k, int) { mass[k] = mass_keys(p[k], mass[k]); });
     }
-    take_largest(sl, budget - a.recent, [&](auto k, int b) {
+    take_largest<false>(sl, budget - a.recent, [&](auto k, int b) {
       if constexpr (NB > 0) return mass[k];
       const int page = raw_page(b);
       return mass_keys(page, read(a.c.mass, page, b));
-    }, 1, count, sh);
+    }, sh.hist[1], count, sh);
   }
   // kept slots before each block
   sl.each([&](auto k, int b) {
@@ -472,6 +480,8 @@ gsi_status launch_evict(const EvictArgs &a, int dtype, hipStream_t st) {
   const size_t lds = (size_t)blocks * 36 + (size_t)holes * 4;
   if (slots <= kWaves * kBlock)
     select_kernel<1><<<(unsigned)rows, kThreads, lds, st>>>(a, blocks, holes, pieces);
+  else if (slots <= 2 * kWaves * kBlock)
+    select_kernel<2><<<(unsigned)rows, kThreads, lds, st>>>(a, blocks, holes, pieces);
   else if (slots <= 8 * kWaves * kBlock)
     select_kernel<8><<<(unsigned)rows, kThreads, lds, st>>>(a, blocks, holes, pieces);
   else
