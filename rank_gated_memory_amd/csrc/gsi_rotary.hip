@@ -28,7 +28,7 @@ struct Split {
 // What a workgroup's tokens share: amplitude times cos and sin of their angles,
 // and where their entries lie.
 struct Tokens {
-  float2 turn[kMostTokens][kMostPairs];
+  float2 turn[kMostTokens][kMostPairs + 8];  // a run's last pairs may lie behind
   int64_t entry[kMostTokens];   // bytes from K (V) to head 0's entry
   int64_t number[kMostTokens];  // of head 0 in mass and age
   bool has[kMostTokens];
@@ -102,111 +102,108 @@ __device__ __forceinline__ Item item_of(const RotateArgs &a, const Split &sp, co
   return r;
 }
 
-// Bound by HBM for many tokens (8191 of 40 heads of 128: 168 MB in 30 us, 5.6
+// A run of `count` elements, 16 bytes of them where they are all there.
+template <bool Whole, typename vec, typename E, int V>
+__device__ __forceinline__ vec load_run(const uint8_t *at, int count) {
+  vec v = {};
+  if (Whole || count == V) {
+    __builtin_memcpy(&v, Whole ? __builtin_assume_aligned(at, 16) : at, 16);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (e < count) v[e] = reinterpret_cast<const E *>(at)[e];
+  }
+  return v;
+}
+template <bool Whole, typename vec, typename E, int V>
+__device__ __forceinline__ void store_run(uint8_t *at, const vec &v, int count) {
+  if (Whole || count == V) {
+    __builtin_memcpy(Whole ? __builtin_assume_aligned(at, 16) : at, &v, 16);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (e < count) reinterpret_cast<E *>(at)[e] = v[e];
+  }
+}
+
+// Bound by HBM for many tokens (8191 of 40 heads of 128: 168 MB in 33 us, 5.1
 // TB/s; 4939 of 16 heads of 256 with their keys and values into the pages: 243
-// MB), by latency for few: the position, the sine and cosine, the head.  The
-// angles are formed once for all heads of a token.
-template <typename E, bool Halves>
+// MB in 55 us, 4.4 TB/s), by latency for few: the position, the sine and cosine,
+// the head.  The angles are formed once for all heads of a token.  Whole: runs of
+// 16 bytes end where the turned part does; otherwise the turned part, what lies
+// before it and what lies behind are cut into runs each by itself, the last one
+// shorter, at any address (333 tokens of 40 fp32 heads of 200: all turned in
+// halves 5.8 us, 74 elements of each 7.8).
+template <typename E, bool Halves, bool Whole>
 __global__ void __launch_bounds__(kThreads, 8) rotate_kernel(RotateArgs a, Split sp) {
   __shared__ Tokens k;
   constexpr int es = sizeof(E), V = 16 / es;
-  constexpr int kAhead = Halves ? 2 : 4;  // items of a thread under way, of two pieces and of one
+  constexpr int kAhead = Halves ? (Whole ? 2 : 1) : (Whole ? 4 : 2);  // items of a thread under way
   typedef E vec __attribute__((ext_vector_type(V)));
   const int group = blockIdx.x / sp.strips, strip = blockIdx.x - group * sp.strips;
   const int t0 = group * sp.tokens, tokens = min(sp.tokens, a.T - t0), pairs = a.turned / 2;
+  const int run = Halves ? pairs : a.turned, runs = (run + V - 1) / V, left = (a.start + V - 1) / V;
   prepare(a, k, t0, tokens, strip == 0);
   const int all = tokens * sp.items, step = sp.strips * kThreads;
   for (int i0 = strip * kThreads + threadIdx.x; i0 < all; i0 += kAhead * step) {
     uint8_t *to[kAhead];
-    u32x4_t x0[kAhead], x1[kAhead];
-    int at[kAhead], turn[kAhead];  // of the (first) piece, and its first pair or -1
+    vec x0[kAhead], x1[kAhead];
+    int count[kAhead], turn[kAhead];  // of the (first) run, and its first pair or -1
     const float2 *w[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       const int i = i0 + j * step;
       to[j] = nullptr;
-      x0[j] = x1[j] = u32x4_t{0, 0, 0, 0};
-      at[j] = 0;
+      x0[j] = x1[j] = vec{};
+      count[j] = V;
       turn[j] = -1;
       w[j] = k.turn[0];
       if (i >= all) continue;
       const Item it = item_of(a, sp, k, t0, tokens, i);
       w[j] = k.turn[it.t];
-      to[j] = it.to;
-      at[j] = it.unit * 16;
+      int e = it.unit * V;
       if (it.turns) {
-        if constexpr (Halves) {  // two pieces, or a piece of those that stay
-          const int half = pairs / V;
-          if (it.unit < half) {
-            at[j] = (a.start + it.unit * V) * es;
-            turn[j] = it.unit * V;
-          } else {
-            const int e = (it.unit - half) * V;
-            at[j] = (e < a.start ? e : e + a.turned) * es;
-          }
+        if (it.unit < runs) {
+          turn[j] = Halves ? e : e / 2;
+          count[j] = min(V, run - e);
+          e += a.start;
+        } else if (it.unit < runs + left) {
+          e -= runs * V;
+          count[j] = min(V, a.start - e);
         } else {
-          const int e = it.unit * V - a.start;
-          if (e >= 0 && e < a.turned) turn[j] = e / 2;
+          e += a.start + a.turned - (runs + left) * V;
+          count[j] = min(V, a.d - e);
         }
-        if (turn[j] < 0 && it.from == it.to) to[j] = nullptr;  // in place
       }
-      if (!to[j]) continue;
-      x0[j] = *reinterpret_cast<const u32x4_t *>(it.from + at[j]);
-      if (Halves && turn[j] >= 0) x1[j] = *reinterpret_cast<const u32x4_t *>(it.from + at[j] + pairs * es);
+      if (!it.to || (it.turns && turn[j] < 0 && it.from == it.to)) continue;  // no entry; in place
+      const uint8_t *const from = it.from + e * es;
+      to[j] = it.to + e * es;
+      x0[j] = load_run<Whole, vec, E, V>(from, count[j]);
+      if (Halves && turn[j] >= 0) x1[j] = load_run<Whole, vec, E, V>(from + pairs * es, count[j]);
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (!to[j]) continue;
       if (turn[j] >= 0) {
         const float2 *const u = w[j] + turn[j];
-        const vec a0 = __builtin_bit_cast(vec, x0[j]), a1 = __builtin_bit_cast(vec, x1[j]);
         vec y0, y1;
         if constexpr (Halves) {
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            y0[e] = (E)((float)a0[e] * u[e].x - (float)a1[e] * u[e].y);
-            y1[e] = (E)((float)a1[e] * u[e].x + (float)a0[e] * u[e].y);
+            y0[e] = (E)((float)x0[j][e] * u[e].x - (float)x1[j][e] * u[e].y);
+            y1[e] = (E)((float)x1[j][e] * u[e].x + (float)x0[j][e] * u[e].y);
           }
-          *reinterpret_cast<vec *>(to[j] + at[j] + pairs * es) = y1;
+          store_run<Whole, vec, E, V>(to[j] + pairs * es, y1, count[j]);
         } else {
 #pragma unroll
           for (int e = 0; e < V; e += 2) {
-            y0[e] = (E)((float)a0[e] * u[e / 2].x - (float)a0[e + 1] * u[e / 2].y);
-            y0[e + 1] = (E)((float)a0[e + 1] * u[e / 2].x + (float)a0[e] * u[e / 2].y);
+            y0[e] = (E)((float)x0[j][e] * u[e / 2].x - (float)x0[j][e + 1] * u[e / 2].y);
+            y0[e + 1] = (E)((float)x0[j][e + 1] * u[e / 2].x + (float)x0[j][e] * u[e / 2].y);
           }
         }
-        x0[j] = __builtin_bit_cast(u32x4_t, y0);
+        x0[j] = y0;
       }
-      *reinterpret_cast<u32x4_t *>(to[j] + at[j]) = x0[j];
-    }
-  }
-}
-
-// The same where pieces of 16 bytes do not end where the turned part does: a
-// unit is a pair, or an element of those that stay.
-template <typename E, bool Halves>
-__global__ void __launch_bounds__(kThreads) rotate_elements_kernel(RotateArgs a, Split sp) {
-  __shared__ Tokens k;
-  const int group = blockIdx.x / sp.strips, strip = blockIdx.x - group * sp.strips;
-  const int t0 = group * sp.tokens, tokens = min(sp.tokens, a.T - t0), pairs = a.turned / 2;
-  prepare(a, k, t0, tokens, strip == 0);
-  const int all = tokens * sp.items, step = sp.strips * kThreads;
-  for (int i = strip * kThreads + threadIdx.x; i < all; i += step) {
-    const Item it = item_of(a, sp, k, t0, tokens, i);
-    if (!it.to) continue;
-    const E *const from = reinterpret_cast<const E *>(it.from);
-    E *const to = reinterpret_cast<E *>(it.to);
-    if (!it.turns) {
-      reinterpret_cast<u32x4_t *>(to)[it.unit] = reinterpret_cast<const u32x4_t *>(from)[it.unit];
-    } else if (it.unit < pairs) {
-      const int i0 = a.start + (Halves ? it.unit : 2 * it.unit), i1 = i0 + (Halves ? pairs : 1);
-      const float2 u = k.turn[it.t][it.unit];
-      const float x0 = (float)from[i0], x1 = (float)from[i1];
-      to[i0] = (E)(x0 * u.x - x1 * u.y);
-      to[i1] = (E)(x1 * u.x + x0 * u.y);
-    } else if (from != to) {
-      const int e = it.unit - pairs, at = e < a.start ? e : e + a.turned;
-      to[at] = from[at];
+      store_run<Whole, vec, E, V>(to[j], x0[j], count[j]);
     }
   }
 }
@@ -215,7 +212,8 @@ template <typename E, bool Halves>
 gsi_status launch_as(const RotateArgs &a, bool whole, hipStream_t st) {
   constexpr int V = 16 / sizeof(E);
   const int pairs = a.turned / 2, copies = a.d / V;
-  const int turn_units = !whole ? a.d - pairs : Halves ? copies - pairs / V : copies;
+  const int run = Halves ? pairs : a.turned, behind = a.d - a.start - a.turned;
+  const int turn_units = (run + V - 1) / V + (a.start + V - 1) / V + (behind + V - 1) / V;
   Split sp{};
   sp.turn_units = div_by(turn_units);
   sp.copy_units = div_by(copies);
@@ -232,9 +230,9 @@ gsi_status launch_as(const RotateArgs &a, bool whole, hipStream_t st) {
   if (groups * sp.strips * kThreads > kMostLaunch) return GSI_E_SHAPE;
   const unsigned grid = (unsigned)(groups * sp.strips);
   if (whole)
-    rotate_kernel<E, Halves><<<grid, kThreads, 0, st>>>(a, sp);
+    rotate_kernel<E, Halves, true><<<grid, kThreads, 0, st>>>(a, sp);
   else
-    rotate_elements_kernel<E, Halves><<<grid, kThreads, 0, st>>>(a, sp);
+    rotate_kernel<E, Halves, false><<<grid, kThreads, 0, st>>>(a, sp);
   return hipGetLastError() == hipSuccess ? GSI_OK : GSI_E_HIP;
 }
 
