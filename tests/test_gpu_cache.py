@@ -47,7 +47,8 @@ def bits(t):
 
 def within(y, ref, tol, what):
     y = f64(y)
-    bad = ~((np.abs(y - ref) <= tol) | ((y == ref) & np.isinf(ref)))
+    with np.errstate(invalid="ignore"):  # inf - inf: those are equal or bad
+        bad = ~((np.abs(y - ref) <= tol) | ((y == ref) & np.isinf(ref)))
     assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off, first at {np.argwhere(bad)[0]}: " \
         f"{y[bad][0]} for {ref[bad][0]}"
 
@@ -171,6 +172,24 @@ def test_rotary_far_positions_and_back():
     within(back, f64(x), 2 * size * 2 * (2.0**-20 + 2.0**-23 + np.abs(ints(pos))[:, None, None] * 2.0**-51), "back")
 
 
+def test_rotary_of_many_tokens():
+    """More tokens than workgroups fit side by side, and row addresses past 32 bits."""
+    g = gen(6)
+    T = 1 << 20
+    wide = torch.empty(T, 2200, device=DEV, dtype=BF16)  # 4.6 GB apart from first to last
+    x = wide[:, 64:72].view(T, 1, 8)
+    x.copy_(torch.randn(T, 1, 8, generator=g, device=DEV))
+    freqs = gsi.rotary_freqs(8)
+    r = gsi.Rotary(freqs, device=DEV)
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, device=DEV)
+    y = gsi.gsi_rotary(r, x, pos)
+    at = torch.randint(0, T, (300,), generator=g, device=DEV)
+    at[:2] = torch.tensor([0, T - 1], device=DEV)
+    check_rotary(y[at], x[at], pos[at], freqs, "halves", 0, 1.0, BF16, "many tokens")
+    z = gsi.gsi_rotary(r, x[T - 2001:].contiguous(), pos[T - 2001:].contiguous())
+    assert torch.equal(bits(z), bits(y[T - 2001:]))
+
+
 def test_rotary_keeps_rows_apart():
     """A row that is not finite, and no rows at all."""
     g = gen(5)
@@ -290,7 +309,7 @@ def test_attend_head_sizes(d, page, dtype):
 
 @DTYPES
 @pytest.mark.parametrize("heads,group", [(1, 1), (40, 1), (3, 2), (8, 4), (5, 7), (2, 8), (1, 15), (2, 16), (1, 17),
-                                         (2, 32), (1, 33), (1, 71), (1, 128)])
+                                         (2, 32), (1, 33), (1, 71), (1, 128), (1, 300)])
 def test_attend_groups(heads, group, dtype):
     g = gen(heads * 100 + group)
     lengths = torch.tensor([77, 5, 130], device=DEV, dtype=torch.int32)
@@ -330,6 +349,110 @@ def test_attend_long(n, S, heads, group, d, page, dtype):
         again, lse2 = gsi.gsi_cache_attend(c, table, lengths, q, accumulate=False)
         assert torch.equal(bits(before), bits(c.mass)) and torch.equal(bits(lse), bits(lse2))
         assert torch.equal(bits(out), bits(again))
+
+
+def plain_attend(c, table, lengths, q, scale, window=0):
+    """The oracle's formula for many sequences at once: 64-bit products on the
+    GPU.  (out, lse, weights by slot, sum of weight |v|, largest scale sum |q k|)."""
+    S, H, d = q.shape
+    kv = c.heads
+    k, v = (t.double()[table.long()].transpose(1, 2).flatten(2, 3) for t in (c.K, c.V))  # [S][kv][slots][d]
+    t = torch.arange(k.shape[2], device=DEV)
+    n = lengths.long()[:, None]
+    first = (n - window).clamp(min=0) if window else torch.zeros_like(n)
+    inside = ((t >= first) & (t < n))[:, None, None]
+    k, v = (u.masked_fill(~inside.transpose(2, 3), 0.0) for u in (k, v))
+    Q = q.double().view(S, kv, H // kv, d)
+    score = (scale * (Q @ k.transpose(2, 3).contiguous())).masked_fill(~inside, -float("inf"))
+    big = abs(scale) * (Q.abs() @ k.abs().transpose(2, 3).contiguous()).amax(3).view(S, H)
+    lse = torch.logsumexp(score, 3)
+    w = torch.exp(score - lse.clamp(min=-1e300)[..., None])
+    return (w @ v).view(S, H, d), lse.view(S, H), w.sum(2), (w @ v.abs()).view(S, H, d), big
+
+
+@DTYPES
+@pytest.mark.parametrize("page", [8, 32])
+@pytest.mark.parametrize("d", [24, 64, 80, 128, 136, 192, 200, 256])
+def test_attend_many_rows(d, page, dtype):
+    """Many more rows than workgroups: each takes several, cut ones among them,
+    and the lengths of more than 64 sequences are counted."""
+    g = gen(d + page)
+    S, kv, H, most = 250, 8, 24, 160
+    lengths = torch.randint(0, most + 1, (S,), generator=g, device=DEV, dtype=torch.int32)
+    lengths[torch.rand(S, generator=g, device=DEV) < 0.3] = 3
+    lengths[:5] = torch.tensor([0, 0, most, 1, most], device=DEV)
+    c, table = make_pool(g, S, lengths.tolist(), kv, page, d, dtype, most=most // page, age=False)
+    q = 2 * torch.randn(S, H, d, generator=g, device=DEV).to(dtype)
+    before = c.mass.clone()
+    ref, lse, w, size, big = (t.cpu().numpy() for t in plain_attend(c, table, lengths, q, d**-0.5))
+    out, l = gsi.gsi_cache_attend(c, table, lengths, q, accumulate=True)
+    delta = (d + 8) * 2.0**-24 * big + (2 * big + 8) * 2.0**-23
+    chain = (most / 16 + 64) * 2.0**-23
+    rel = 2 * delta + 2.0**-16 + chain
+    within(out, ref, half(dtype) * np.abs(ref) * 1.001 + size * rel[:, :, None] * 1.01 + 1e-30, "many rows")
+    within(l, lse, delta + chain + 2.0**-22 + 2.0**-22 * np.abs(np.where(np.isfinite(lse), lse, 0.0)), "many rows lse")
+    add = torch.zeros_like(c.mass).double()
+    add[table.long()] = torch.from_numpy(w).to(DEV).view(S, kv, most // page, page).transpose(1, 2)
+    want = before.double() + add
+    off = (c.mass.double() - want).abs() > add * float(rel.max()) * 1.01 + want.abs() * 2.0**-23
+    assert not bool((off & ~torch.isnan(before)).any()) and torch.equal(torch.isnan(before), torch.isnan(c.mass))
+
+
+@pytest.mark.parametrize("window", [0, 50])
+def test_attend_more_sequences_than_a_wavefront_counts(window):
+    """2500 sequences, most of them short, some empty, in every place."""
+    g = gen(41 + window)
+    S = 2500
+    lengths = torch.randint(0, 30, (S,), generator=g, device=DEV, dtype=torch.int32)
+    lengths[torch.randint(0, S, (40,), generator=g, device=DEV)] = 190
+    c, table = make_pool(g, S, lengths.tolist(), 1, 16, 16, BF16, most=12, age=False)
+    q = 2 * torch.randn(S, 3, 16, generator=g, device=DEV).to(BF16)
+    before = c.mass.clone()
+    ref, lse, w, size, big = (t.cpu().numpy() for t in plain_attend(c, table, lengths, q, 0.25, window))
+    out, l = gsi.gsi_cache_attend(c, table, lengths, q, window=window, accumulate=True)
+    delta = 24 * 2.0**-24 * big + (2 * big + 8) * 2.0**-23
+    rel = 2 * delta + 2.0**-16 + 76 * 2.0**-23
+    within(out, ref, half(BF16) * np.abs(ref) * 1.001 + size * rel[:, :, None] * 1.01 + 1e-30, "sequences")
+    within(l, lse, delta + 76 * 2.0**-23 + 2.0**-22 + 2.0**-22 * np.abs(np.where(np.isfinite(lse), lse, 0.0)), "lse")
+    add = torch.zeros_like(c.mass).double()
+    add[table.long()] = torch.from_numpy(w).to(DEV).view(S, 1, 12, 16).transpose(1, 2)
+    off = (c.mass.double() - before.double() - add).abs() > add * float(rel.max()) * 1.01 + (before + add).abs() * 2.0**-23
+    assert not bool((off & ~torch.isnan(before)).any()) and torch.equal(torch.isnan(before), torch.isnan(c.mass))
+
+
+def test_attend_nothing_at_all():
+    """Only empty sequences; tables without a page; no sequence."""
+    g = gen(42)
+    c, table = make_pool(g, 3, [0, 0, 0], 2, 16, 64, BF16)
+    q = torch.randn(3, 4, 64, generator=g, device=DEV).to(BF16)
+    zero = torch.zeros(3, device=DEV, dtype=torch.int32)
+    for tab, n in ((table, zero), (table[:, :0], zero + 9), (table, zero - 1)):
+        before = c.mass.clone()
+        out, lse = gsi.gsi_cache_attend(c, tab, n, q, accumulate=True)
+        assert bool((out == 0).all()) and bool((lse == -float("inf")).all())
+        assert torch.equal(bits(before), bits(c.mass))
+    out, lse = gsi.gsi_cache_attend(c, table[:0], zero[:0], q[:0])
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    length, moved = gsi.gsi_cache_evict(c, table[:, :0], zero + 5, 4)
+    assert length.tolist() == [0, 0, 0] and bool((moved == -1).all())
+
+
+def test_attend_a_billion_slots():
+    """2^30 slots of one sequence on pages that come again and again: as many
+    products as 64-bit counts of shares need.  Equal pages give the average over
+    one of them; a lane adds 2^30 / (32 * 768 * 4) = 10923 steps of 8 weights, the
+    sum of which is off by 2^-24 each at most, and shares are joined: below
+    (8 * 10923 + 1024) 2^-24 = 0.0053 of the sum, and of each sum of values."""
+    g = gen(43)
+    K, V = (torch.randn(2, 1, 4096, 8, generator=g, device=DEV).to(BF16) for _ in range(2))
+    c = gsi.Cache(K, V)
+    table = torch.zeros(1, 1 << 18, device=DEV, dtype=torch.int32)
+    q = torch.randn(1, 2, 8, generator=g, device=DEV).to(BF16)
+    one, lse1 = gsi.gsi_cache_attend(c, table[:, :1].contiguous(), torch.tensor([4096], device=DEV, dtype=torch.int32), q)
+    out, lse = gsi.gsi_cache_attend(c, table, torch.tensor([1 << 30], device=DEV, dtype=torch.int32), q)
+    _, _, _, size, _ = plain_attend(c, table[:, :1], torch.tensor([4096], device=DEV, dtype=torch.int32), q, 8**-0.5)
+    assert bool(((out.double() - one.double()).abs() <= 2 * 0.0053 * size + 2.0**-7 * one.double().abs()).all())
+    assert bool(((lse - lse1 - 18 * np.log(2.0)).abs() <= 0.0054 + 1e-5).all())
 
 
 @DTYPES
@@ -582,6 +705,32 @@ def test_evict_long(n, budget, recent):
         assert np.array_equal(new, M[h][want])
 
 
+@pytest.mark.parametrize("n,budget", [(32768, 16384), (60000, 30000), (8192, 4095), (4096, 2048), (4097, 4000)])
+def test_evict_when_the_newest_weigh_most(n, budget):
+    """All that stay lie behind the budget as far as they can: every slot below it
+    that is given up takes one of them, more of them than a list in LDS holds."""
+    g = gen(n)
+    c, table = make_pool(g, 1, [n], 1, 256, 16, F32)
+    at = table[0].long()
+    slots = torch.arange(at.numel() * 256, device=DEV)
+    c.mass[at, 0] = slots.float().view(-1, 256)
+    K = c.K[at, 0].reshape(-1, 16)[:n].clone()
+    age = c.age[at, 0].reshape(-1)[:n].clone()
+    _, moved = gsi.gsi_cache_evict(c, table, torch.tensor([n], device=DEV, dtype=torch.int32), budget)
+    want = slots[:budget].clone()
+    stay = max(0, 2 * budget - n)  # the last slots below the budget stay where they are
+    want[:budget - stay] = torch.arange(max(budget, n - budget), n, device=DEV)[:budget - stay]
+    assert torch.equal(moved[0, 0].long(), want)
+    assert torch.equal(c.K[at, 0].reshape(-1, 16)[:budget], K[want]) and torch.equal(c.age[at, 0].reshape(-1)[:budget], age[want])
+
+
+def test_evict_of_sequences_beyond_a_wavefront():
+    g = gen(52)
+    lens = [(7 * i) % 61 for i in range(150)]
+    c, table = make_pool(g, 150, lens, 2, 8, 8, BF16, most=8)
+    check_evict(c, table, torch.tensor(lens, device=DEV, dtype=torch.int32), 33, 10, what="many sequences")
+
+
 # ---- the operators together ----
 
 
@@ -681,6 +830,23 @@ def test_calls_on_two_streams():
         torch.cuda.synchronize()
         for (a, l), (b, m) in zip(got, want):
             assert torch.equal(bits(a), bits(b)) and torch.equal(bits(l), bits(m))
+    # all of a step on a stream of its own, its results read on the current one
+    r = gsi.Rotary(gsi.rotary_freqs(64), device=DEV)
+    k, v = (torch.randn(2, 2, 64, generator=g, device=DEV).to(BF16) for _ in range(2))
+    results = []
+    for st in (None, torch.cuda.Stream()):
+        c, t, n, q, _ = jobs[0]
+        K, V, mass, age = (x.clone() for x in (c.K, c.V, c.mass, c.age))
+        c, slots, pos = gsi.Cache(K, V, mass, age), n - 1, n.long()
+        torch.cuda.synchronize()  # the inputs are made on the current stream
+        qt = gsi.gsi_cache_append(c, t, slots, k, v, rotary=r, positions=pos, q=q, stream=st)
+        out, lse = gsi.gsi_cache_attend(c, t, n, qt, accumulate=True, stream=st)
+        length, moved = gsi.gsi_cache_evict(c, t, n, 600, recent=40, stream=st)
+        y = gsi.gsi_rotary(r, q, pos, stream=st)
+        torch.cuda.synchronize()
+        results.append([qt, out, lse, length, moved, y, K, V, mass])
+    for a, b in zip(*results):
+        assert torch.equal(bits(a), bits(b))
 
 
 def test_between_two_maps_of_a_block():
