@@ -27,7 +27,10 @@
 // run.  No value goes through LDS and no layout of the pool other than rows is
 // needed.  With fewer than 16 query heads the other rows of the tile are idle:
 // at 16 B a clock and CU from HBM the matrix cores are at 5 % (bf16) or 30 %
-// (fp32) of their rate even then.
+// (fp32) of their rate even then.  More than 16 are further rows, which read keys
+// and values again.  (Two tiles in one pass were no faster: 64 sequences of 2000
+// slots, one key head for 32: 38 us in two rows and 39 in one; one of 65536: 25
+// and 40, for the larger sums to join.)
 //
 // Weights are rounded to bf16 twice, p = hi + lo to 2^-17, and multiplied in two
 // instructions, so that in bf16 too only the result's own rounding shows.
@@ -51,10 +54,11 @@ constexpr int kWaves = kThreads / 64;
 // for one that it begins.
 struct Plan {
   int tiles;   // rows of a key head
+  int kept;    // query heads of a row at most
   int shares;  // workgroups
   int scores_row;
-  float *stats;    // [2 shares][16]: maximum (times log2 e) and sum
-  float *partial;  // [2 shares][16][d], sums at that maximum
+  float *stats;    // [2 shares][kept]: maximum (times log2 e) and sum
+  float *partial;  // [2 shares][kept][d], sums at that maximum
   float *level;    // [S * heads]: log2 of the sum of all weights, infinity for none
   float *scores;   // [S * heads][scores_row], times log2 e
 };
@@ -474,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
       for (int j = 0; j < NC; ++j) red[wave][h][col0 + j] = acc[j][i] * f;
   }
   __syncthreads();
-  const int64_t slot = 2 * (int64_t)share + (seg.skip == 0);
+  const int64_t slot = (2 * (int64_t)share + (seg.skip == 0)) * p.kept;
   for (int h = wave; h < live; h += kWaves) {
     float top = red_m[0][h], total = 0.f;
     for (int w = 1; w < kWaves; ++w) top = fmaxf(top, red_m[w][h]);
@@ -484,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
       if (whole)
         finish_row(a, p, row, top, total);
       else
-        p.stats[2 * (slot * 16 + h)] = top, p.stats[2 * (slot * 16 + h) + 1] = total;
+        p.stats[2 * (slot + h)] = top, p.stats[2 * (slot + h) + 1] = total;
     }
     const float inv = total == 0.f ? 0.f : 1.f / total;
     for (int c = lane; c < d; c += 64) {
@@ -494,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
       if (whole)
         reinterpret_cast<E *>(a.out.p + s * a.out.row + (head0 + h) * a.out.head)[c] = (E)(total == 0.f ? 0.f : o * inv);
       else
-        p.partial[(slot * 16 + h) * d + c] = o;
+        p.partial[(slot + h) * d + c] = o;
     }
   }
   if (last) return;
@@ -524,8 +528,8 @@ inline __host__ __device__ int heads_at_once(int d) { return max(1, 4 * kThreads
 // query heads each; otherwise a workgroup takes a query head of a sequence.
 // All latency: the lengths, and then all pieces' statistics and sums at once.
 // (A first round for the statistics and second ones for eight pieces at a time
-// took 5 us more for 65 pieces; workgroups of 1024 threads took 10 us alone to
-// start and end.)
+// took 5 us more for 65 pieces; 1024 threads, which take all pieces in one round,
+// lose 3 us to their sums in LDS, and in many workgroups 10 us to their start.)
 template <typename E>
 __global__ void __launch_bounds__(kThreads) join_kernel(AttendArgs a, Plan p, bool cuts, int sets) {
   __shared__ __attribute__((aligned(16))) float red[kThreads * 4];
@@ -577,7 +581,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttendArgs a, Plan p, bo
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const int i = min(i0 + k * sides, pieces - 1);
-        const int64_t at = (2 * (int64_t)(first + i) + (i == 0)) * 16 + in_tile + h;
+        const int64_t at = (2 * (int64_t)(first + i) + (i == 0)) * p.kept + in_tile + h;
         u[k] = *reinterpret_cast<const f32x4_t *>(p.partial + at * d + c);
         t[k] = *reinterpret_cast<const Stat *>(p.stats + 2 * at);
       }
@@ -686,6 +690,7 @@ Plan plan_of(const Pool &c, int q_heads, bool accumulate, uint8_t *ws, size_t *b
   const int64_t slots = (int64_t)c.most << c.shift;
   const int64_t units = std::max<int64_t>(1, (slots + kWaves * kStep<E> - 1) / (kWaves * kStep<E>));
   p.tiles = (q_heads / c.heads + 15) / 16;
+  p.kept = std::min(q_heads / c.heads, 16);
   p.shares = (int)std::min<int64_t>(shares_for(c.d), c.S * units * c.heads * p.tiles);
   p.scores_row = (int)((slots + 31) / 32 * 32);
   size_t at = 0;
@@ -695,8 +700,8 @@ Plan plan_of(const Pool &c, int q_heads, bool accumulate, uint8_t *ws, size_t *b
     return r;
   };
   if (units > 1) {
-    p.stats = take((size_t)p.shares * 2 * 16 * 2);
-    p.partial = take((size_t)p.shares * 2 * 16 * c.d);
+    p.stats = take((size_t)p.shares * 2 * p.kept * 2);
+    p.partial = take((size_t)p.shares * 2 * p.kept * c.d);
   }
   if (accumulate) {
     p.level = take((size_t)c.S * q_heads);
@@ -735,9 +740,11 @@ gsi_status launch_as(const AttendArgs &a, hipStream_t st) {
     go(std::integral_constant<int, 8>{});
   if (hipGetLastError() != hipSuccess) return GSI_E_HIP;
   if (p.stats && p.shares > 1) {
-    const int most = heads_at_once(a.c.d), sets = (std::min(16, a.group) + most - 1) / most;
+    const int most = heads_at_once(a.c.d), sets = (p.kept + most - 1) / most;
     const int64_t by_cuts = (int64_t)(p.shares - 1) * sets, by_heads = (int64_t)a.c.S * a.q.n;
-    const bool cuts = by_heads > 2048 && by_cuts < by_heads;  // a head for each workgroup has more threads for many pieces
+    // a query head for each workgroup has more threads for many pieces, as long
+    // as they run at once
+    const bool cuts = by_heads > 2048 && by_cuts < by_heads;
     join_kernel<E><<<(unsigned)(cuts ? by_cuts : by_heads), kThreads, 0, st>>>(a, p, cuts, sets);
     if (hipGetLastError() != hipSuccess) return GSI_E_HIP;
   }
