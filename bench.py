@@ -25,7 +25,8 @@ Prints one JSON line (rank 0, N=1):
                all host threads and on one thread
 Other workloads (--workload): the chained stack, the 13B-shaped stack, the
 batched T=256 map, single GPT-J-shaped maps at T=1, the operating-point
-sweep and the basis calibration.
+sweep, the basis calibration and the GPT-J-shaped stack with its key-value
+cache at a budget.
 """
 from __future__ import annotations
 
@@ -53,7 +54,7 @@ def parse():
     p.add_argument("--warmup", type=int, default=32)
     p.add_argument("--workload", default="gptj6b-28L",
                    choices=["gptj6b-28L", "gptj6b-28L-chained", "llama13b-40L", "batched-t256", "sweep",
-                            "calibrate-gptj6b-28L", "gptj-maps-t1"])
+                            "calibrate-gptj6b-28L", "gptj-maps-t1", "gptj6b-28L-cache"])
     p.add_argument("--layers", type=int, default=None, help="override the layer count")
     p.add_argument("--exact-rho", action="store_true",
                    help="every map caches E = V^T V - I and gates on the exact residual ratio")
@@ -650,6 +651,99 @@ def bench_single_maps(args):
     }), flush=True)
 
 
+def bench_cache(args):
+    """Decode steps of the GPT-J-shaped stack with a key-value cache at a budget.
+
+    A step of a layer, one token: the gated QKV and fc_in maps (one gsi_stack
+    launch), the new key and value into the layer's paged cache with 64 of 256
+    elements of queries and keys turned in pairs (gsi_cache_append), attention
+    over its 2049 entries with the weights kept (gsi_cache_attend), the cache
+    cut back to 2048, the newest 512 of them for certain (gsi_cache_evict), and
+    the gated out and fc_out maps, out from attention's output (one gsi_stack
+    launch).  All layers are one HIP graph, replayed; positions and the tables
+    stay as they are, the caches go on from step to step.  Beside it the same
+    graph without the cache's calls, and the cache's calls alone.
+    """
+    import torch
+
+    from rank_gated_memory_amd import gsi, synth
+
+    dev = torch.device("cuda:0")
+    layers, budget, recent, page = args.layers or 28, 2048, 512, 16
+    heads, d = 16, 256
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(20260506)
+    cfg, _, roles, _, _, cascade = synth.STACKS["gptj6b-28L"]
+    data = synth.stack_config(cfg, layers, roles, 8, 0.0, device=dev, cascade=cascade)
+    rotary = gsi.Rotary(gsi.rotary_freqs(64), layout="pairs", device=dev)
+    pages = budget // page + 1
+    work = []
+    for row in data:
+        maps = [gsi.gsi_prepare(gsi.Map(mi.W, mi.V)) for mi in row]
+        y = [torch.empty(mi.d_out, dtype=torch.bfloat16, device=dev) for mi in row]
+        att = torch.randn(heads * d, generator=gen, device=dev).to(torch.bfloat16)
+        first = gsi.Stack([(maps[0], row[0].X[0], y[0], 0.05, None, None), (maps[2], row[2].X[0], y[2], 0.05, None, None)],
+                          device=dev)
+        second = gsi.Stack([(maps[1], att, y[1], 0.05, None, None), (maps[3], row[3].X[0], y[3], 0.05, None, None)],
+                           device=dev)
+        K, V = (torch.randn(pages, heads, page, d, generator=gen, device=dev).to(torch.bfloat16) for _ in range(2))
+        cache = gsi.Cache(K, V, torch.rand(pages, heads, page, generator=gen, device=dev),
+                          torch.randint(0, budget, (pages, heads, page), generator=gen, device=dev, dtype=torch.int32))
+        work.append((first, second, cache, y, att))
+    table = torch.randperm(pages, generator=gen, device=dev).int()[None]
+    slots = torch.tensor([budget], dtype=torch.int32, device=dev)
+    lengths, positions = slots + 1, torch.tensor([5000], device=dev)
+    # a workspace for each of the two layouts: the counters of one would lie among
+    # the other's sums, which no run leaves at zero
+    ws_first, ws_second = (gsi.workspace(work[0][k].ws_bytes, dev) for k in range(2))
+
+    def step(with_maps, with_cache):
+        for first, second, cache, y, att in work:
+            if with_maps:
+                gsi.gsi_stack(first, gsi.GATED, ws_first)
+            if with_cache:
+                qkv = y[0].view(1, 3 * heads, d)
+                q = gsi.gsi_cache_append(cache, table, slots, qkv[:, heads:2 * heads], qkv[:, 2 * heads:], rotary=rotary,
+                                         positions=positions, q=qkv[:, :heads])
+                gsi.gsi_cache_attend(cache, table, lengths, q, accumulate=True, out=att.view(1, heads, d))
+                gsi.gsi_cache_evict(cache, table, lengths, budget, recent=recent)
+            if with_maps:
+                gsi.gsi_stack(second, gsi.GATED, ws_second)
+
+    times = {}
+    for name, what in (("step", (True, True)), ("maps alone", (True, False)), ("cache alone", (False, True))):
+        step(*what)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step(*what)
+        for _ in range(args.warmup):
+            graph.replay()
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        for _ in range(args.steps):
+            graph.replay()
+        torch.cuda.synchronize()
+        times[name] = (time.perf_counter() - t0) * 1e6 / args.steps
+        log(f"{name}: {times[name]:.1f} us per step of {layers} layers")
+        del graph
+    status = max(work[0][0].status(ws_first), work[0][1].status(ws_second))
+    finite = all(bool(torch.isfinite(t).all()) for w in work for t in (*w[3], w[4]))
+    read = layers * (budget + 1) * heads * (2 * d * 2 + 8)
+    gbps = read / times["cache alone"] / 1e3
+    print(json.dumps({
+        "metric": "decode steps/s of the GPT-J-shaped stack with a key-value cache at a budget", "value": 1e6 / times["step"],
+        "unit": "tokens/s", "n_gpus": 1, "steps": args.steps, "warmup": args.warmup, "ms_per_step": times["step"] / 1e3,
+        "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+        "config": {"workload": f"gptj6b-28L-cache: {layers} layers, 16 heads of 256, 64 elements turned in pairs, pages of "
+                               f"{page}, 2049 entries cut to 2048 at every step and layer", "us_per_step": times},
+        "roofline": {"bound": "hbm", "kernel": "attend_kernel and the calls around it", "achieved": gbps,
+                     "peak": PEAK_HBM_GBPS, "unit": "GB/s", "frac": gbps / PEAK_HBM_GBPS, "traffic": None},
+        "status": status, "finite": finite}), flush=True)
+    if status or not finite:
+        sys.exit(3)
+
+
 def bench_sweep(args):
     """Operating points: basis size k, threshold eps and the forced modes on spectral tokens.
 
@@ -1020,6 +1114,9 @@ def main():
         return
     if args.workload == "calibrate-gptj6b-28L":
         bench_calibrate(args)
+        return
+    if args.workload == "gptj6b-28L-cache":
+        bench_cache(args)
         return
     if args.trace:
         bench_trace(args)

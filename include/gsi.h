@@ -515,7 +515,7 @@ gsi_status gsi_cache_attend(const gsi_cache *cache, const gsi_table *table, cons
  * head by itself: the `recent` entries of the largest age (without ages: of the
  * highest slots) stay, and of the others those of the largest mass; ties go to
  * the lowest slot, a mass that is NaN and an entry of no page count as the
- * least.  Entries in slots below the budget stay where they are; the others
+ * least (nothing is moved for one that stays all the same).  Entries in slots below the budget stay where they are; the others
  * that stay fill, in the order of their slots, the slots below the budget that
  * were given up.  (Attention does not go by the order of slots.)
  *   budget, recent : 1 <= budget <= 2^20, 0 <= recent <= budget

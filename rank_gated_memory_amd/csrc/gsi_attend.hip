@@ -283,8 +283,9 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
   const auto here = [](const uint8_t *at) {
     if constexpr (Uniform) {
       const uint64_t p = reinterpret_cast<uint64_t>(at);
-      return reinterpret_cast<const uint8_t *>((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)p) |
-                                               (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(p >> 32)) << 32);
+      const uint32_t low = __builtin_amdgcn_readfirstlane((int)p);
+      const uint32_t high = __builtin_amdgcn_readfirstlane((int)(p >> 32));
+      return reinterpret_cast<const uint8_t *>(low | (uint64_t)high << 32);
     } else {
       asm volatile("" : "+v"(at));
       return at;
@@ -325,193 +326,195 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
     load_v(seg, now, seg.st);
   }
   for (;;) {
-  // The next segment, whose first loads go out as this one's last are used: while
-  // the wavefronts are joined nothing has to be waited for.
-  const bool last = left == 0;
-  Segment then = seg;
-  Where then_now{}, then_next{};
-  if (!last) {  // then this segment ends its row
-    if (++then.row_at == rows) {
-      then.row_at = 0;
-      then.sp = span_of<E>(a, __builtin_amdgcn_readfirstlane(clamped_length(a.c, a.lengths, ++then.s)));
+    // The next segment, whose first loads go out as this one's last are used: while
+    // the wavefronts are joined nothing has to be waited for.
+    const bool last = left == 0;
+    Segment then = seg;
+    Where then_now{}, then_next{};
+    if (!last) {  // then this segment ends its row
+      if (++then.row_at == rows) {
+        then.row_at = 0;
+        then.sp = span_of<E>(a, __builtin_amdgcn_readfirstlane(clamped_length(a.c, a.lengths, ++then.s)));
+      }
+      then.skip = 0;
+      place(then);
+      if (then.st < then.end) {
+        then_now = pages_of(then, then.st);
+        then_next = pages_of(then, then.st + kWaves);
+      }
     }
-    then.skip = 0;
-    place(then);
-    if (then.st < then.end) {
-      then_now = pages_of(then, then.st);
-      then_next = pages_of(then, then.st + kWaves);
-    }
-  }
-  const bool ahead = !last && then.st < then.end;
-  const bool whole = seg.mine == seg.sp.units;
-  const int s = seg.s, live = min(16, a.group - seg.tile * 16);  // query heads of this tile
-  const int head0 = seg.kh * a.group + seg.tile * 16;
-  const Span &sp = seg.sp;
+    const bool ahead = !last && then.st < then.end;
+    const bool whole = seg.mine == seg.sp.units;
+    const int s = seg.s, live = min(16, a.group - seg.tile * 16);  // query heads of this tile
+    const int head0 = seg.kh * a.group + seg.tile * 16;
+    const Span &sp = seg.sp;
 
-  f32x4_t acc[NC];
+    f32x4_t acc[NC];
 #pragma unroll
-  for (int j = 0; j < NC; ++j) acc[j] = f32x4_t{0, 0, 0, 0};
-  float m = -INFINITY, sum = 0.f;  // of head l16; the sum over this lane's slots
-  if (kAhead && seg.st >= seg.end && !last) {  // no step of this wavefront
-    load_q(then);
-    if (ahead) {
-      load_k(then, then_now, then.st);
-      load_v(then, then_now, then.st);
+    for (int j = 0; j < NC; ++j) acc[j] = f32x4_t{0, 0, 0, 0};
+    float m = -INFINITY, sum = 0.f;  // of head l16; the sum over this lane's slots
+    if (kAhead && seg.st >= seg.end && !last) {  // no step of this wavefront
+      load_q(then);
+      if (ahead) {
+        load_k(then, then_now, then.st);
+        load_v(then, then_now, then.st);
+      }
     }
-  }
-  for (int st = seg.st; st < seg.end; st += kWaves) {
-    f32x4_t sc[KT];
+    for (int st = seg.st; st < seg.end; st += kWaves) {
+      f32x4_t sc[KT];
 #pragma unroll
-    for (int u = 0; u < KT; ++u) {
-      sc[u] = f32x4_t{0, 0, 0, 0};
+      for (int u = 0; u < KT; ++u) {
+        sc[u] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        if (c >= GC && c * CE + 16 / es * quad >= d) k[u][c] = u32x4_t{0, 0, 0, 0};
-        if constexpr (f32) {
+        for (int c = 0; c < CH; ++c) {
+          if (c >= GC && c * CE + 16 / es * quad >= d) k[u][c] = u32x4_t{0, 0, 0, 0};
+          if constexpr (f32) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            sc[u] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k[u][c][i]), __uint_as_float(q[c][i]), sc[u],
-                                                         0, 0, 0);
-        } else {
-          sc[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, k[u][c]),
-                                                          __builtin_bit_cast(bf16x8_t, q[c]), sc[u], 0, 0, 0);
+            for (int i = 0; i < 4; ++i)
+              sc[u] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k[u][c][i]), __uint_as_float(q[c][i]), sc[u],
+                                                           0, 0, 0);
+          } else {
+            sc[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, k[u][c]),
+                                                            __builtin_bit_cast(bf16x8_t, q[c]), sc[u], 0, 0, 0);
+          }
         }
       }
-    }
-    // the next step's keys into the registers that have just been read
-    const bool more = st + kWaves < seg.end;
-    const Where after = pages_of(seg, st + 2 * kWaves);
-    if (more) {
-      load_k(seg, next, st + kWaves);
-    } else if (kAhead && !last) {
-      load_q(then);
-      if (ahead) load_k(then, then_now, then.st);
-    }
-    float w[VT];
-#pragma unroll
-    for (int i = 0; i < VT; ++i) w[i] = sc[i / 4][i % 4] * scale2;
-    const int t0 = st * step;
-    // the ends of the sequence and pages that are none: no score, no value
-    uint32_t in[VT];
-#pragma unroll
-    for (int i = 0; i < VT; ++i) {
-      const int t = t0 + VT * quad + i;
-      in[i] = t >= sp.first && t < sp.n && now.v < pages ? ~0u : 0u;
-      w[i] = in[i] ? w[i] : -INFINITY;
-    }
-    if (p.scores && l16 < live) {
-      float *const to = p.scores + ((int64_t)s * a.q.n + head0 + l16) * p.scores_row + t0 + VT * quad;
-#pragma unroll
-      for (int i = 0; i < VT; i += 4) *reinterpret_cast<f32x4_t *>(to + i) = f32x4_t{w[i], w[i + 1], w[i + 2], w[i + 3]};
-    }
-    // The maximum moves only when a score is 2^8 times it in weight: sums and
-    // weights then stay within 2^8 of what they would be, far from any limit,
-    // and most steps leave the sums so far as they are.
-    float top = w[0];
-#pragma unroll
-    for (int i = 1; i < VT; ++i) top = fmaxf(top, w[i]);
-    if (__any(top > m + 8.f)) {
-      const float to = fmaxf(m, quads_max(top)), fade = exp2_of(m - base_of(to));
-      m = to;
-      sum *= fade;
-      float f[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = __shfl(fade, 4 * quad + i, 64);
-#pragma unroll
-      for (int j = 0; j < NC; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][i] *= f[i];
-    }
-    const float base = base_of(m);
-#pragma unroll
-    for (int i = 0; i < VT; ++i) {
-      w[i] = exp2_of(w[i] - base);
-      sum += w[i];
-    }
-    if constexpr (f32) {
-#pragma unroll
-      for (int j = 0; j < NC; ++j)
-#pragma unroll
-        for (int e = 0; e < VT; ++e)
-          acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[e], __uint_as_float(v[e][j] & in[e]), acc[j], 0, 0, 0);
-    } else {
-      bf16x8_t hi, lo;
-      uint32_t both[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) both[t] = (in[2 * t] & 0xffffu) | (in[2 * t + 1] & 0xffff0000u);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        hi[i] = (__bf16)w[i];
-        lo[i] = (__bf16)(w[i] - (float)hi[i]);
+      // the next step's keys into the registers that have just been read
+      const bool more = st + kWaves < seg.end;
+      const Where after = pages_of(seg, st + 2 * kWaves);
+      if (more) {
+        load_k(seg, next, st + kWaves);
+      } else if (kAhead && !last) {
+        load_q(then);
+        if (ahead) load_k(then, then_now, then.st);
       }
+      float w[VT];
 #pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        u32x4_t o;
+      for (int i = 0; i < VT; ++i) w[i] = sc[i / 4][i % 4] * scale2;
+      const int t0 = st * step;
+      // the ends of the sequence and pages that are none: no score, no value
+      uint32_t in[VT];
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-          o[t] = __builtin_amdgcn_perm(v[2 * t + 1][j / 2], v[2 * t][j / 2], j & 1 ? 0x07060302u : 0x05040100u) &
-                 both[t];
-        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, __builtin_bit_cast(bf16x8_t, o), acc[j], 0, 0, 0);
-        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, __builtin_bit_cast(bf16x8_t, o), acc[j], 0, 0, 0);
+      for (int i = 0; i < VT; ++i) {
+        const int t = t0 + VT * quad + i;
+        in[i] = t >= sp.first && t < sp.n && now.v < pages ? ~0u : 0u;
+        w[i] = in[i] ? w[i] : -INFINITY;
       }
+      if (p.scores && l16 < live) {
+        float *const to = p.scores + ((int64_t)s * a.q.n + head0 + l16) * p.scores_row + t0 + VT * quad;
+#pragma unroll
+        for (int i = 0; i < VT; i += 4)
+          *reinterpret_cast<f32x4_t *>(to + i) = f32x4_t{w[i], w[i + 1], w[i + 2], w[i + 3]};
+      }
+      // The maximum moves only when a score is 2^8 times it in weight: sums and
+      // weights then stay within 2^8 of what they would be, far from any limit,
+      // and most steps leave the sums so far as they are.
+      float top = w[0];
+#pragma unroll
+      for (int i = 1; i < VT; ++i) top = fmaxf(top, w[i]);
+      if (__any(top > m + 8.f)) {
+        const float to = fmaxf(m, quads_max(top)), fade = exp2_of(m - base_of(to));
+        m = to;
+        sum *= fade;
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = __shfl(fade, 4 * quad + i, 64);
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[j][i] *= f[i];
+      }
+      const float base = base_of(m);
+#pragma unroll
+      for (int i = 0; i < VT; ++i) {
+        w[i] = exp2_of(w[i] - base);
+        sum += w[i];
+      }
+      if constexpr (f32) {
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+#pragma unroll
+          for (int e = 0; e < VT; ++e)
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[e], __uint_as_float(v[e][j] & in[e]), acc[j], 0, 0, 0);
+      } else {
+        bf16x8_t hi, lo;
+        uint32_t both[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) both[t] = (in[2 * t] & 0xffffu) | (in[2 * t + 1] & 0xffff0000u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          hi[i] = (__bf16)w[i];
+          lo[i] = (__bf16)(w[i] - (float)hi[i]);
+        }
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+          u32x4_t o;
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            o[t] = __builtin_amdgcn_perm(v[2 * t + 1][j / 2], v[2 * t][j / 2], j & 1 ? 0x07060302u : 0x05040100u) &
+                   both[t];
+          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, __builtin_bit_cast(bf16x8_t, o), acc[j], 0, 0, 0);
+          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, __builtin_bit_cast(bf16x8_t, o), acc[j], 0, 0, 0);
+        }
+      }
+      if (more)
+        load_v(seg, next, st + kWaves);
+      else if (kAhead && ahead)
+        load_v(then, then_now, then.st);
+      now = next;
+      next = after;
     }
-    if (more)
-      load_v(seg, next, st + kWaves);
-    else if (kAhead && ahead)
-      load_v(then, then_now, then.st);
-    now = next;
-    next = after;
-  }
 
-  // the four wavefronts' sums at their common maximum
-  sum = quads_sum(sum);
-  if (lane < 16) red_m[wave][lane] = m, red_l[wave][lane] = sum;
-  __syncthreads();
+    // the four wavefronts' sums at their common maximum
+    sum = quads_sum(sum);
+    if (lane < 16) red_m[wave][lane] = m, red_l[wave][lane] = sum;
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int h = 4 * quad + i;
-    float top = red_m[0][h];
-    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, red_m[w][h]);
-    const float f = exp2_of(red_m[wave][h] - base_of(top));
-    if (h < live)
+    for (int i = 0; i < 4; ++i) {
+      const int h = 4 * quad + i;
+      float top = red_m[0][h];
+      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, red_m[w][h]);
+      const float f = exp2_of(red_m[wave][h] - base_of(top));
+      if (h < live)
 #pragma unroll
-      for (int j = 0; j < NC; ++j) red[wave][h][col0 + j] = acc[j][i] * f;
-  }
-  __syncthreads();
-  const int64_t slot = (2 * (int64_t)share + (seg.skip == 0)) * p.kept;
-  for (int h = wave; h < live; h += kWaves) {
-    float top = red_m[0][h], total = 0.f;
-    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, red_m[w][h]);
-    for (int w = 0; w < kWaves; ++w) total += red_l[w][h] * exp2_of(red_m[w][h] - base_of(top));
-    const int64_t row = (int64_t)s * a.q.n + head0 + h;
-    if (lane == 0) {
-      if (whole)
-        finish_row(a, p, row, top, total);
-      else
-        p.stats[2 * (slot + h)] = top, p.stats[2 * (slot + h) + 1] = total;
+        for (int j = 0; j < NC; ++j) red[wave][h][col0 + j] = acc[j][i] * f;
     }
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    for (int c = lane; c < d; c += 64) {
-      float o = 0.f;
+    __syncthreads();
+    const int64_t slot = (2 * (int64_t)share + (seg.skip == 0)) * p.kept;
+    for (int h = wave; h < live; h += kWaves) {
+      float top = red_m[0][h], total = 0.f;
+      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, red_m[w][h]);
+      for (int w = 0; w < kWaves; ++w) total += red_l[w][h] * exp2_of(red_m[w][h] - base_of(top));
+      const int64_t row = (int64_t)s * a.q.n + head0 + h;
+      if (lane == 0) {
+        if (whole)
+          finish_row(a, p, row, top, total);
+        else
+          p.stats[2 * (slot + h)] = top, p.stats[2 * (slot + h) + 1] = total;
+      }
+      const float inv = total == 0.f ? 0.f : 1.f / total;
+      for (int c = lane; c < d; c += 64) {
+        float o = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) o += red[w][h][c];
-      if (whole)
-        reinterpret_cast<E *>(a.out.p + s * a.out.row + (head0 + h) * a.out.head)[c] = (E)(total == 0.f ? 0.f : o * inv);
-      else
-        p.partial[(slot + h) * d + c] = o;
+        for (int w = 0; w < kWaves; ++w) o += red[w][h][c];
+        if (whole)
+          reinterpret_cast<E *>(a.out.p + s * a.out.row + (head0 + h) * a.out.head)[c] =
+              (E)(total == 0.f ? 0.f : o * inv);
+        else
+          p.partial[(slot + h) * d + c] = o;
+      }
     }
-  }
-  if (last) return;
-  seg = then;
-  now = then_now, next = then_next;
-  if (!kAhead) {
-    load_q(seg);
-    if (ahead) {
-      load_k(seg, now, seg.st);
-      load_v(seg, now, seg.st);
+    if (last) return;
+    seg = then;
+    now = then_now, next = then_next;
+    if (!kAhead) {
+      load_q(seg);
+      if (ahead) {
+        load_k(seg, now, seg.st);
+        load_v(seg, now, seg.st);
+      }
     }
-  }
-  __syncthreads();  // the sums have been read
+    __syncthreads();  // the sums have been read
   }
 }
 

@@ -254,7 +254,8 @@ __device__ __forceinline__ void take_largest(Slots<NB> &sl, int count, const Key
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ void move_piece(const EvictArgs &a, int64_t from, int64_t to) {
-  const u32x4_t k = *reinterpret_cast<const u32x4_t *>(a.c.K + from), v = *reinterpret_cast<const u32x4_t *>(a.c.V + from);
+  const u32x4_t k = *reinterpret_cast<const u32x4_t *>(a.c.K + from);
+  const u32x4_t v = *reinterpret_cast<const u32x4_t *>(a.c.V + from);
   *reinterpret_cast<u32x4_t *>(a.c.K + to) = k;
   *reinterpret_cast<u32x4_t *>(a.c.V + to) = v;
 }
