@@ -8,15 +8,14 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMostPairs = 128;
-constexpr int kMostTokens = 8;  // of a workgroup
+constexpr int kMostTokens = 4;  // of a workgroup
 
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 
 // A workgroup's items one after the other: the units of its tokens' query heads,
 // of their key heads and of their value heads.  Queries go token by token, as
-// their rows lie; keys and values head by head, each for all tokens, so that
-// entries that lie side by side in a page are written together (4939 tokens of
-// 16 heads of 256 into pages of 32: 59 and 54 us).
+// their rows lie; keys and values head by head, each for all tokens, as entries
+// lie side by side in a page.
 struct Split {
   Div turn_units, copy_units;   // of a head that is turned, and of one that is copied
   Div q_heads;
@@ -126,10 +125,10 @@ __device__ __forceinline__ void store_run(uint8_t *at, const vec &v, int count) 
   }
 }
 
-// Bound by HBM for many tokens (8191 of 40 heads of 128: 168 MB in 33 us, 5.1
+// Bound by HBM for many tokens (8191 of 40 heads of 128: 168 MB in 29 us, 5.8
 // TB/s; 4939 of 16 heads of 256 with their keys and values into the pages: 243
-// MB in 55 us, 4.4 TB/s), by latency for few: the position, the sine and cosine,
-// the head.  The angles are formed once for all heads of a token.  Whole: runs of
+// MB in 54 us, 4.5 TB/s), by latency for few (one token of 16 heads of 256 3 us):
+// the position, the sine and cosine, the head.  The angles are formed once for all heads of a token.  Whole: runs of
 // 16 bytes end where the turned part does; otherwise the turned part, what lies
 // before it and what lies behind are cut into runs each by itself, the last one
 // shorter, at any address (333 tokens of 40 fp32 heads of 200: all turned in
@@ -138,7 +137,9 @@ template <typename E, bool Halves, bool Whole>
 __global__ void __launch_bounds__(kThreads, 8) rotate_kernel(RotateArgs a, Split sp) {
   __shared__ Tokens k;
   constexpr int es = sizeof(E), V = 16 / es;
-  constexpr int kAhead = Halves ? (Whole ? 2 : 1) : (Whole ? 4 : 2);  // items of a thread under way
+  // items of a thread under way: 64 bytes read, and half for runs of any length,
+  // as much as eight wavefronts' registers hold
+  constexpr int kAhead = Halves ? (Whole ? 2 : 1) : (Whole ? 4 : 2);
   typedef E vec __attribute__((ext_vector_type(V)));
   const int group = blockIdx.x / sp.strips, strip = blockIdx.x - group * sp.strips;
   const int t0 = group * sp.tokens, tokens = min(sp.tokens, a.T - t0), pairs = a.turned / 2;
@@ -221,8 +222,14 @@ gsi_status launch_as(const RotateArgs &a, bool whole, hipStream_t st) {
   sp.q_items = a.q.n * turn_units;
   sp.k_items = sp.q_items + a.k.n * turn_units;
   sp.items = sp.k_items + a.v.n * copies;
-  // Tokens share a workgroup where there are enough of them to fill the chip.
-  sp.tokens = a.T >= 2048 ? kMostTokens : 1;
+  // Tokens share a workgroup, and with it the wait for positions and pages, where
+  // there are enough to fill the chip and one has little to move.  One token and
+  // four, us, bf16 in halves: 8191 of 8 heads of 64 9.2 and 5.7, of 16 heads of 128 13.4
+  // and 12.6, of 24 17.3 and 18.0, of 40 29.3 and 32.4; into pages, 3 prompts up to
+  // 16000 of 8 query and 8 key heads of 64 32.5 and 23.0, of 16 and 16 of 256 169 and
+  // 187; 1000 of 8 heads of 128 4.0 and 3.9, of 16 heads of 256 6.0 and 6.5.
+  const int bytes = (a.q.n + a.k.n + a.v.n) * a.d * (int)sizeof(E);
+  sp.tokens = a.T >= 2048 && bytes < 6144 ? kMostTokens : 1;
   const int64_t groups = ((int64_t)a.T + sp.tokens - 1) / sp.tokens;
   const int64_t per = ((int64_t)sp.tokens * sp.items + kThreads - 1) / kThreads;
   const int64_t most = 2048 / groups > 1 ? 2048 / groups : 1;
