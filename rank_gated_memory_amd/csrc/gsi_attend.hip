@@ -28,7 +28,11 @@
 // needed.  With fewer than 16 query heads the other rows of the tile are idle:
 // at 16 B a clock and CU from HBM the matrix cores are at 5 % (bf16) or 30 %
 // (fp32) of their rate even then.  More than 16 are further rows, which read keys
-// and values again.  (Two tiles in one pass were no faster: 64 sequences of 2000
+// and values again.  Bound by HBM where the lengths fill the chip: two sequences of
+// 131071 slots, 8 heads of 128, 537 MB in 100 us, 5.4 TB/s; 64 of 1 to 4096 slots, 40
+// heads of 128, 700 MB in 160 us with the scores kept, 4.4.  One sequence of 1777
+// slots of 16 heads of 256, 29 MB, takes 12 us and 4 for the join, a page number's,
+// the keys' and the values' latency after the launch's.  (Two tiles in one pass were no faster: 64 sequences of 2000
 // slots, one key head for 32: 38 us in two rows and 39 in one; one of 65536: 25
 // and 40, for the larger sums to join.)
 //
@@ -180,9 +184,8 @@ __device__ __forceinline__ void finish_row(const AttendArgs &a, const Plan &p, i
   if (p.level) p.level[row] = total == 0.f ? INFINITY : level;
 }
 
-// KS: the head's size in units of 32, rounded up.  Uniform: a page holds whole
-// steps, so that a step has one page; otherwise each 8 slots have one.
-template <typename E, int KS, bool Uniform>
+// KS: the head's size in units of 32, rounded up.
+template <typename E, int KS>
 __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) attend_kernel(AttendArgs a, Plan p) {
   constexpr bool f32 = sizeof(E) == 4;
   constexpr int es = sizeof(E), step = kStep<E>;
@@ -193,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
   constexpr int NC = 2 * KS;               // columns of a value that a lane holds
   constexpr int VD = NC * es / 4;          // dwords
   // whether the next segment's first loads go out before the present one is done:
-  // for large fp32 heads there are no registers for it
+  // for fp32 heads above 96 there are no registers for it
   constexpr bool kAhead = !f32 || KS <= 3;
   constexpr int GC = CH - (f32 ? 2 : 1) * (KS > 4 ? 2 : 1);  // pieces from here on may lie behind the key
   __shared__ float red[kWaves][16][32 * KS];
@@ -235,11 +238,12 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
     place(seg);
   }
 
-  // this lane's first column, and its offsets from the start of a step (of a
-  // block of 8 slots): the last run of columns ends with the value
+  // A lane's keys (and its values) of a step lie in one block of 8 slots, so in one
+  // page.  Its first column, and its offsets from the start of the block: the last
+  // run of columns ends with the value.  (One page for a whole step, in scalar
+  // registers, where pages hold whole steps: 3 % slower to 2 % faster.)
   const int col0 = min(l16 * NC, d - NC);
-  const int ktoken = f32 ? (Uniform ? l16 : l16 & 7) : (Uniform ? 8 * (l16 >> 2) : 0) + (l16 & 3);
-  const int vtoken = f32 ? (Uniform ? 4 * quad : 4 * (quad & 1)) : (Uniform ? 8 * quad : 0);
+  const int ktoken = f32 ? l16 & 7 : l16 & 3, vtoken = f32 ? 4 * (quad & 1) : 0;
   const int kblock = f32 ? l16 >> 3 : l16 >> 2, vblock = f32 ? quad >> 1 : quad;
   const uint32_t ss = (uint32_t)a.c.slot_stride, pages = a.c.pages;
   const uint32_t ko = ktoken * ss + 16 * quad, vo = vtoken * ss + col0 * es;
@@ -254,15 +258,9 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
   const auto pages_of = [&](const Segment &g, int st) {
     const int32_t *const table = a.c.table + g.s * a.c.ld;
     const auto page = [&](int t) { return (uint32_t)table[min(t, g.sp.n - 1) >> a.c.shift]; };
-    if constexpr (Uniform) {
-      const uint32_t w = page(st * step);
-      return Where{w, w};
-    } else {
-      return Where{page(st * step + 8 * kblock), page(st * step + 8 * vblock)};
-    }
+    return Where{page(st * step + 8 * kblock), page(st * step + 8 * vblock)};
   };
   const auto start_of = [&](const Segment &g, uint32_t page, int t) {
-    if constexpr (Uniform) page = __builtin_amdgcn_readfirstlane(page);
     return entry_at(a.c, page < pages ? page : 0, g.kh, t);
   };
   u32x4_t q[CH];  // this lane's query head as the operand B of S^T
@@ -281,18 +279,11 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
   // The addresses are formed one after the other: all at once they would take as
   // many registers as what they load.
   const auto here = [](const uint8_t *at) {
-    if constexpr (Uniform) {
-      const uint64_t p = reinterpret_cast<uint64_t>(at);
-      const uint32_t low = __builtin_amdgcn_readfirstlane((int)p);
-      const uint32_t high = __builtin_amdgcn_readfirstlane((int)(p >> 32));
-      return reinterpret_cast<const uint8_t *>(low | (uint64_t)high << 32);
-    } else {
-      asm volatile("" : "+v"(at));
-      return at;
-    }
+    asm volatile("" : "+v"(at));
+    return at;
   };
   const auto load_k = [&](const Segment &g, const Where &w, int st) {
-    const uint8_t *at = here(a.c.K + start_of(g, w.k, st * step + (Uniform ? 0 : 8 * kblock)));
+    const uint8_t *at = here(a.c.K + start_of(g, w.k, st * step + 8 * kblock));
 #pragma unroll
     for (int u = 0; u < KT; ++u) {
 #pragma unroll
@@ -300,18 +291,18 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
         const uint32_t in = c < GC || c * CE + 16 / es * quad < d ? c * 64 : 0;
         k[u][c] = *reinterpret_cast<const u32x4_t *>(at + (ko + in));
       }
-      if (u + 1 < KT) at = Uniform ? at + 4 * (uint64_t)ss : here(at + 4 * (uint64_t)ss);
+      if (u + 1 < KT) at = here(at + 4 * (uint64_t)ss);
     }
   };
   const auto load_v = [&](const Segment &g, const Where &w, int st) {
-    const uint8_t *at = here(a.c.V + start_of(g, w.v, st * step + (Uniform ? 0 : 8 * vblock)));
+    const uint8_t *at = here(a.c.V + start_of(g, w.v, st * step + 8 * vblock));
     struct Run {
       uint32_t w[VD];
     };
 #pragma unroll
     for (int e = 0; e < VT; ++e) {
       __builtin_memcpy(v[e], at + vo, sizeof(Run));
-      at = Uniform ? at + ss : here(at + ss);
+      at = here(at + ss);
     }
   };
 
@@ -625,10 +616,10 @@ constexpr int kMassSlots = 256;  // of a strip
 constexpr int kMassGrid = 2048;
 
 // The strips of kMassSlots slots of all sequences and key heads, four slots a
-// lane, which lie in one page.  `sharers` wavefronts (1, 2 or 4) divide a strip's
-// query heads.  Bound by latency: lengths, pages, then masses and scores.  (A
-// strip for a whole workgroup, one slot a thread: 14.5 us for 64 ragged
-// sequences of 40 heads, 4.0 us for 24 of 2 heads of 32.)
+// lane, which lie in one page.  `sharers` wavefronts (1 or 4) divide a strip's
+// query heads.  Bound by latency: lengths, pages, then masses and scores.  64
+// ragged sequences of 40 heads: 9.7 us, 24 of 2 key heads of 32 query heads 4.1 us.
+// (A strip for a whole workgroup, one slot a thread: 14.5 and 4.0 us.)
 __global__ void __launch_bounds__(kThreads) mass_kernel(AttendArgs a, Plan p, int sharers) {
   __shared__ __attribute__((aligned(16))) float sums[kWaves][kMassSlots];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -684,7 +675,10 @@ __global__ void __launch_bounds__(kThreads) mass_kernel(AttendArgs a, Plan p, in
   }
 }
 
-// Workgroups that the chip holds at once, by the registers of the kernel.
+// Workgroups that the chip holds at once, by the registers of the kernel.  With as
+// many for each CU as with one more and one less (us): 64 ragged sequences of 40
+// heads of 128: 2 182, 3 199, 1 212; 16 of 4000 slots, 8 heads of 64: 3 31.6, 2 31.0,
+// 4 34.8; of 256: 1 103, 2 110.
 inline int shares_for(int d) { return 256 * (d <= 64 ? 3 : d <= 128 ? 2 : 1); }
 
 template <typename E>
@@ -720,13 +714,8 @@ gsi_status launch_as(const AttendArgs &a, hipStream_t st) {
   // units of all sequences, a unit each at least, are counted in 32 bits
   if ((((int64_t)a.c.most << a.c.shift) / 64 + 1) * a.c.S > INT32_MAX) return GSI_E_SHAPE;
   const unsigned grid = p.shares;
-  const bool uniform = 1 << a.c.shift >= kStep<E>;
   const auto go = [&](auto ks) {
-    constexpr int KS = decltype(ks)::value;
-    if (uniform)
-      attend_kernel<E, KS, true><<<grid, kThreads, 0, st>>>(a, p);
-    else
-      attend_kernel<E, KS, false><<<grid, kThreads, 0, st>>>(a, p);
+    attend_kernel<E, decltype(ks)::value><<<grid, kThreads, 0, st>>>(a, p);
   };
   const int ks = (a.c.d + 31) / 32;
   if (ks == 1)
@@ -745,15 +734,21 @@ gsi_status launch_as(const AttendArgs &a, hipStream_t st) {
   if (p.stats && p.shares > 1) {
     const int most = heads_at_once(a.c.d), sets = (p.kept + most - 1) / most;
     const int64_t by_cuts = (int64_t)(p.shares - 1) * sets, by_heads = (int64_t)a.c.S * a.q.n;
-    // a query head for each workgroup has more threads for many pieces, as long
-    // as they run at once
+    // A query head for each workgroup has more threads for many pieces, as long as
+    // they run at once.  By heads and by cuts, us more or less of a call: 2000
+    // slots of 2 key heads for 64, 4 sequences (256 heads) 2.2 less, 24 (1536) 0.7
+    // less, 64 (4096) 5.5 more; 8 for 32, 24 sequences (768) 0.3 less, 48 (1536)
+    // 1.6 more, 96 4.0 more.
     const bool cuts = by_heads > 2048 && by_cuts < by_heads;
     join_kernel<E><<<(unsigned)(cuts ? by_cuts : by_heads), kThreads, 0, st>>>(a, p, cuts, sets);
     if (hipGetLastError() != hipSuccess) return GSI_E_HIP;
   }
   if (a.accumulate && a.c.most > 0) {
     const int64_t strips = (((int64_t)a.c.most << a.c.shift) + kMassSlots - 1) / kMassSlots * a.c.S * a.c.heads;
-    const int sharers = a.group >= 4 ? 4 : a.group >= 2 ? 2 : 1, at_once = kWaves / sharers;
+    // A wavefront alone where its heads' scores are one round of loads: with four
+    // for a strip 64 sequences of 2000 slots, 8 key heads for 64, take 1.3 us more;
+    // 24 sequences of 2 key heads of 32 take 2.3 us less.
+    const int sharers = a.group > 8 ? 4 : 1, at_once = kWaves / sharers;
     const int64_t grid = std::min<int64_t>((strips + at_once - 1) / at_once, kMassGrid);
     mass_kernel<<<(unsigned)grid, kThreads, 0, st>>>(a, p, sharers);
     if (hipGetLastError() != hipSuccess) return GSI_E_HIP;

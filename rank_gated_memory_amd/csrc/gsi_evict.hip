@@ -13,7 +13,8 @@
 // slots one after the other, which lie in one page, so that a load of 16 bytes
 // reads them; up to 32768 slots stay in registers and are read once.  A call for
 // a few thousand slots is bound by the latency of these reads and of the dozen
-// barriers behind them, one for long sequences by the counting in LDS.
+// barriers behind them (2049 slots, 128 workgroups: 12 us), one for long sequences by
+// the counting in LDS of one CU each (30011 slots, 24 workgroups: 44 us).
 #include <algorithm>
 #include <utility>
 
@@ -24,7 +25,9 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
-constexpr int kFewMoves = 64;  // that select_kernel makes itself
+// Moves that select_kernel makes itself.  16 sequences of 8 heads to 2048 of 2049
+// (2112) entries: 13.2 (15.4) us, with move_kernel 21.9 (23.7).
+constexpr int kFewMoves = 64;
 
 // Keys whose unsigned order is that of the scores.  NaN and an entry of no page
 // are the least; the two zeros are alike.
@@ -307,17 +310,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(EvictArgs a, int block
     return r;
   };
   for (int k = tid; k < 2 * 4 * 256; k += kThreads) (&sh.hist[0][0][0])[k] = 0;
-  // All reads of a selection at once, those of both where there are registers.
-  constexpr bool kBoth = NB <= 8;
   int p[NB > 0 ? NB : 1];
   Four age[NB > 0 ? NB : 1], mass[NB > 0 ? NB : 1];
-  const auto read_masses = [&] {
-    sl.each([&](auto k, int b) { mass[k] = read(a.c.mass, p[k], b); });
-  };
-  if constexpr (NB > 0) {
+  if constexpr (NB > 0) {  // all reads of both selections at once
     sl.each([&](auto k, int b) { p[k] = raw_page(b); });
     if (by_age) sl.each([&](auto k, int b) { age[k] = read(a.c.age, p[k], b); });
-    if (kBoth && by_mass) read_masses();
+    if (by_mass) sl.each([&](auto k, int b) { mass[k] = read(a.c.mass, p[k], b); });
     if (by_age) sl.each([&](auto k, int) { age[k] = age_keys(p[k], age[k]); });
   } else {
     for (int k = tid; k < 4 * nb; k += kThreads) sl.keep[k] = 0;
@@ -337,10 +335,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(EvictArgs a, int block
     __syncthreads();
   }
   if (by_mass) {
-    if constexpr (NB > 0) {
-      if (!kBoth) read_masses();
-      sl.each([&](auto k, int) { mass[k] = mass_keys(p[k], mass[k]); });
-    }
+    if constexpr (NB > 0) sl.each([&](auto k, int) { mass[k] = mass_keys(p[k], mass[k]); });
     take_largest<false>(sl, budget - a.recent, [&](auto k, int b) {
       if constexpr (NB > 0) return mass[k];
       const int page = raw_page(b);
@@ -430,7 +425,9 @@ __global__ void __launch_bounds__(kThreads) select_kernel(EvictArgs a, int block
 
 constexpr int kMoveRows = 2;  // of a thread
 
-// 16 bytes of a key and of a value per thread and row; `side` rows at a time.
+// 16 bytes of a key and of a value per thread and row.  Reads and writes all that
+// moves once: 98304000 bytes of 24 heads' entries into other pages in 23 us, 4.3
+// TB/s (with 4 rows a thread 29 us).
 __global__ void __launch_bounds__(256) move_kernel(EvictArgs a, int strips, Div pieces) {
   const int sh = blockIdx.x / strips, strip = blockIdx.x - sh * strips, s = sh / a.c.heads, h = sh - s * a.c.heads;
   const int rows = 256 / pieces.by, row = quotient(threadIdx.x, pieces), piece = threadIdx.x - row * pieces.by;
@@ -479,6 +476,9 @@ gsi_status launch_evict(const EvictArgs &a, int dtype, hipStream_t st) {
   if (rows * kThreads > kMostLaunch || rows * strips * 256 > kMostLaunch) return GSI_E_SHAPE;
   const int holes = std::max(1, std::min({a.budget, slots - a.budget, 8192}));
   const size_t lds = (size_t)blocks * 36 + (size_t)holes * 4;
+  // As few blocks of keys in registers as hold the slots, us with 1, 2, 8 and 0 (in
+  // memory) of a wavefront: 2049 to 2048 12.9, 13.5, 17.4, 17.6; 5003 to 777 (fp32)
+  // -, 22.0, 25.9, 28.1; 30011 to 4000 -, -, 63.6, 79.6.
   if (slots <= kWaves * kBlock)
     select_kernel<1><<<(unsigned)rows, kThreads, lds, st>>>(a, blocks, holes, pieces);
   else if (slots <= 2 * kWaves * kBlock)
