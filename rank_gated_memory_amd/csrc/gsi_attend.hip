@@ -1,13 +1,14 @@
 // Attention of one new token of every sequence over the paged cache on gfx950
 // MFMA (gsi_cache_attend).
 //
-//   attend_kernel : the slots of a sequence, key head and up to 16 query heads of
-//                   it (a row) are counted in units, four steps of 32 slots
-//                   (bf16; 16 in fp32), one for each wavefront of a workgroup.
-//                   All rows' units, one after the other, are dealt to as many
-//                   workgroups as the chip holds at once in equal shares, from
-//                   the lengths as they are: no workgroup is idle however the
-//                   lengths differ.  A step's keys and values are read once,
+//   attend_kernel : the slots of a sequence and key head (a row) are counted in
+//                   units, four steps of 32 slots (bf16; 16 in fp32), one for each
+//                   wavefront of a workgroup.  All rows' units, one after the
+//                   other, are dealt to as many workgroups as the chip holds at
+//                   once in equal shares, from the lengths as they are: no
+//                   workgroup is idle however the lengths differ.  A workgroup
+//                   takes up to 16 query heads of its rows (a tile); where a key
+//                   head has more, a share has a workgroup for each tile.  A step's keys and values are read once,
 //                   straight into the registers that the matrix instructions
 //                   take them from.  One pass with the running maximum and sum
 //                   of the softmax; wavefronts are joined through LDS.
@@ -27,8 +28,10 @@
 // run.  No value goes through LDS and no layout of the pool other than rows is
 // needed.  With fewer than 16 query heads the other rows of the tile are idle:
 // at 16 B a clock and CU from HBM the matrix cores are at 5 % (bf16) or 30 %
-// (fp32) of their rate even then.  More than 16 are further rows, which read keys
-// and values again.  Bound by HBM where the lengths fill the chip: two sequences of
+// (fp32) of their rate even then.  The workgroups of a share's tiles run on one XCD
+// at one time, so that one of them reads from HBM and all from its L2: 64 sequences
+// of 2000 slots, 8 key heads for 256, 524 MB, 119 us; with tiles as further rows 190,
+// 16 query heads for each key head 100.  Bound by HBM where the lengths fill the chip: two sequences of
 // 131071 slots, 8 heads of 128, 537 MB in 100 us, 5.4 TB/s; 64 of 1 to 4096 slots, 40
 // heads of 128, 700 MB in 160 us with the scores kept, 4.4.  One sequence of 1777
 // slots of 16 heads of 256, 29 MB, takes 12 us and 4 for the join, a page number's,
@@ -57,12 +60,12 @@ constexpr int kWaves = kThreads / 64;
 // two rows unfinished: 2 b for one that an earlier workgroup has begun, 2 b + 1
 // for one that it begins.
 struct Plan {
-  int tiles;   // rows of a key head
-  int kept;    // query heads of a row at most
-  int shares;  // workgroups
+  int tiles;   // of a key head
+  int kept;    // query heads of a tile at most
+  int shares;  // workgroups of a tile
   int scores_row;
-  float *stats;    // [2 shares][kept]: maximum (times log2 e) and sum
-  float *partial;  // [2 shares][kept][d], sums at that maximum
+  float *stats;    // [tiles][2 shares][kept]: maximum (times log2 e) and sum
+  float *partial;  // [tiles][2 shares][kept][d], sums at that maximum
   float *level;    // [S * heads]: log2 of the sum of all weights, infinity for none
   float *scores;   // [S * heads][scores_row], times log2 e
 };
@@ -153,7 +156,7 @@ struct Shares {
   __device__ __forceinline__ int owner(int64_t unit) const { return (int)over((unit + 1) * of - 1, all); }
 };
 __device__ __forceinline__ Shares shares_of(const AttendArgs &a, const Plan &p, int units) {
-  const int64_t all = (int64_t)units * (a.c.heads * p.tiles);
+  const int64_t all = (int64_t)units * a.c.heads;
   return {all, (int)min((int64_t)p.shares, all)};
 }
 
@@ -204,7 +207,9 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int quad = lane >> 4, l16 = lane & 15, d = a.c.d;
-  const int share = blockIdx.x, rows = a.c.heads * p.tiles;  // of a sequence
+  // eight shares' first tiles, their second ones ..: workgroups go to the XCDs in turn
+  const int eight = blockIdx.x / 8, tile = p.tiles == 1 ? 0 : eight % p.tiles;
+  const int share = eight / p.tiles * 8 + blockIdx.x % 8, rows = a.c.heads;  // of a sequence
   const auto units_of = [&](int n) { return span_of<E>(a, n).units; };
   const Counted counted(a, units_of);
   const Shares sh = shares_of(a, p, counted.sum);
@@ -214,12 +219,10 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
   // A row's part in this share: its units from `skip` on, `mine` of them, and of
   // this wavefront the steps st, st + kWaves, .. below end.
   struct Segment {
-    int s, row_at, kh, tile, skip, mine, st, end;
+    int s, kh, skip, mine, st, end;
     Span sp;
   };
   const auto place = [&](Segment &g) {
-    g.kh = p.tiles == 1 ? g.row_at : (int)over(g.row_at, p.tiles);
-    g.tile = g.row_at - g.kh * p.tiles;
     g.mine = (int)min((int64_t)(g.sp.units - g.skip), left);
     g.st = g.sp.lo + g.skip * kWaves + wave;
     g.end = g.sp.lo + min(g.sp.steps, (g.skip + g.mine) * kWaves);
@@ -232,8 +235,8 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
     const int64_t in_rows = unit - (int64_t)at.before * rows;
     seg.s = at.s;
     seg.sp = span_of<E>(a, at.n);
-    seg.row_at = (int)over(in_rows, seg.sp.units);
-    seg.skip = (int)(in_rows - (int64_t)seg.row_at * seg.sp.units);
+    seg.kh = (int)over(in_rows, seg.sp.units);
+    seg.skip = (int)(in_rows - (int64_t)seg.kh * seg.sp.units);
     left -= unit;
     place(seg);
   }
@@ -267,8 +270,8 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
   u32x4_t k[KT][CH];
   uint32_t v[VT][VD];
   const auto load_q = [&](const Segment &g) {
-    const int live = a.group - g.tile * 16;
-    const uint8_t *const at = a.q.p + g.s * a.q.row + (g.kh * a.group + g.tile * 16 + l16) * a.q.head;
+    const int live = a.group - tile * 16;
+    const uint8_t *const at = a.q.p + g.s * a.q.row + (g.kh * a.group + tile * 16 + l16) * a.q.head;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int e = c * CE + 16 / es * quad;
@@ -323,8 +326,8 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
     Segment then = seg;
     Where then_now{}, then_next{};
     if (!last) {  // then this segment ends its row
-      if (++then.row_at == rows) {
-        then.row_at = 0;
+      if (++then.kh == rows) {
+        then.kh = 0;
         then.sp = span_of<E>(a, __builtin_amdgcn_readfirstlane(clamped_length(a.c, a.lengths, ++then.s)));
       }
       then.skip = 0;
@@ -336,8 +339,8 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
     }
     const bool ahead = !last && then.st < then.end;
     const bool whole = seg.mine == seg.sp.units;
-    const int s = seg.s, live = min(16, a.group - seg.tile * 16);  // query heads of this tile
-    const int head0 = seg.kh * a.group + seg.tile * 16;
+    const int s = seg.s, live = min(16, a.group - tile * 16);  // query heads of this tile
+    const int head0 = seg.kh * a.group + tile * 16;
     const Span &sp = seg.sp;
 
     f32x4_t acc[NC];
@@ -471,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
         for (int j = 0; j < NC; ++j) red[wave][h][col0 + j] = acc[j][i] * f;
     }
     __syncthreads();
-    const int64_t slot = (2 * (int64_t)share + (seg.skip == 0)) * p.kept;
+    const int64_t slot = (2 * ((int64_t)tile * p.shares + share) + (seg.skip == 0)) * p.kept;
     for (int h = wave; h < live; h += kWaves) {
       float top = red_m[0][h], total = 0.f;
       for (int w = 1; w < kWaves; ++w) top = fmaxf(top, red_m[w][h]);
@@ -517,8 +520,8 @@ struct Stat {
 // Query heads that a workgroup of join_kernel takes: four columns a thread.
 inline __host__ __device__ int heads_at_once(int d) { return max(1, 4 * kThreads / d); }
 
-// Joins the rows that are cut.  By `cuts`, `sets` workgroups for each share's end
-// join the row that this end cuts, if no earlier one cuts it, heads_at_once()
+// Joins the rows that are cut.  By `cuts`, `sets` workgroups for each tile and share's
+// end join the row that this end cuts, if no earlier one cuts it, heads_at_once()
 // query heads each; otherwise a workgroup takes a query head of a sequence.
 // All latency: the lengths, and then all pieces' statistics and sums at once.
 // (A first round for the statistics and second ones for eight pieces at a time
@@ -528,25 +531,25 @@ template <typename E>
 __global__ void __launch_bounds__(kThreads) join_kernel(AttendArgs a, Plan p, bool cuts, int sets) {
   __shared__ __attribute__((aligned(16))) float red[kThreads * 4];
   __shared__ float red_m[kThreads], red_l[kThreads];
-  const int tid = threadIdx.x, d = a.c.d, rows = a.c.heads * p.tiles;
+  const int tid = threadIdx.x, d = a.c.d, rows = a.c.heads;
   const auto units_of = [&](int n) { return span_of<E>(a, n).units; };
   const Counted counted(a, units_of);
   const Shares sh = shares_of(a, p, counted.sum);
   int64_t start;
   int s, first, units, kh, tile, in_tile, live;
   if (cuts) {
-    const int share = blockIdx.x / sets + 1, most = heads_at_once(d);
+    const int set = blockIdx.x % sets, most = heads_at_once(d), share = blockIdx.x / sets % (p.shares - 1) + 1;
+    tile = blockIdx.x / sets / (p.shares - 1);
     if (share >= sh.of) return;
     const int64_t cut = sh.begin(share);
     const Sequence at = counted.of_thing((int)over(cut, rows));
     s = at.s;
     units = units_of(at.n);
-    const int row_at = (int)over(cut - (int64_t)at.before * rows, units);
-    start = (int64_t)at.before * rows + (int64_t)row_at * units;
+    kh = (int)over(cut - (int64_t)at.before * rows, units);
+    start = (int64_t)at.before * rows + (int64_t)kh * units;
     first = sh.owner(start);
     if (cut == start || share != first + 1) return;
-    kh = row_at / p.tiles, tile = row_at - kh * p.tiles;
-    in_tile = (blockIdx.x - (share - 1) * sets) * most;
+    in_tile = set * most;
     live = min(min(16, a.group - tile * 16) - in_tile, most);
     if (live <= 0) return;
   } else {
@@ -555,7 +558,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttendArgs a, Plan p, bo
     kh = h / a.group, tile = (h - kh * a.group) / 16, in_tile = (h - kh * a.group) % 16, live = 1;
     const Sequence at = counted.number(s);
     units = units_of(at.n);
-    start = (int64_t)at.before * rows + (int64_t)(kh * p.tiles + tile) * units;
+    start = (int64_t)at.before * rows + (int64_t)kh * units;
     first = sh.owner(start);
   }
   const int pieces = sh.owner(start + units - 1) - first + 1;
@@ -575,7 +578,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttendArgs a, Plan p, bo
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const int i = min(i0 + k * sides, pieces - 1);
-        const int64_t at = (2 * (int64_t)(first + i) + (i == 0)) * p.kept + in_tile + h;
+        const int64_t at = (2 * ((int64_t)tile * p.shares + first + i) + (i == 0)) * p.kept + in_tile + h;
         u[k] = *reinterpret_cast<const f32x4_t *>(p.partial + at * d + c);
         t[k] = *reinterpret_cast<const Stat *>(p.stats + 2 * at);
       }
@@ -688,7 +691,9 @@ Plan plan_of(const Pool &c, int q_heads, bool accumulate, uint8_t *ws, size_t *b
   const int64_t units = std::max<int64_t>(1, (slots + kWaves * kStep<E> - 1) / (kWaves * kStep<E>));
   p.tiles = (q_heads / c.heads + 15) / 16;
   p.kept = std::min(q_heads / c.heads, 16);
-  p.shares = (int)std::min<int64_t>(shares_for(c.d), c.S * units * c.heads * p.tiles);
+  // of each tile as many on every XCD, or some would wait for a place
+  const int shares = std::max(8, shares_for(c.d) / p.tiles / 8 * 8);
+  p.shares = (int)std::min<int64_t>(shares, c.S * units * c.heads);
   p.scores_row = (int)((slots + 31) / 32 * 32);
   size_t at = 0;
   const auto take = [&](size_t floats) {
@@ -697,8 +702,8 @@ Plan plan_of(const Pool &c, int q_heads, bool accumulate, uint8_t *ws, size_t *b
     return r;
   };
   if (units > 1) {
-    p.stats = take((size_t)p.shares * 2 * p.kept * 2);
-    p.partial = take((size_t)p.shares * 2 * p.kept * c.d);
+    p.stats = take((size_t)p.tiles * p.shares * 2 * p.kept * 2);
+    p.partial = take((size_t)p.tiles * p.shares * 2 * p.kept * c.d);
   }
   if (accumulate) {
     p.level = take((size_t)c.S * q_heads);
@@ -713,7 +718,7 @@ gsi_status launch_as(const AttendArgs &a, hipStream_t st) {
   const Plan p = plan_of<E>(a.c, a.q.n, a.accumulate, a.ws, nullptr);
   // units of all sequences, a unit each at least, are counted in 32 bits
   if ((((int64_t)a.c.most << a.c.shift) / 64 + 1) * a.c.S > INT32_MAX) return GSI_E_SHAPE;
-  const unsigned grid = p.shares;
+  const unsigned grid = (p.shares + 7) / 8 * 8 * p.tiles;
   const auto go = [&](auto ks) {
     attend_kernel<E, decltype(ks)::value><<<grid, kThreads, 0, st>>>(a, p);
   };
@@ -733,7 +738,7 @@ gsi_status launch_as(const AttendArgs &a, hipStream_t st) {
   if (hipGetLastError() != hipSuccess) return GSI_E_HIP;
   if (p.stats && p.shares > 1) {
     const int most = heads_at_once(a.c.d), sets = (p.kept + most - 1) / most;
-    const int64_t by_cuts = (int64_t)(p.shares - 1) * sets, by_heads = (int64_t)a.c.S * a.q.n;
+    const int64_t by_cuts = (int64_t)(p.shares - 1) * p.tiles * sets, by_heads = (int64_t)a.c.S * a.q.n;
     // A query head for each workgroup has more threads for many pieces, as long as
     // they run at once.  By heads and by cuts, us more or less of a call: 2000
     // slots of 2 key heads for 64, 4 sequences (256 heads) 2.2 less, 24 (1536) 0.7
