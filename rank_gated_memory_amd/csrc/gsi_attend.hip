@@ -571,12 +571,14 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttendArgs a, Plan p, bo
     constexpr int kAhead = 12;
     f32x4_t o = {0, 0, 0, 0};
     Stat all{-INFINITY, 0.f};
-    for (int i0 = side; i0 < pieces; i0 += kAhead * sides) {
-      f32x4_t u[kAhead];
-      Stat t[kAhead];
+    for (int at0 = 0; at0 < pieces; at0 += kAhead * sides) {
+      const int i0 = at0 + side;
+      f32x4_t u[kAhead] = {};
+      Stat t[kAhead] = {};
       float top = all.m;
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
+        if (at0 + k * sides >= pieces) continue;  // of every side
         const int i = min(i0 + k * sides, pieces - 1);
         const int64_t at = (2 * ((int64_t)tile * p.shares + first + i) + (i == 0)) * p.kept + in_tile + h;
         u[k] = *reinterpret_cast<const f32x4_t *>(p.partial + at * d + c);
