@@ -50,6 +50,7 @@ namespace gsi {
 namespace {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 
@@ -202,7 +203,8 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
   // for fp32 heads above 96 there are no registers for it
   constexpr bool kAhead = !f32 || KS <= 3;
   constexpr int GC = CH - (f32 ? 2 : 1) * (KS > 4 ? 2 : 1);  // pieces from here on may lie behind the key
-  __shared__ float red[kWaves][16][32 * KS];
+  // rows of 16-byte pieces, four rows apart on other banks
+  __shared__ __attribute__((aligned(16))) float red[kWaves][16][32 * KS + 4];
   __shared__ float red_m[kWaves][16], red_l[kWaves][16];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -459,43 +461,53 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
       next = after;
     }
 
-    // the four wavefronts' sums at their common maximum
+    // The four wavefronts' sums at their common maximum.  Every wavefront has every
+    // head's, in lane l16; a thread then adds four columns of a head.
     sum = quads_sum(sum);
     if (lane < 16) red_m[wave][lane] = m, red_l[wave][lane] = sum;
     __syncthreads();
+    float ms[kWaves], ls[kWaves];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) ms[w] = red_m[w][l16], ls[w] = red_l[w][l16];
+    const float top = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3])), base = base_of(top), fade = exp2_of(m - base);
+    float total = 0.f, f[4];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) total += ls[w] * exp2_of(ms[w] - base);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __shfl(fade, 4 * quad + i, 64);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int h = 4 * quad + i;
-      float top = red_m[0][h];
-      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, red_m[w][h]);
-      const float f = exp2_of(red_m[wave][h] - base_of(top));
-      if (h < live)
+      if (4 * quad + i >= live) continue;
 #pragma unroll
-        for (int j = 0; j < NC; ++j) red[wave][h][col0 + j] = acc[j][i] * f;
+      for (int j = 0; j < NC; j += 2)
+        *reinterpret_cast<f32x2_t *>(&red[wave][4 * quad + i][col0 + j]) = f32x2_t{acc[j][i] * f[i], acc[j + 1][i] * f[i]};
     }
     __syncthreads();
     const int64_t slot = (2 * ((int64_t)tile * p.shares + share) + (seg.skip == 0)) * p.kept;
-    for (int h = wave; h < live; h += kWaves) {
-      float top = red_m[0][h], total = 0.f;
-      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, red_m[w][h]);
-      for (int w = 0; w < kWaves; ++w) total += red_l[w][h] * exp2_of(red_m[w][h] - base_of(top));
-      const int64_t row = (int64_t)s * a.q.n + head0 + h;
-      if (lane == 0) {
-        if (whole)
-          finish_row(a, p, row, top, total);
-        else
-          p.stats[2 * (slot + h)] = top, p.stats[2 * (slot + h) + 1] = total;
-      }
-      const float inv = total == 0.f ? 0.f : 1.f / total;
-      for (int c = lane; c < d; c += 64) {
-        float o = 0.f;
+    if (wave == 0 && lane < live) {
+      if (whole)
+        finish_row(a, p, (int64_t)s * a.q.n + head0 + lane, top, total);
+      else
+        *reinterpret_cast<f32x2_t *>(p.stats + 2 * (slot + lane)) = f32x2_t{top, total};
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;  // zero for a head without a weight
+    constexpr int W = KS == 3 ? 32 : KS == 6 ? 64 : 8 * KS;  // threads of a head
+    const int c = 4 * (threadIdx.x % W);
+    for (int h0 = 0; h0 < live; h0 += kThreads / W) {
+      const int h = h0 + threadIdx.x / W;
+      const float scale = __shfl(inv, h & 15, 64);
+      if (h >= live || c >= d) continue;
+      f32x4_t o = *reinterpret_cast<const f32x4_t *>(&red[0][h][c]);
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) o += red[w][h][c];
-        if (whole)
-          reinterpret_cast<E *>(a.out.p + s * a.out.row + (head0 + h) * a.out.head)[c] =
-              (E)(total == 0.f ? 0.f : o * inv);
-        else
-          p.partial[(slot + h) * d + c] = o;
+      for (int w = 1; w < kWaves; ++w) o += *reinterpret_cast<const f32x4_t *>(&red[w][h][c]);
+      if (whole) {
+        typedef E out_t __attribute__((ext_vector_type(4)));
+        out_t r;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = (E)(scale == 0.f ? 0.f : o[e] * scale);
+        *reinterpret_cast<out_t *>(a.out.p + s * a.out.row + (head0 + h) * a.out.head + c * es) = r;
+      } else {
+        *reinterpret_cast<f32x4_t *>(p.partial + (slot + h) * d + c) = o;
       }
     }
     if (last) return;
