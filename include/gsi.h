@@ -505,7 +505,7 @@ size_t gsi_cache_attend_workspace(const gsi_cache *cache, const gsi_table *table
  * are -inf) gives zeros, and lse -inf.  What lies behind the n slots is never
  * part of a result, whatever it holds.  Needs `ws` of at least
  * gsi_cache_attend_workspace() bytes, 16-byte aligned.
- * S (most * page / 64 + 1) below 2^31. */
+ * S (most * page / 32 + 3) below 2^31. */
 gsi_status gsi_cache_attend(const gsi_cache *cache, const gsi_table *table, const int32_t *lengths,
                             const gsi_heads *q, const gsi_heads *out, float scale, int32_t window,
                             int32_t accumulate, float *lse, void *ws, size_t ws_bytes,

@@ -5,8 +5,8 @@
 //                   units, four steps of 32 slots (bf16; 16 in fp32), one for each
 //                   wavefront of a workgroup.  All rows' units, one after the
 //                   other, are dealt to as many workgroups as the chip holds at
-//                   once in equal shares, from the lengths as they are: no
-//                   workgroup is idle however the lengths differ.  A workgroup
+//                   once in shares of equal cost, from the lengths as they are:
+//                   no workgroup is idle however the lengths differ.  A workgroup
 //                   takes up to 16 query heads of its rows (a tile); where a key
 //                   head has more, a share has a workgroup for each tile.  A step's keys and values are read once,
 //                   straight into the registers that the matrix instructions
@@ -149,17 +149,61 @@ __device__ __forceinline__ int64_t over(int64_t n, int64_t by) {
          (int64_t)__builtin_amdgcn_readfirstlane((int)(q >> 32)) << 32;
 }
 
-// Shares of `all` units: share b begins at unit b all / shares.
-struct Shares {
-  int64_t all;
-  int of;
-  __device__ __forceinline__ int64_t begin(int b) const { return over(b * all, of); }
-  __device__ __forceinline__ int owner(int64_t unit) const { return (int)over((unit + 1) * of - 1, all); }
+// Where a unit is: a row of a sequence and the row's units before it.
+struct Place {
+  int s, kh, skip;
+  __device__ __forceinline__ bool in_row_of(const Place &o) const { return s == o.s && kh == o.kh; }
 };
-__device__ __forceinline__ Shares shares_of(const AttendArgs &a, const Plan &p, int units) {
-  const int64_t all = (int64_t)units * a.c.heads;
-  return {all, (int)min((int64_t)p.shares, all)};
-}
+
+// The shares of all rows' units.  A unit costs two and a row one, what its first
+// loads and its join take (64 ragged sequences of 40 heads, 6 rows of a share in
+// the mean: 158 us by units alone, where the shares of many short rows end last,
+// CCC us so); share b begins with the first unit at or behind b all / of of the
+// cost.  Units are at most three apart: a share is not empty where it has as much;
+// where that is not so, units alone are the cost.
+template <typename Count>
+struct Shares {
+  const AttendArgs &a;
+  const Counted<Count> &counted;
+  int of, unit;  // shares, and a unit's cost
+  int64_t all;
+
+  __device__ __forceinline__ Shares(const AttendArgs &args, const Plan &p, const Counted<Count> &c)
+      : a(args), counted(c), unit(2) {
+    all = (int64_t)cost(c.sum, a.c.S) * a.c.heads;
+    if (all < 3 * (int64_t)p.shares) {
+      unit = 1;
+      all = (int64_t)c.sum * a.c.heads;
+    }
+    of = (int)min((int64_t)p.shares, all);
+  }
+  // of a key head's units in so many rows
+  __device__ __forceinline__ int cost(int units, int rows) const { return unit * units + (unit - 1) * rows; }
+  __device__ __forceinline__ int64_t start_of(const Sequence &q, int kh, int units) const {
+    return (int64_t)cost(q.before, q.s) * a.c.heads + (int64_t)cost(units, 1) * kh;
+  }
+  __device__ __forceinline__ int owner(int64_t at) const { return (int)over((at + 1) * of - 1, all); }
+  // `q` is the place's sequence, unless share b is one behind the last
+  __device__ __forceinline__ Place begin(int b, Sequence *q) const {
+    if (b == of) return {a.c.S, 0, 0};
+    const int64_t at = over(b * all, of);
+    const int v = (int)over(at, a.c.heads);
+    *q = counted.search([&](int s, int to) { return cost(to, s + 1) > v; });
+    const int units = counted.count(q->n), row = cost(units, 1);
+    const int64_t in = at - (int64_t)cost(q->before, q->s) * a.c.heads;
+    Place r{q->s, (int)over(in, row), 0};
+    r.skip = (int)(in - (int64_t)r.kh * row + unit - 1) >> (unit - 1);
+    if (r.skip >= units) {
+      r.skip = 0;
+      if (++r.kh == a.c.heads) {
+        r.kh = 0;
+        *q = {q->s + 1, q->s + 1 < a.c.S ? clamped_length(a.c, a.lengths, q->s + 1) : 0, q->before + units};
+        r.s = q->s;
+      }
+    }
+    return r;
+  }
+};
 
 // The largest (the sum) of a value over the four lanes l % 16 + 16 k.
 __device__ __forceinline__ float quads_max(float v) {
@@ -211,36 +255,30 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
   const int quad = lane >> 4, l16 = lane & 15, d = a.c.d;
   // eight shares' first tiles, their second ones ..: workgroups go to the XCDs in turn
   const int eight = blockIdx.x / 8, tile = p.tiles == 1 ? 0 : eight % p.tiles;
-  const int share = eight / p.tiles * 8 + blockIdx.x % 8, rows = a.c.heads;  // of a sequence
+  const int share = eight / p.tiles * 8 + blockIdx.x % 8;
   const auto units_of = [&](int n) { return span_of<E>(a, n).units; };
   const Counted counted(a, units_of);
-  const Shares sh = shares_of(a, p, counted.sum);
+  const Shares sh(a, p, counted);
   if (share >= sh.of) return;
-  int64_t left = sh.begin(share + 1);  // units of the share behind the present segment
 
   // A row's part in this share: its units from `skip` on, `mine` of them, and of
   // this wavefront the steps st, st + kWaves, .. below end.
-  struct Segment {
-    int s, kh, skip, mine, st, end;
+  struct Segment : Place {
+    int mine, st, end;
     Span sp;
   };
+  Segment seg;
+  Place behind{-1, 0, 0};  // the first unit of the next share
   const auto place = [&](Segment &g) {
-    g.mine = (int)min((int64_t)(g.sp.units - g.skip), left);
+    g.mine = (g.in_row_of(behind) ? behind.skip : g.sp.units) - g.skip;
     g.st = g.sp.lo + g.skip * kWaves + wave;
     g.end = g.sp.lo + min(g.sp.steps, (g.skip + g.mine) * kWaves);
-    left -= g.mine;
   };
-  Segment seg;
   {
-    const int64_t unit = sh.begin(share);
-    const Sequence at = counted.of_thing((int)over(unit, rows));
-    const int64_t in_rows = unit - (int64_t)at.before * rows;
-    seg.s = at.s;
-    seg.sp = span_of<E>(a, at.n);
-    seg.kh = (int)over(in_rows, seg.sp.units);
-    seg.skip = (int)(in_rows - (int64_t)seg.kh * seg.sp.units);
-    left -= unit;
-    place(seg);
+    Sequence at;
+    static_cast<Place &>(seg) = sh.begin(share, &at);
+    seg.sp = span_of<E>(a, __builtin_amdgcn_readfirstlane(at.n));
+    place(seg);  // as if it ended its row
   }
 
   // A lane's keys (and its values) of a step lie in one block of 8 slots, so in one
@@ -321,18 +359,21 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
     load_k(seg, now, seg.st);
     load_v(seg, now, seg.st);
   }
+  {
+    Sequence at;
+    behind = sh.begin(share + 1, &at);  // while they are under way
+    place(seg);
+  }
   for (;;) {
     // The next segment, whose first loads go out as this one's last are used: while
     // the wavefronts are joined nothing has to be waited for.
-    const bool last = left == 0;
     Segment then = seg;
     Where then_now{}, then_next{};
-    if (!last) {  // then this segment ends its row
-      if (++then.kh == rows) {
-        then.kh = 0;
-        then.sp = span_of<E>(a, __builtin_amdgcn_readfirstlane(clamped_length(a.c, a.lengths, ++then.s)));
-      }
-      then.skip = 0;
+    if (++then.kh == a.c.heads) then.kh = 0, ++then.s;
+    then.skip = 0;
+    const bool last = seg.in_row_of(behind) || (behind.skip == 0 && then.in_row_of(behind));
+    if (!last) {
+      if (then.kh == 0) then.sp = span_of<E>(a, __builtin_amdgcn_readfirstlane(clamped_length(a.c, a.lengths, then.s)));
       place(then);
       if (then.st < then.end) {
         then_now = pages_of(then, then.st);
@@ -543,24 +584,24 @@ template <typename E>
 __global__ void __launch_bounds__(kThreads) join_kernel(AttendArgs a, Plan p, bool cuts, int sets) {
   __shared__ __attribute__((aligned(16))) float red[kThreads * 4];
   __shared__ float red_m[kThreads], red_l[kThreads];
-  const int tid = threadIdx.x, d = a.c.d, rows = a.c.heads;
+  const int tid = threadIdx.x, d = a.c.d;
   const auto units_of = [&](int n) { return span_of<E>(a, n).units; };
   const Counted counted(a, units_of);
-  const Shares sh = shares_of(a, p, counted.sum);
+  const Shares sh(a, p, counted);
   int64_t start;
   int s, first, units, kh, tile, in_tile, live;
   if (cuts) {
     const int set = blockIdx.x % sets, most = heads_at_once(d), share = blockIdx.x / sets % (p.shares - 1) + 1;
     tile = blockIdx.x / sets / (p.shares - 1);
     if (share >= sh.of) return;
-    const int64_t cut = sh.begin(share);
-    const Sequence at = counted.of_thing((int)over(cut, rows));
-    s = at.s;
+    Sequence at;
+    const Place cut = sh.begin(share, &at);
+    if (cut.skip == 0) return;
+    s = at.s, kh = cut.kh;
     units = units_of(at.n);
-    kh = (int)over(cut - (int64_t)at.before * rows, units);
-    start = (int64_t)at.before * rows + (int64_t)kh * units;
+    start = sh.start_of(at, kh, units);
     first = sh.owner(start);
-    if (cut == start || share != first + 1) return;
+    if (share != first + 1) return;
     in_tile = set * most;
     live = min(min(16, a.group - tile * 16) - in_tile, most);
     if (live <= 0) return;
@@ -570,10 +611,10 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttendArgs a, Plan p, bo
     kh = h / a.group, tile = (h - kh * a.group) / 16, in_tile = (h - kh * a.group) % 16, live = 1;
     const Sequence at = counted.number(s);
     units = units_of(at.n);
-    start = (int64_t)at.before * rows + (int64_t)kh * units;
+    start = sh.start_of(at, kh, units);
     first = sh.owner(start);
   }
-  const int pieces = sh.owner(start + units - 1) - first + 1;
+  const int pieces = sh.owner(start + (int64_t)sh.unit * (units - 1)) - first + 1;
   if (pieces <= 1) return;
   const int head0 = kh * a.group + tile * 16 + in_tile;
   // `sides` threads share four columns of a head, each takes every sides-th piece
@@ -730,8 +771,9 @@ Plan plan_of(const Pool &c, int q_heads, bool accumulate, uint8_t *ws, size_t *b
 template <typename E>
 gsi_status launch_as(const AttendArgs &a, hipStream_t st) {
   const Plan p = plan_of<E>(a.c, a.q.n, a.accumulate, a.ws, nullptr);
-  // units of all sequences, a unit each at least, are counted in 32 bits
-  if ((((int64_t)a.c.most << a.c.shift) / 64 + 1) * a.c.S > INT32_MAX) return GSI_E_SHAPE;
+  // units of 64 slots or more, one of a sequence at least, cost two, and a row one:
+  // that of a key head is counted in 32 bits
+  if ((((int64_t)a.c.most << a.c.shift) / 32 + 3) * a.c.S > INT32_MAX) return GSI_E_SHAPE;
   const unsigned grid = (p.shares + 7) / 8 * 8 * p.tiles;
   const auto go = [&](auto ks) {
     attend_kernel<E, decltype(ks)::value><<<grid, kThreads, 0, st>>>(a, p);
