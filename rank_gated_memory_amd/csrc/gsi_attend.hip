@@ -140,25 +140,34 @@ struct Counted {
   }
 };
 
-// A quotient of wave-uniform numbers, in 32 bits where they are: a division of
-// 64 bits takes a good part of a microsecond.
+// A quotient of wave-uniform numbers below 2^62, in 32 bits where they are; where
+// not, bit by bit: the compiler's own steps for 64 bits are long, and code that is
+// jumped over is waited for too.
 __device__ __forceinline__ int64_t over(int64_t n, int64_t by) {
-  const int64_t q = (uint64_t)(n | by) >> 32 ? n / by : (int64_t)((uint32_t)n / (uint32_t)by);
-  // a division's steps are vector instructions: back to scalar registers
-  return (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)q) |
-         (int64_t)__builtin_amdgcn_readfirstlane((int)(q >> 32)) << 32;
+  if (__builtin_expect((uint64_t)(n | by) >> 32 == 0, 1))
+    // a division's steps are vector instructions: back to scalar registers
+    return (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)n / (uint32_t)by));
+  int64_t q = 0, rest = 0;
+#pragma unroll 1
+  for (int k = 61; k >= 0; --k) {
+    rest = rest * 2 + (n >> k & 1);
+    const bool in = rest >= by;
+    rest -= in ? by : 0;
+    q = q * 2 + in;
+  }
+  return q;
 }
 
-// Where a unit is: a row of a sequence and the row's units before it.
+// Where a unit is: a row of a sequence, its length, and the row's units before it.
 struct Place {
-  int s, kh, skip;
-  __device__ __forceinline__ bool in_row_of(const Place &o) const { return s == o.s && kh == o.kh; }
+  int s, kh, n, skip;
+  int64_t at;  // the cost before it
 };
 
 // The shares of all rows' units.  A unit costs two and a row one, what its first
 // loads and its join take (64 ragged sequences of 40 heads, 6 rows of a share in
 // the mean: 158 us by units alone, where the shares of many short rows end last,
-// CCC us so); share b begins with the first unit at or behind b all / of of the
+// 145 so); share b begins with the first unit at or behind b all / of of the
 // cost.  Units are at most three apart: a share is not empty where it has as much;
 // where that is not so, units alone are the cost.
 template <typename Count>
@@ -183,22 +192,24 @@ struct Shares {
     return (int64_t)cost(q.before, q.s) * a.c.heads + (int64_t)cost(units, 1) * kh;
   }
   __device__ __forceinline__ int owner(int64_t at) const { return (int)over((at + 1) * of - 1, all); }
-  // `q` is the place's sequence, unless share b is one behind the last
-  __device__ __forceinline__ Place begin(int b, Sequence *q) const {
-    if (b == of) return {a.c.S, 0, 0};
-    const int64_t at = over(b * all, of);
+  __device__ __forceinline__ int64_t part(int b) const { return over(b * all, of); }
+  __device__ __forceinline__ Place begin(int b) const {
+    const int64_t at = part(b);
     const int v = (int)over(at, a.c.heads);
-    *q = counted.search([&](int s, int to) { return cost(to, s + 1) > v; });
-    const int units = counted.count(q->n), row = cost(units, 1);
-    const int64_t in = at - (int64_t)cost(q->before, q->s) * a.c.heads;
-    Place r{q->s, (int)over(in, row), 0};
-    r.skip = (int)(in - (int64_t)r.kh * row + unit - 1) >> (unit - 1);
-    if (r.skip >= units) {
+    const Sequence q = counted.search([&](int s, int to) { return cost(to, s + 1) > v; });
+    const int units = counted.count(q.n), row = cost(units, 1);
+    const int64_t in = at - (int64_t)cost(q.before, q.s) * a.c.heads;
+    Place r{q.s, (int)over(in, row), q.n, 0, at};
+    const int off = (int)(in - (int64_t)r.kh * row);
+    r.skip = (off + unit - 1) >> (unit - 1);
+    if (r.skip < units) {
+      r.at += unit * r.skip - off;
+    } else {  // the next row
+      r.at += row - off;
       r.skip = 0;
       if (++r.kh == a.c.heads) {
         r.kh = 0;
-        *q = {q->s + 1, q->s + 1 < a.c.S ? clamped_length(a.c, a.lengths, q->s + 1) : 0, q->before + units};
-        r.s = q->s;
+        r.n = clamped_length(a.c, a.lengths, ++r.s);
       }
     }
     return r;
@@ -263,22 +274,24 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
 
   // A row's part in this share: its units from `skip` on, `mine` of them, and of
   // this wavefront the steps st, st + kWaves, .. below end.
-  struct Segment : Place {
-    int mine, st, end;
+  struct Segment {
+    int s, kh, skip, mine, st, end;
     Span sp;
   };
-  Segment seg;
-  Place behind{-1, 0, 0};  // the first unit of the next share
+  int64_t left;  // cost of the share behind the present segment
   const auto place = [&](Segment &g) {
-    g.mine = (g.in_row_of(behind) ? behind.skip : g.sp.units) - g.skip;
+    g.mine = (int)min((int64_t)(g.sp.units - g.skip), (left + sh.unit - 1) >> (sh.unit - 1));
     g.st = g.sp.lo + g.skip * kWaves + wave;
     g.end = g.sp.lo + min(g.sp.steps, (g.skip + g.mine) * kWaves);
+    left -= sh.unit * g.mine + (g.skip + g.mine == g.sp.units ? sh.unit - 1 : 0);
   };
+  Segment seg;
   {
-    Sequence at;
-    static_cast<Place &>(seg) = sh.begin(share, &at);
+    const Place at = sh.begin(share);
+    seg.s = at.s, seg.kh = at.kh, seg.skip = at.skip;
     seg.sp = span_of<E>(a, __builtin_amdgcn_readfirstlane(at.n));
-    place(seg);  // as if it ended its row
+    left = sh.part(share + 1) - at.at;
+    place(seg);
   }
 
   // A lane's keys (and its values) of a step lie in one block of 8 slots, so in one
@@ -359,21 +372,18 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
     load_k(seg, now, seg.st);
     load_v(seg, now, seg.st);
   }
-  {
-    Sequence at;
-    behind = sh.begin(share + 1, &at);  // while they are under way
-    place(seg);
-  }
   for (;;) {
     // The next segment, whose first loads go out as this one's last are used: while
     // the wavefronts are joined nothing has to be waited for.
+    const bool last = left <= 0;
     Segment then = seg;
     Where then_now{}, then_next{};
-    if (++then.kh == a.c.heads) then.kh = 0, ++then.s;
-    then.skip = 0;
-    const bool last = seg.in_row_of(behind) || (behind.skip == 0 && then.in_row_of(behind));
-    if (!last) {
-      if (then.kh == 0) then.sp = span_of<E>(a, __builtin_amdgcn_readfirstlane(clamped_length(a.c, a.lengths, then.s)));
+    if (!last) {  // then this segment ends its row
+      if (++then.kh == a.c.heads) {
+        then.kh = 0;
+        then.sp = span_of<E>(a, __builtin_amdgcn_readfirstlane(clamped_length(a.c, a.lengths, ++then.s)));
+      }
+      then.skip = 0;
       place(then);
       if (then.st < then.end) {
         then_now = pages_of(then, then.st);
@@ -594,12 +604,11 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttendArgs a, Plan p, bo
     const int set = blockIdx.x % sets, most = heads_at_once(d), share = blockIdx.x / sets % (p.shares - 1) + 1;
     tile = blockIdx.x / sets / (p.shares - 1);
     if (share >= sh.of) return;
-    Sequence at;
-    const Place cut = sh.begin(share, &at);
+    const Place cut = sh.begin(share);
     if (cut.skip == 0) return;
-    s = at.s, kh = cut.kh;
-    units = units_of(at.n);
-    start = sh.start_of(at, kh, units);
+    s = cut.s, kh = cut.kh;
+    units = units_of(cut.n);
+    start = cut.at - sh.unit * cut.skip;
     first = sh.owner(start);
     if (share != first + 1) return;
     in_tile = set * most;
