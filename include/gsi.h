@@ -499,8 +499,8 @@ size_t gsi_cache_attend_workspace(const gsi_cache *cache, const gsi_table *table
  *   q, out     : S rows of q->n heads, q->n a multiple of cache->heads
  *   lse        : [S][q->n] fp32, or NULL
  *   accumulate : not 0: mass of every slot in [first, n) += the sum of its
- *                weights over the query heads of its key head; sequences then
- *                share no page
+ *                weights over the query heads of its key head; no page is then
+ *                named twice for slots in use, by one sequence or two
  * A sequence without slots (or with no page that there is, or whose scores all
  * are -inf) gives zeros, and lse -inf.  What lies behind the n slots is never
  * part of a result, whatever it holds.  Needs `ws` of at least
@@ -515,12 +515,14 @@ gsi_status gsi_cache_attend(const gsi_cache *cache, const gsi_table *table, cons
  * head by itself: the `recent` entries of the largest age (without ages: of the
  * highest slots) stay, and of the others those of the largest mass; ties go to
  * the lowest slot, a mass that is NaN and an entry of no page count as the
- * least (nothing is moved for one that stays all the same).  Entries in slots below the budget stay where they are; the others
- * that stay fill, in the order of their slots, the slots below the budget that
- * were given up.  (Attention does not go by the order of slots.)
+ * least (nothing is moved for one that stays all the same).  Entries in slots
+ * below the budget stay where they are; the others that stay fill, in the order
+ * of their slots, the slots below the budget that were given up.  (Attention does
+ * not go by the order of slots.)
  *   budget, recent : 1 <= budget <= 2^20, 0 <= recent <= budget
  *   to          : NULL to move entries in place (only those that change slots;
- *                 sequences then share no page), or the table of the S
+ *                 no page is then named twice for slots in use, by one
+ *                 sequence or two), or the table of the S
  *                 sequences in other pages of the same pool, into which all
  *                 that stay are copied, from sequences of any length; none of
  *                 its pages is a page of `table` or is named twice;

@@ -33,7 +33,7 @@
 // of 2000 slots, 8 key heads for 256, 524 MB, 119 us; with tiles as further rows 190,
 // 16 query heads for each key head 100.  Bound by HBM where the lengths fill the chip: two sequences of
 // 131071 slots, 8 heads of 128, 537 MB in 100 us, 5.4 TB/s; 64 of 1 to 4096 slots, 40
-// heads of 128, 700 MB in 160 us with the scores kept, 4.4.  One sequence of 1777
+// heads of 128, 700 MB in 143 us with the scores kept, 4.9.  One sequence of 1777
 // slots of 16 heads of 256, 29 MB, takes 12 us and 4 for the join, a page number's,
 // the keys' and the values' latency after the launch's.  (Two tiles in one pass were no faster: 64 sequences of 2000
 // slots, one key head for 32: 38 us in two rows and 39 in one; one of 65536: 25
