@@ -11,13 +11,11 @@
 // it.  The threshold comes eight bits at a time: entries that agree with it so
 // far are counted by their next eight bits in LDS.  A lane holds the keys of four
 // slots one after the other, which lie in one page, so that a load of 16 bytes
-// reads them; up to 32768 slots are read once.  A call for a few thousand slots
-// is bound by the latency of these reads and of the dozen barriers behind them
-// (2049 slots, 128 workgroups: 12 us), one for long sequences by the counting in
-// LDS of one CU each (30011 slots, 24 workgroups: 44 us; the masses' first pass 6
-// of them, 10 in one copy of the bins).
+// reads them; up to 32768 slots stay in registers and are read once.  A call for
+// a few thousand slots is bound by the latency of these reads and of the dozen
+// barriers behind them (2049 slots, 128 workgroups: 12 us), one for long sequences by
+// the counting in LDS of one CU each (30011 slots, 24 workgroups: 44 us).
 #include <algorithm>
-#include <type_traits>
 #include <utility>
 
 #include "gsi_cache.h"
@@ -43,19 +41,11 @@ struct Four {
   uint32_t v[4];
 };
 
-constexpr int kBins = 256;
-// Copies of the bins that lanes count in in turn, where many slots fall into few
-// bins: of one address LDS does one addition after the other.
-template <int NB>
-constexpr int kCopies = NB > 0 ? 1 : 4;
-
 // LDS of a workgroup.
 struct Shared {
-  // Passes use them in turn; a pass clears the next one's, which the wavefronts
-  // have last read two barriers ago.  Copies on different banks.
-  int hist[3][4][kBins + 16];
+  int hist[2][4][256];  // of the two selections' passes, zero at first
   uint32_t all[kWaves], any[kWaves];
-  int part[kWaves], low;
+  int part[kWaves];
   int2 moves[kFewMoves];
 };
 
@@ -83,15 +73,13 @@ __device__ __forceinline__ uint64_t below(int lane) { return (1ull << lane) - 1;
 
 // The slots of a workgroup in blocks of 256: slot 256 b + 4 lane + e of a block,
 // blocks dealt to the wavefronts in turn.  NB blocks at most of a wavefront, with
-// their keys in registers; kInLds: up to kLdsBlocks, keys in LDS; 0: any number,
-// keys are read again each time.
+// their keys in registers; 0: any number, keys are read again each time.
 constexpr int kBlock = 256;
-constexpr int kInLds = -1, kLdsBlocks = 8;
 template <int NB>
 struct Slots {
   int n, lane, wave;
-  uint64_t *keep;     // [block][e]: a bit per lane, for NB 0
-  uint32_t kept = 0;  // else: bit 4 k + e
+  uint64_t *keep;     // [block][e]: a bit per lane (for NB > 0 written at the end)
+  uint32_t kept = 0;  // NB > 0: bit 4 k + e
 
   // f(k, b) for each of the wavefront's blocks; k is a constant, or the arrays
   // that it indexes would not stay in registers
@@ -99,8 +87,6 @@ struct Slots {
   __device__ __forceinline__ void each(const F &f) const {
     if constexpr (NB > 0)
       unrolled(f, std::make_integer_sequence<int, NB>());
-    else if constexpr (NB < 0)
-      for (int k = 0; (wave + kWaves * k) * kBlock < n; ++k) f(k, wave + kWaves * k);
     else
       for (int b = wave; b * kBlock < n; b += kWaves) f(std::integral_constant<int, 0>{}, b);
   }
@@ -111,7 +97,7 @@ struct Slots {
   // bit e: slot e of this lane is there and not kept yet
   __device__ __forceinline__ uint32_t is_free(int k, int b) const {
     uint32_t mine;
-    if constexpr (NB != 0) {
+    if constexpr (NB > 0) {
       mine = kept >> (4 * k);
     } else {
       mine = 0;
@@ -122,7 +108,7 @@ struct Slots {
     return ~mine & (left >= 4 ? 15u : left <= 0 ? 0u : (1u << left) - 1);
   }
   __device__ __forceinline__ void take(int k, int b, uint32_t mine) {  // every lane of the wavefront
-    if constexpr (NB != 0) {
+    if constexpr (NB > 0) {
       kept |= mine << (4 * k);
     } else {
 #pragma unroll
@@ -136,10 +122,10 @@ struct Slots {
 
 // Keeps the `count` free slots of the largest key, ties to the lowest slot;
 // there are at least `count`.  keys(k, b): this lane's four keys; Common: they may
-// agree in their upper bits, as ages do; turn: the next pass's bins, zero; counts:
+// agree in their upper bits, as ages do; hists: the selection's bins, zero; counts:
 // LDS for a number per block.
 template <bool Common, int NB, typename Keys>
-__device__ __forceinline__ void take_largest(Slots<NB> &sl, int count, const Keys &keys, int *turn, int *counts,
+__device__ __forceinline__ void take_largest(Slots<NB> &sl, int count, const Keys &keys, int (*hists)[256], int *counts,
                                              Shared &sh) {
   const int lane = sl.lane;
   int shift = 32, need = count;
@@ -167,35 +153,27 @@ __device__ __forceinline__ void take_largest(Slots<NB> &sl, int count, const Key
     if (shift < 32) span = (1u << shift) - 1, base = all & ~span;
   }
   bool tied = true;  // more slots at the threshold than are taken
-  while (shift > 0 && tied) {
+  for (int pass = 0; shift > 0 && tied; ++pass) {
     const int low = max(shift - 8, 0);
-    int *const hists = sh.hist[*turn][0], *const hist = sh.hist[*turn][lane % kCopies<NB>];
-    *turn = *turn == 2 ? 0 : *turn + 1;
-    for (int k = threadIdx.x; k < kCopies<NB> * (kBins + 16); k += kThreads) sh.hist[*turn][0][k] = 0;
+    int *const hist = hists[pass];
     sl.each([&](auto k, int b) {
       const uint32_t is_free = sl.is_free(k, b);
       const Four key = keys(k, b);
+      // Neighbours often agree in these bits (ages are slots at first), and lanes
+      // at one bin take their turns: a lane's run of one bin is counted at once,
+      // and of the lanes' last runs those of the first lane's bin.
       uint32_t among = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) among |= (uint32_t)(key.v[e] - base <= span) << e;
       among &= is_free;
       if (__ballot(among != 0) == 0) return;  // few are left after a pass or two
-      if constexpr (!Common) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (among >> e & 1) atomicAdd(&hist[(key.v[e] - base) >> low], 1);  // integers: any order
-        return;
-      }
-      // Neighbours often agree in these bits (ages are slots at first), and lanes
-      // at one bin take their turns: a lane's run of one bin is counted at once,
-      // and of the lanes' last runs those of the first lane's bin.
       int bin = 0, c = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint32_t off = key.v[e] - base;
         const bool in = among >> e & 1;
         if (in && c > 0 && (int)(off >> low) != bin) {
-          atomicAdd(&hist[bin], c);
+          atomicAdd(&hist[bin], c);  // integers: any order
           c = 0;
         }
         bin = in ? off >> low : bin;
@@ -215,16 +193,11 @@ __device__ __forceinline__ void take_largest(Slots<NB> &sl, int count, const Key
     __syncthreads();
     // from the top, four bins a lane: the bin where the running count reaches
     // `need`; every wavefront by itself
-    int4 h = *reinterpret_cast<const int4 *>(hists + kBins - 4 - 4 * lane);
-#pragma unroll
-    for (int k = 1; k < kCopies<NB>; ++k) {
-      const int4 more = *reinterpret_cast<const int4 *>(hists + k * (kBins + 16) + kBins - 4 - 4 * lane);
-      h.x += more.x, h.y += more.y, h.z += more.z, h.w += more.w;
-    }
+    const int4 h = *reinterpret_cast<const int4 *>(hist + 252 - 4 * lane);
     const int sum = h.x + h.y + h.z + h.w;
     const int incl = sums_to(sum);
     const int at = __ffsll((unsigned long long)__ballot(incl >= need)) - 1;
-    int above = __builtin_amdgcn_readlane(incl - sum, at), bin = kBins - 1 - 4 * at;
+    int above = __builtin_amdgcn_readlane(incl - sum, at), bin = 255 - 4 * at;
     int c = __builtin_amdgcn_readlane(h.w, at);
     if (above + c < need) {
       above += c, --bin, c = __builtin_amdgcn_readlane(h.z, at);
@@ -295,8 +268,8 @@ __device__ __forceinline__ void move_numbers(const EvictArgs &a, int64_t from, i
   if (a.c.age) a.c.age[to] = a.c.age[from];
 }
 
-// blocks: for which there is LDS; holes: for which there is, a multiple of four;
-// pieces: of 16 bytes of a key.
+// blocks: for which there is LDS; holes: for which there is; pieces: of 16 bytes
+// of a key.
 template <int NB>
 __global__ void __launch_bounds__(kThreads) select_kernel(EvictArgs a, int blocks, int holes, int pieces) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -310,8 +283,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(EvictArgs a, int block
     return;
   }
   const int nb = (n + kBlock - 1) / kBlock;
-  int *const count = reinterpret_cast<int *>(lds + (NB == 0 ? 32 * blocks : 0)), *const list = count + blocks;
-  Four *const held = reinterpret_cast<Four *>(list + holes);  // [block][lane], for kInLds
+  int *const count = reinterpret_cast<int *>(lds + 32 * blocks);
   Slots<NB> sl{n, tid & 63, tid >> 6, reinterpret_cast<uint64_t *>(lds)};
   const bool by_age = a.c.age && a.recent > 0, by_mass = budget > a.recent;
   // This lane's four slots of a block: one page.  What lies behind the last slot
@@ -337,8 +309,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(EvictArgs a, int block
     for (int e = 0; e < 4; ++e) r.v[e] = is_page(p) ? age_key((int32_t)r.v[e]) : 0;
     return r;
   };
-  int turn = 0;
-  for (int k = tid; k < kCopies<NB> * (kBins + 16); k += kThreads) sh.hist[0][0][k] = 0;
+  for (int k = tid; k < 2 * 4 * 256; k += kThreads) (&sh.hist[0][0][0])[k] = 0;
   int p[NB > 0 ? NB : 1];
   Four age[NB > 0 ? NB : 1], mass[NB > 0 ? NB : 1];
   if constexpr (NB > 0) {  // all reads of both selections at once
@@ -346,27 +317,16 @@ __global__ void __launch_bounds__(kThreads) select_kernel(EvictArgs a, int block
     if (by_age) sl.each([&](auto k, int b) { age[k] = read(a.c.age, p[k], b); });
     if (by_mass) sl.each([&](auto k, int b) { mass[k] = read(a.c.mass, p[k], b); });
     if (by_age) sl.each([&](auto k, int) { age[k] = age_keys(p[k], age[k]); });
-  } else if constexpr (NB == 0) {
+  } else {
     for (int k = tid; k < 4 * nb; k += kThreads) sl.keep[k] = 0;
-  }
-  // all reads of both selections at once
-  const Slots<kLdsBlocks> lasting{n, sl.lane, sl.wave, nullptr};
-  int lp[NB < 0 ? kLdsBlocks : 1];
-  Four later[NB < 0 ? kLdsBlocks : 1];
-  if constexpr (NB < 0) {
-    lasting.each([&](auto k, int b) { lp[k] = raw_page(b); });
-    if (by_age)
-      lasting.each([&](auto k, int b) { held[64 * b + sl.lane] = age_keys(lp[k], read(a.c.age, lp[k], b)); });
-    if (by_mass) lasting.each([&](auto k, int b) { later[k] = read(a.c.mass, lp[k], b); });
   }
   __syncthreads();
   if (by_age) {
     take_largest<true>(sl, a.recent, [&](auto k, int b) {
       if constexpr (NB > 0) return age[k];
-      if constexpr (NB < 0) return held[64 * b + sl.lane];
       const int page = raw_page(b);
       return age_keys(page, read(a.c.age, page, b));
-    }, &turn, count, sh);
+    }, sh.hist[0], count, sh);
   } else if (a.recent > 0) {
     sl.each([&](auto k, int b) {
       const int before = n - a.recent - (b * kBlock + 4 * sl.lane);  // slots of this lane before the newest
@@ -376,68 +336,54 @@ __global__ void __launch_bounds__(kThreads) select_kernel(EvictArgs a, int block
   }
   if (by_mass) {
     if constexpr (NB > 0) sl.each([&](auto k, int) { mass[k] = mass_keys(p[k], mass[k]); });
-    if constexpr (NB < 0)  // each wavefront its own
-      lasting.each([&](auto k, int b) { held[64 * b + sl.lane] = mass_keys(lp[k], later[k]); });
     take_largest<false>(sl, budget - a.recent, [&](auto k, int b) {
       if constexpr (NB > 0) return mass[k];
-      if constexpr (NB < 0) return held[64 * b + sl.lane];
       const int page = raw_page(b);
       return mass_keys(page, read(a.c.mass, page, b));
-    }, &turn, count, sh);
+    }, sh.hist[1], count, sh);
   }
-  // kept slots before each block, and of a block's before each lane's
-  int before[NB > 0 ? NB : 1];
+  // kept slots before each block
   sl.each([&](auto k, int b) {
-    int c = 0, lower = 0;
+    int c = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint64_t m = NB != 0 ? __ballot(sl.kept >> (4 * k + e) & 1) : sl.keep[4 * b + e];
+      uint64_t m;
+      if constexpr (NB > 0) {
+        m = __ballot(sl.kept >> (4 * k + e) & 1);
+        if (sl.lane == 0) sl.keep[4 * b + e] = m;
+      } else {
+        m = sl.keep[4 * b + e];
+      }
       c += __popcll(m);
-      lower += __popcll(m & below(sl.lane));
     }
-    if constexpr (NB > 0) before[k] = lower;
     if (sl.lane == 0) count[b] = c;
   });
   sums_before(count, nb, sh);
-  // of this lane's four slots, the kept ones and how many are kept before them
-  const auto kept_of = [&](auto k, int b, uint32_t *kept) {
+  // of a lane's four slots, the kept ones and how many are kept before them
+  const auto kept_of = [&](int b, int lane, uint32_t *kept) {
     int c = count[b];
-    if constexpr (NB != 0) {
-      *kept = sl.kept >> (4 * k) & 15;
-      if constexpr (NB > 0) {
-        c += before[k];
-      } else {
+    *kept = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) c += __popcll(__ballot(*kept >> e & 1) & below(sl.lane));
-      }
-    } else {
-      *kept = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint64_t w = sl.keep[4 * b + e];
-        c += __popcll(w & below(sl.lane));
-        *kept |= (uint32_t)(w >> sl.lane & 1) << e;
-      }
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t w = sl.keep[4 * b + e];
+      c += __popcll(w & below(lane));
+      *kept |= (uint32_t)(w >> lane & 1) << e;
     }
     return c;
   };
-  sl.each([&](auto k, int b) {  // kept below the budget; budget < n
-    if (b != budget / kBlock) return;
-    uint32_t kept;
-    const int c = kept_of(k, b, &kept);
-    if (sl.lane == budget / 4 % 64) sh.low = c + __popc(kept & ((1u << (budget & 3)) - 1));
-  });
-  __syncthreads();
-  const int low = sh.low;
+  uint32_t kept;
+  int low = kept_of(budget / kBlock, budget / 4 % 64, &kept);  // kept below the budget; budget < n
+  low += __popc(kept & ((1u << (budget & 3)) - 1));
   const bool few = budget - low <= kFewMoves && !a.to;
   // The holes below the budget and the kept slots behind it, both in order, go
   // together: through a list of the holes in LDS, `holes` at a time.
+  int *const list = count + blocks;
   for (int first = 0; first == 0 || first < budget - low; first += holes) {
-    sl.each([&](auto k, int b) {
+    sl.each([&](auto, int b) {
       const int i0 = b * kBlock + 4 * sl.lane;
       if (b * kBlock >= budget) return;
       uint32_t mine;
-      int hole = i0 - kept_of(k, b, &mine) - first;
+      int hole = i0 - kept_of(b, sl.lane, &mine) - first;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (i0 + e >= budget) continue;
@@ -450,22 +396,21 @@ __global__ void __launch_bounds__(kThreads) select_kernel(EvictArgs a, int block
       }
     });
     __syncthreads();
-    sl.each([&](auto k, int b) {
+    sl.each([&](auto, int b) {
       if ((b + 1) * kBlock <= budget) return;
       const int i0 = b * kBlock + 4 * sl.lane;
       uint32_t mine;
-      int hole = kept_of(k, b, &mine) - low - first, to[4];
-      bool goes[4];
+      int rank = kept_of(b, sl.lane, &mine) - low;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        goes[e] = (mine >> e & 1) && i0 + e >= budget && hole >= 0 && hole < holes;
-        to[e] = list[goes[e] ? hole : 0];
-        if (few && goes[e]) sh.moves[hole] = make_int2(i0 + e, to[e]);  // few: first is 0
-        hole += mine >> e & 1;
+        if (!(mine >> e & 1)) continue;
+        const int hole = rank - first;
+        if (i0 + e >= budget && hole >= 0 && hole < holes) {
+          from[list[hole]] = i0 + e;
+          if (few) sh.moves[rank] = make_int2(i0 + e, list[hole]);
+        }
+        ++rank;
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (goes[e]) from[to[e]] = i0 + e;
     });
     __syncthreads();
   }
@@ -525,28 +470,23 @@ __global__ void __launch_bounds__(256) move_kernel(EvictArgs a, int strips, Div 
 }  // namespace
 
 gsi_status launch_evict(const EvictArgs &a, int dtype, hipStream_t st) {
-  const int slots = a.c.most << a.c.shift, blocks = (slots / kBlock + 4) / 4 * 4;  // pieces of 16 bytes behind them
+  const int slots = a.c.most << a.c.shift, blocks = slots / kBlock + 1;
   const int pieces = a.c.d * (dtype == GSI_FP32 ? 4 : 2) / 16, per = 256 / pieces * kMoveRows;
   const int64_t rows = (int64_t)a.c.S * a.c.heads, strips = (a.budget + per - 1) / per;
   if (rows * kThreads > kMostLaunch || rows * strips * 256 > kMostLaunch) return GSI_E_SHAPE;
-  const int wanted = (std::max(1, std::min({a.budget, slots - a.budget, 8192})) + 3) / 4 * 4;
-  // As few blocks of keys in registers as hold the slots, otherwise keys in LDS, us
-  // with 1 and 2 blocks, LDS and keys read again: 2049 to 2048 12.2, 12.8, 14.3, 17.5;
-  // 5003 to 777 (fp32) -, 21.2, 22.3, 26.8; 512 heads of 8000 to 7999 -, 48.0, 51.2,
-  // 63.5; 30011 to 4000 -, -, 63.8, 77.0.  (Eight blocks in registers: as LDS, and 4 us
-  // more for 4001 slots among them; so much straight code waits for its fetch.)
-  const auto select = [&](auto nb, int holes, size_t keys) {
-    const size_t lds = (size_t)blocks * (nb == 0 ? 36 : 4) + (size_t)holes * 4 + keys;
-    select_kernel<decltype(nb)::value><<<(unsigned)rows, kThreads, lds, st>>>(a, blocks, holes, pieces);
-  };
+  const int holes = std::max(1, std::min({a.budget, slots - a.budget, 8192}));
+  const size_t lds = (size_t)blocks * 36 + (size_t)holes * 4;
+  // As few blocks of keys in registers as hold the slots, us with 1, 2, 8 and 0 (in
+  // memory) of a wavefront: 2049 to 2048 12.9, 13.5, 17.4, 17.6; 5003 to 777 (fp32)
+  // -, 22.0, 25.9, 28.1; 30011 to 4000 -, -, 63.6, 79.6.
   if (slots <= kWaves * kBlock)
-    select(std::integral_constant<int, 1>{}, wanted, 0);
+    select_kernel<1><<<(unsigned)rows, kThreads, lds, st>>>(a, blocks, holes, pieces);
   else if (slots <= 2 * kWaves * kBlock)
-    select(std::integral_constant<int, 2>{}, wanted, 0);
-  else if (slots <= kLdsBlocks * kWaves * kBlock)
-    select(std::integral_constant<int, kInLds>{}, std::min(wanted, 4096), (size_t)((slots + kBlock - 1) / kBlock) * kBlock * 4);
+    select_kernel<2><<<(unsigned)rows, kThreads, lds, st>>>(a, blocks, holes, pieces);
+  else if (slots <= 8 * kWaves * kBlock)
+    select_kernel<8><<<(unsigned)rows, kThreads, lds, st>>>(a, blocks, holes, pieces);
   else
-    select(std::integral_constant<int, 0>{}, wanted, 0);
+    select_kernel<0><<<(unsigned)rows, kThreads, lds, st>>>(a, blocks, holes, pieces);
   if (hipGetLastError() != hipSuccess) return GSI_E_HIP;
   // In place no more move than there are slots behind the budget; select_kernel
   // has made few (and made again they change nothing: nothing is moved from
