@@ -420,6 +420,46 @@ def test_attend_more_sequences_than_a_wavefront_counts(window):
     assert not bool((off & ~torch.isnan(before)).any()) and torch.equal(torch.isnan(before), torch.isnan(c.mass))
 
 
+def check_against_plain(c, table, lengths, q, what):
+    """Held to plain_attend; n / 16 + 64 additions of a chain at most, as in check_attend."""
+    d = c.d
+    ref, lse, _, size, big = (t.cpu().numpy() for t in plain_attend(c, table, lengths, q, d**-0.5))
+    out, l = gsi.gsi_cache_attend(c, table, lengths, q)
+    delta = (d + 8) * 2.0**-24 * big + (2 * big + 8) * 2.0**-23
+    chain = (max(int(lengths.max()), 1) / 16 + 64) * 2.0**-23
+    rel = 2 * delta + 2.0**-16 + chain
+    within(out, ref, half(c.dtype) * np.abs(ref) * 1.001 + size * rel[:, :, None] * 1.01 + 1e-30, what)
+    within(l, lse, delta + chain + 2.0**-22 + 2.0**-22 * np.abs(np.where(np.isfinite(lse), lse, 0.0)), what + " lse")
+
+
+@DTYPES
+@pytest.mark.parametrize("d", [16, 128, 256])
+@pytest.mark.parametrize("heads,group", [(1, 17), (3, 33), (2, 40), (1, 300), (1, 1000)])
+def test_attend_shares_of_many_query_heads(heads, group, d, dtype):
+    """Ragged lengths, some empty, over more than 16 query heads of a key head: two
+    to 63 workgroups of a share, eight shares of them at least."""
+    g = gen(heads + group + d)
+    S = 21
+    lengths = torch.exp(torch.rand(S, generator=g, device=DEV) * np.log(1500)).int()
+    lengths[::5] = 0
+    c, table = make_pool(g, S, lengths.tolist(), heads, 16, d, dtype, most=94, age=False)
+    q = 2 * torch.randn(S, heads * group, d, generator=g, device=DEV).to(dtype)
+    check_against_plain(c, table, lengths, q, f"{heads} heads of {group}")
+
+
+@pytest.mark.parametrize("n", [49024, 49025, 49152, 65537])
+@pytest.mark.parametrize("others", [[], [0], [5, 0, 1, 700]])
+def test_attend_shares_by_units_and_by_cost(n, others):
+    """A long sequence around the length from which on rows cost too, before and
+    behind short ones."""
+    g = gen(n + len(others))
+    for lens in ([n] + others, others + [n]):
+        lengths = torch.tensor(lens, device=DEV, dtype=torch.int32)
+        c, table = make_pool(g, len(lens), lens, 1, 64, 256, BF16, most=-(-n // 64), age=False)
+        q = 2 * torch.randn(len(lens), 2, 256, generator=g, device=DEV).to(BF16)
+        check_against_plain(c, table, lengths, q, f"{lens}")
+
+
 def test_attend_nothing_at_all():
     """Only empty sequences; tables without a page; no sequence."""
     g = gen(42)
