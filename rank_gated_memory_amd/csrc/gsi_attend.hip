@@ -742,10 +742,10 @@ __global__ void __launch_bounds__(kThreads) mass_kernel(AttendArgs a, Plan p, in
   }
 }
 
-// Workgroups that the chip holds at once, by the registers of the kernel.  With as
-// many for each CU as with one more and one less (us): 64 ragged sequences of 40
-// heads of 128: 2 182, 3 199, 1 212; 16 of 4000 slots, 8 heads of 64: 3 31.6, 2 31.0,
-// 4 34.8; of 256: 1 103, 2 110.
+// Workgroups that the chip holds at once, by the registers of the kernel.  With 1, 2,
+// 3 and 4 for each CU, us: 64 ragged sequences of 40 heads of 128 201, 163, 181, 165; of
+// 8 heads of 64 34, 28, 27, 31; 16 of 4000 slots of 8 heads of 64 35, 30, 31, 34, of 256
+// 101, 105, 113.
 inline int shares_for(int d) { return 256 * (d <= 64 ? 3 : d <= 128 ? 2 : 1); }
 
 template <typename E>
@@ -805,11 +805,11 @@ gsi_status launch_as(const AttendArgs &a, hipStream_t st) {
     const int most = heads_at_once(a.c.d), sets = (p.kept + most - 1) / most;
     const int64_t by_cuts = (int64_t)(p.shares - 1) * p.tiles * sets, by_heads = (int64_t)a.c.S * a.q.n;
     // A query head for each workgroup has more threads for many pieces, as long as
-    // they run at once.  By heads and by cuts, us more or less of a call: 2000
-    // slots of 2 key heads for 64, 4 sequences (256 heads) 2.2 less, 24 (1536) 0.7
-    // less, 64 (4096) 5.5 more; 8 for 32, 24 sequences (768) 0.3 less, 48 (1536)
-    // 1.6 more, 96 4.0 more.
-    const bool cuts = by_heads > 2048 && by_cuts < by_heads;
+    // they run at once.  By heads and by cuts, us: 2000 slots of 2 key heads for 64, 4
+    // sequences (256 heads) 12.3 and 13.9, 24 (1536) 17.8 and 16.9, 64 (4096) 29.1 and
+    // 22.4; 1 to 8000 slots, 16 (1024) 22.5 and 27.4, 32 (2048) 25.7 both; 2000 slots of 8
+    // key heads for 32, 24 (768) 20.1 and 20.2, 64 (2048) 28.1 and 24.7.
+    const bool cuts = by_heads > 1536 && by_cuts < by_heads;
     join_kernel<E><<<(unsigned)(cuts ? by_cuts : by_heads), kThreads, 0, st>>>(a, p, cuts, sets);
     if (hipGetLastError() != hipSuccess) return GSI_E_HIP;
   }
