@@ -8,10 +8,11 @@
 //                   once in shares of equal cost, from the lengths as they are:
 //                   no workgroup is idle however the lengths differ.  A workgroup
 //                   takes up to 16 query heads of its rows (a tile); where a key
-//                   head has more, a share has a workgroup for each tile.  A step's keys and values are read once,
-//                   straight into the registers that the matrix instructions
-//                   take them from.  One pass with the running maximum and sum
-//                   of the softmax; wavefronts are joined through LDS.
+//                   head has more, a share has a workgroup for each tile.  A
+//                   step's keys and values are read once, straight into the
+//                   registers that the matrix instructions take them from.  One
+//                   pass with the running maximum and sum of the softmax;
+//                   wavefronts are joined through LDS.
 //   join_kernel   : rows that a share's end cuts, from the workspace.
 //   mass_kernel   : the weights added to the mass, from the scores that
 //                   attend_kernel has left in the workspace.
@@ -28,16 +29,18 @@
 // run.  No value goes through LDS and no layout of the pool other than rows is
 // needed.  With fewer than 16 query heads the other rows of the tile are idle:
 // at 16 B a clock and CU from HBM the matrix cores are at 5 % (bf16) or 30 %
-// (fp32) of their rate even then.  The workgroups of a share's tiles run on one XCD
-// at one time, so that one of them reads from HBM and all from its L2: 64 sequences
-// of 2000 slots, 8 key heads for 256, 524 MB, 119 us; with tiles as further rows 190,
-// 16 query heads for each key head 100.  Bound by HBM where the lengths fill the chip: two sequences of
-// 131071 slots, 8 heads of 128, 537 MB in 100 us, 5.4 TB/s; 64 of 1 to 4096 slots, 40
-// heads of 128, 700 MB in 143 us with the scores kept, 4.9.  One sequence of 1777
-// slots of 16 heads of 256, 29 MB, takes 12 us and 4 for the join, a page number's,
-// the keys' and the values' latency after the launch's.  (Two tiles in one pass were no faster: 64 sequences of 2000
-// slots, one key head for 32: 38 us in two rows and 39 in one; one of 65536: 25
-// and 40, for the larger sums to join.)
+// (fp32) of their rate even then.  The workgroups of a share's tiles run on one
+// XCD at one time, so that one of them reads from HBM and all from its L2: 64
+// sequences of 2000 slots, 8 key heads for 256, 524 MB, 115 us (16 query heads for
+// each key head: 98; with the tiles one after the other 190).  Two tiles in one
+// workgroup's registers: 64 sequences of 2000 slots, one key head for 32, 39 us, in
+// two workgroups 28.
+//
+// Bound by HBM where the lengths fill the chip: two sequences of 131071 slots, 8
+// heads of 128, 537 MB in 98 us, 5.5 TB/s; 64 of 1 to 4096 slots, 40 heads of 128,
+// 700 MB in 143 us with the scores kept, 4.9.  One sequence of 1777 slots of 16
+// heads of 256, 29 MB, takes 12 us and 4 for the join: a launch's latency, a
+// length's, a page number's, and the keys' and values' own.
 //
 // Weights are rounded to bf16 twice, p = hi + lo to 2^-17, and multiplied in two
 // instructions, so that in bf16 too only the result's own rounding shows.
@@ -167,9 +170,9 @@ struct Place {
 // The shares of all rows' units.  A unit costs two and a row one, what its first
 // loads and its join take (64 ragged sequences of 40 heads, 6 rows of a share in
 // the mean: 158 us by units alone, where the shares of many short rows end last,
-// 145 so); share b begins with the first unit at or behind b all / of of the
-// cost.  Units are at most three apart: a share is not empty where it has as much;
-// where that is not so, units alone are the cost.
+// 143 so); share b begins with the first unit at or behind b / of of the cost.
+// Units are at most three apart: a share is not empty where it has as much; where
+// that is not so, units alone are the cost.
 template <typename Count>
 struct Shares {
   const AttendArgs &a;
@@ -531,7 +534,8 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
       if (4 * quad + i >= live) continue;
 #pragma unroll
       for (int j = 0; j < NC; j += 2)
-        *reinterpret_cast<f32x2_t *>(&red[wave][4 * quad + i][col0 + j]) = f32x2_t{acc[j][i] * f[i], acc[j + 1][i] * f[i]};
+        *reinterpret_cast<f32x2_t *>(&red[wave][4 * quad + i][col0 + j]) =
+            f32x2_t{acc[j][i] * f[i], acc[j + 1][i] * f[i]};
     }
     __syncthreads();
     const int64_t slot = (2 * ((int64_t)tile * p.shares + share) + (seg.skip == 0)) * p.kept;
