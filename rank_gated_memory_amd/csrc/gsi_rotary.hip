@@ -101,16 +101,47 @@ __device__ __forceinline__ Item item_of(const RotateArgs &a, const Split &sp, co
   return r;
 }
 
+// Fewer elements than 8 bytes hold, in pieces of 4 and 2 bytes.
+template <typename E>
+__device__ __forceinline__ uint64_t load_few(const uint8_t *at, int count) {
+  uint64_t v = 0;
+  uint32_t four = 0;
+  if constexpr (sizeof(E) == 4) {
+    if (count > 0) __builtin_memcpy(&four, at, 4);
+    v = four;
+  } else {
+    uint16_t two = 0;
+    if (count & 2) __builtin_memcpy(&four, at, 4);
+    if (count & 1) __builtin_memcpy(&two, at + 2 * (count & 2), 2);
+    v = (uint64_t)two << 16 * (count & 2) | four;
+  }
+  return v;
+}
+template <typename E>
+__device__ __forceinline__ void store_few(uint8_t *at, uint64_t v, int count) {
+  const uint32_t four = (uint32_t)v;
+  if constexpr (sizeof(E) == 4) {
+    if (count > 0) __builtin_memcpy(at, &four, 4);
+  } else {
+    const uint16_t two = (uint16_t)(v >> 16 * (count & 2));
+    if (count & 2) __builtin_memcpy(at, &four, 4);
+    if (count & 1) __builtin_memcpy(at + 2 * (count & 2), &two, 2);
+  }
+}
+
 // A run of `count` elements, 16 bytes of them where they are all there.
 template <bool Whole, typename vec, typename E, int V>
 __device__ __forceinline__ vec load_run(const uint8_t *at, int count) {
   vec v = {};
   if (Whole || count == V) {
     __builtin_memcpy(&v, Whole ? __builtin_assume_aligned(at, 16) : at, 16);
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (e < count) v[e] = reinterpret_cast<const E *>(at)[e];
+  } else if (count > 0) {
+    const bool half = count >= V / 2;
+    uint64_t two[2] = {0, 0};
+    if (half) __builtin_memcpy(two, at, 8);
+    const uint64_t rest = load_few<E>(at + (half ? 8 : 0), count % (V / 2));
+    two[half ? 1 : 0] = rest;
+    __builtin_memcpy(&v, two, 16);
   }
   return v;
 }
@@ -118,10 +149,12 @@ template <bool Whole, typename vec, typename E, int V>
 __device__ __forceinline__ void store_run(uint8_t *at, const vec &v, int count) {
   if (Whole || count == V) {
     __builtin_memcpy(Whole ? __builtin_assume_aligned(at, 16) : at, &v, 16);
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (e < count) reinterpret_cast<E *>(at)[e] = v[e];
+  } else if (count > 0) {
+    const bool half = count >= V / 2;
+    uint64_t two[2];
+    __builtin_memcpy(two, &v, 16);
+    if (half) __builtin_memcpy(at, two, 8);
+    store_few<E>(at + (half ? 8 : 0), half ? two[1] : two[0], count % (V / 2));
   }
 }
 
@@ -164,17 +197,19 @@ __global__ void __launch_bounds__(kThreads, 8) rotate_kernel(RotateArgs a, Split
       w[j] = k.turn[it.t];
       int e = it.unit * V;
       if (it.turns) {
-        if (it.unit < runs) {
-          turn[j] = Halves ? e : e / 2;
-          count[j] = min(V, run - e);
-          e += a.start;
-        } else if (it.unit < runs + left) {
-          e -= runs * V;
-          count[j] = min(V, a.start - e);
-        } else {
-          e += a.start + a.turned - (runs + left) * V;
-          count[j] = min(V, a.d - e);
+        // the part that the run is of, and where that begins
+        const bool turns = it.unit < runs, before = it.unit < runs + left;
+        const int part = turns ? run : before ? a.start : a.d - a.start - a.turned;
+        const int first = turns ? a.start : before ? 0 : a.start + a.turned;
+        e -= V * (turns ? 0 : before ? runs : runs + left);
+        if (!Whole) {
+          if (it.from != it.to && part >= V)
+            e = min(e, part - V);  // again what the run before has: the same values
+          else
+            count[j] = min(V, part - e);
         }
+        if (turns) turn[j] = Halves ? e : e / 2;
+        e += first;
       }
       if (!it.to || (it.turns && turn[j] < 0 && it.from == it.to)) continue;  // no entry; in place
       const uint8_t *const from = it.from + e * es;
