@@ -161,11 +161,13 @@ __device__ __forceinline__ void store_run(uint8_t *at, const vec &v, int count) 
 // Bound by HBM for many tokens (8191 of 40 heads of 128: 168 MB in 29 us, 5.8
 // TB/s; 4939 of 16 heads of 256 with their keys and values into the pages: 243
 // MB in 54 us, 4.5 TB/s), by latency for few (one token of 16 heads of 256 3 us):
-// the position, the sine and cosine, the head.  The angles are formed once for all heads of a token.  Whole: runs of
-// 16 bytes end where the turned part does; otherwise the turned part, what lies
-// before it and what lies behind are cut into runs each by itself, the last one
-// shorter, at any address (333 tokens of 40 fp32 heads of 200: all turned in
-// halves 5.8 us, 74 elements of each 7.8).
+// the position, the sine and cosine, the head.  The angles are formed once for all
+// heads of a token.  Whole: runs of 16 bytes end where the turned part does;
+// otherwise the turned part, what lies before it and what lies behind are cut into
+// runs each by itself, at any address.  Their last run then ends where the part
+// does and repeats what the run before it has; in place, where that would turn
+// elements twice, it is the shorter rest (8191 tokens of 40 heads of 128 in halves,
+// bf16: all turned 27 us, 100 elements of each 29, in place 35).
 template <typename E, bool Halves, bool Whole>
 __global__ void __launch_bounds__(kThreads, 8) rotate_kernel(RotateArgs a, Split sp) {
   __shared__ Tokens k;

@@ -140,6 +140,26 @@ def test_rotary(T, heads, d, turned, start, layout, dtype):
 
 
 @DTYPES
+@pytest.mark.parametrize("layout", ["pairs", "halves"])
+def test_rotary_every_part_of_a_head(layout, dtype):
+    """Parts of every size from every element on, in new rows and in place."""
+    g = gen(91)
+    x = torch.randn(3, 2, 24, generator=g, device=DEV).to(dtype)
+    pos = torch.tensor([7, -3, 100003], device=DEV)
+    for turned in range(2, 25, 2):
+        for start in range(25 - turned):
+            freqs = gsi.rotary_freqs(turned)
+            r = gsi.Rotary(freqs, layout=layout, start=start, device=DEV)
+            y = gsi.gsi_rotary(r, x, pos)
+            check_rotary(y, x, pos, freqs, layout, start, 1.0, dtype, f"{turned} from {start}")
+            assert torch.equal(bits(y[..., :start]), bits(x[..., :start]))
+            assert torch.equal(bits(y[..., start + turned:]), bits(x[..., start + turned:]))
+            z = x.clone()
+            gsi.gsi_rotary(r, z, pos, y=z)
+            assert torch.equal(bits(z), bits(y)), f"{turned} from {start} in place"
+
+
+@DTYPES
 def test_rotary_strides_and_what_is_left(dtype):
     g = gen(3)
     T, heads, d = 19, 6, 48
