@@ -47,6 +47,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "gsi_attend_at.h"
 #include "gsi_cache.h"
 
 namespace gsi {
@@ -75,7 +76,7 @@ struct Plan {
 };
 
 template <typename E>
-constexpr int kStep = sizeof(E) == 2 ? 32 : 16;
+constexpr int kStep = attend_step(sizeof(E));
 
 // The slots [first, n) of a sequence in steps [lo, lo + steps), and in units.
 struct Span {
@@ -251,16 +252,15 @@ template <typename E, int KS>
 __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) attend_kernel(AttendArgs a, Plan p) {
   constexpr bool f32 = sizeof(E) == 4;
   constexpr int es = sizeof(E), step = kStep<E>;
-  constexpr int KT = f32 ? 1 : 2;          // tiles of keys of a step
-  constexpr int CH = f32 ? 2 * KS : KS;    // 16-byte pieces of a key that a lane holds
-  constexpr int CE = f32 ? 16 : 32;        // elements of a key in piece c of the four lanes
-  constexpr int VT = f32 ? 4 : 8;          // slots whose scores and values a lane holds
-  constexpr int NC = 2 * KS;               // columns of a value that a lane holds
+  constexpr int KT = key_tiles(es);        // tiles of keys of a step
+  constexpr int CH = key_pieces(es, KS);   // 16-byte pieces of a key that a lane holds
+  constexpr int VT = value_slots(es);      // slots whose scores and values a lane holds
+  constexpr int NC = value_columns(KS);    // columns of a value that a lane holds
   constexpr int VD = NC * es / 4;          // dwords
   // whether the next segment's first loads go out before the present one is done:
   // for fp32 heads above 96 there are no registers for it
   constexpr bool kAhead = !f32 || KS <= 3;
-  constexpr int GC = CH - (f32 ? 2 : 1) * (KS > 4 ? 2 : 1);  // pieces from here on may lie behind the key
+  constexpr int GC = key_guarded(es, KS);  // pieces from here on may lie behind the key
   // rows of 16-byte pieces, four rows apart on other banks
   __shared__ __attribute__((aligned(16))) float red[kWaves][16][32 * KS + 4];
   __shared__ float red_m[kWaves][16], red_l[kWaves][16];
@@ -301,11 +301,10 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
   // page.  Its first column, and its offsets from the start of the block: the last
   // run of columns ends with the value.  (One page for a whole step, in scalar
   // registers, where pages hold whole steps: 3 % slower to 2 % faster.)
-  const int col0 = min(l16 * NC, d - NC);
-  const int ktoken = f32 ? l16 & 7 : l16 & 3, vtoken = f32 ? 4 * (quad & 1) : 0;
-  const int kblock = f32 ? l16 >> 3 : l16 >> 2, vblock = f32 ? quad >> 1 : quad;
+  const int col0 = first_column(KS, d, l16);
+  const int kblock = key_block(es, l16), vblock = value_block(es, quad);
   const uint32_t ss = (uint32_t)a.c.slot_stride, pages = a.c.pages;
-  const uint32_t ko = ktoken * ss + 16 * quad, vo = vtoken * ss + col0 * es;
+  const uint32_t ko = key_slot(es, l16) * ss, vo = value_slot(es, quad) * ss + col0 * es;
   const float scale2 = a.scale * 1.4426950408889634f;
 
   // The page numbers of this lane's keys and values, as the table has them: they
@@ -330,9 +329,8 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
     const uint8_t *const at = a.q.p + g.s * a.q.row + (g.kh * a.group + tile * 16 + l16) * a.q.head;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int e = c * CE + 16 / es * quad;
       q[c] = u32x4_t{0, 0, 0, 0};
-      if (l16 < live && e < d) q[c] = *reinterpret_cast<const u32x4_t *>(at + e * es);
+      if (l16 < live && piece_inside(es, d, c, quad)) q[c] = *reinterpret_cast<const u32x4_t *>(at + 64 * c + 16 * quad);
     }
   };
   // The addresses are formed one after the other: all at once they would take as
@@ -347,8 +345,7 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
     for (int u = 0; u < KT; ++u) {
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const uint32_t in = c < GC || c * CE + 16 / es * quad < d ? c * 64 : 0;
-        k[u][c] = *reinterpret_cast<const u32x4_t *>(at + (ko + in));
+        k[u][c] = *reinterpret_cast<const u32x4_t *>(at + (ko + piece_at(es, KS, d, c, quad)));
       }
       if (u + 1 < KT) at = here(at + 4 * (uint64_t)ss);
     }
@@ -417,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
         sc[u] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-          if (c >= GC && c * CE + 16 / es * quad >= d) k[u][c] = u32x4_t{0, 0, 0, 0};
+          if (c >= GC && !piece_inside(es, d, c, quad)) k[u][c] = u32x4_t{0, 0, 0, 0};
           if constexpr (f32) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -791,7 +788,7 @@ gsi_status launch_as(const AttendArgs &a, hipStream_t st) {
   const auto go = [&](auto ks) {
     attend_kernel<E, decltype(ks)::value><<<grid, kThreads, 0, st>>>(a, p);
   };
-  const int ks = (a.c.d + 31) / 32;
+  const int ks = attend_ks(a.c.d);
   if (ks == 1)
     go(std::integral_constant<int, 1>{});
   else if (ks == 2)
@@ -800,7 +797,7 @@ gsi_status launch_as(const AttendArgs &a, hipStream_t st) {
     go(std::integral_constant<int, 3>{});
   else if (ks == 4)
     go(std::integral_constant<int, 4>{});
-  else if (ks <= 6)
+  else if (ks == 6)
     go(std::integral_constant<int, 6>{});
   else
     go(std::integral_constant<int, 8>{});
