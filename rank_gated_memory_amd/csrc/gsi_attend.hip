@@ -42,8 +42,11 @@
 // heads of 256, 29 MB, takes 12 us and 4 for the join: a launch's latency, a
 // length's, a page number's, and the keys' and values' own.
 //
-// Weights are rounded to bf16 twice, p = hi + lo to 2^-17, and multiplied in two
-// instructions, so that in bf16 too only the result's own rounding shows.
+// Weights are two bf16 numbers, p = hi + lo to 2^-16, multiplied in two
+// instructions, so that in bf16 too only the result's own rounding shows.  hi is p
+// cut off, and lo what is left, at least 2^-126: where p is not 0 both are above
+// it, and a value that is infinite gives the same infinity with both (hi rounded,
+// lo may be 0 or below it, and their sum NaN).
 #include <algorithm>
 #include <type_traits>
 
@@ -490,8 +493,9 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
         for (int t = 0; t < 4; ++t) both[t] = (in[2 * t] & 0xffffu) | (in[2 * t + 1] & 0xffff0000u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          hi[i] = (__bf16)w[i];
-          lo[i] = (__bf16)(w[i] - (float)hi[i]);
+          const float cut = __uint_as_float(__float_as_uint(w[i]) & 0xffff0000u);
+          hi[i] = (__bf16)cut;
+          lo[i] = (__bf16)__builtin_amdgcn_fmed3f(w[i] - cut, 0x1p-126f, w[i]);
         }
 #pragma unroll
         for (int j = 0; j < NC; ++j) {

@@ -598,6 +598,35 @@ def test_attend_non_finite_rows_stay_alone(dtype):
 
 
 @DTYPES
+@pytest.mark.parametrize("q_size", [0.0, 0.3, 2.0], ids=["equal weights", "near weights", "weights apart"])
+def test_attend_infinite_values(q_size, dtype):
+    """An infinite value makes its column infinite, whatever its weight (one slot:
+    exactly 1; others on either side of a number with a short significand), two of
+    opposite signs make it NaN; other columns and heads do not see them."""
+    g = gen(61)
+    lens = [1, 2, 3, 7, 40, 700, 2500]
+    lengths = torch.tensor(lens, device=DEV, dtype=torch.int32)
+    c, table = make_pool(g, len(lens), lens, 2, 16, 64, dtype)
+    q = q_size * torch.randn(len(lens), 4, 64, generator=g, device=DEV)
+    q = q.to(dtype)
+    ref, lse = gsi.gsi_cache_attend(c, table, lengths, q)
+    inf = float("inf")
+    want = f64(ref)
+    for s, n in enumerate(lens):
+        a, b = (int(t) for t in torch.randint(0, n, (2,), generator=g, device=DEV))
+        at = lambda t: (int(table[s, t // 16]), 0, t % 16)  # noqa: E731
+        c.V[at(a)][3], c.V[at(a)][4] = inf, -inf
+        want[s, :2, 3], want[s, :2, 4] = inf, -inf
+        if a != b:
+            c.V[at(a)][60], c.V[at(b)][60] = inf, -inf
+            c.V[at(a)][61], c.V[at(b)][61] = inf, inf
+            want[s, :2, 60], want[s, :2, 61] = np.nan, inf
+    out, l = gsi.gsi_cache_attend(c, table, lengths, q)
+    assert np.array_equal(f64(out), want, equal_nan=True)
+    assert torch.equal(bits(l), bits(lse))
+
+
+@DTYPES
 def test_attend_strides_and_what_is_left(dtype):
     g = gen(14)
     S, H, d = 5, 6, 72
