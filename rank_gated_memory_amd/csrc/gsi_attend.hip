@@ -73,7 +73,7 @@ struct Plan {
   int shares;  // workgroups of a tile
   int scores_row;
   float *stats;    // [tiles][2 shares][kept]: maximum (times log2 e) and sum
-  float *partial;  // [tiles][2 shares][kept][d], sums at that maximum
+  float *partial;  // [tiles][2 shares][kept][d], values' sums over that sum
   float *level;    // [S * heads]: log2 of the sum of all weights, infinity for none
   float *scores;   // [S * heads][scores_row], times log2 e
 };
@@ -240,6 +240,14 @@ __device__ __forceinline__ float quads_sum(float v) {
 __device__ __forceinline__ float exp2_of(float v) { return __builtin_amdgcn_exp2f(v); }
 __device__ __forceinline__ float log2_of(float v) { return __builtin_amdgcn_logf(v); }
 
+// Weights are 2^8 at most (see below), and values times their sum over many slots
+// may pass the largest number where the result does not.  Values are therefore added
+// up with weights times this, which over so many slots sum to less than 1.  (In turn
+// products below 2^-126 lose their digits: values of 2^-87 at 2^30 slots.)
+__device__ __forceinline__ float down_of(int slots) {
+  return __uint_as_float((uint32_t)(127 - 41 + __clz(slots)) << 23);  // 2^-9 / slots, rounded down
+}
+
 // Where -inf is the maximum so far nothing has a weight: any finite number does
 // for it in the exponent.
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
@@ -403,6 +411,7 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
 #pragma unroll
     for (int j = 0; j < NC; ++j) acc[j] = f32x4_t{0, 0, 0, 0};
     float m = -INFINITY, sum = 0.f;  // of head l16; the sum over this lane's slots
+    const float down = down_of(seg.mine * step);
     if (kAhead && seg.st >= seg.end && !last) {  // no step of this wavefront
       load_q(then);
       if (ahead) {
@@ -479,6 +488,7 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
       for (int i = 0; i < VT; ++i) {
         w[i] = exp2_of(w[i] - base);
         sum += w[i];
+        w[i] *= down;
       }
       if constexpr (f32) {
 #pragma unroll
@@ -524,12 +534,15 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
     float ms[kWaves], ls[kWaves];
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) ms[w] = red_m[w][l16], ls[w] = red_l[w][l16];
-    const float top = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3])), base = base_of(top), fade = exp2_of(m - base);
+    const float top = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3])), base = base_of(top);
     float total = 0.f, f[4];
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) total += ls[w] * exp2_of(ms[w] - base);
+    const uint64_t none = __ballot(total == 0.f);  // heads without a weight
+    // this wavefront's sums are divided before they are added to the others'
+    const float share_of = exp2_of(m - base) / (total * down);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = __shfl(fade, 4 * quad + i, 64);
+    for (int i = 0; i < 4; ++i) f[i] = __shfl(share_of, 4 * quad + i, 64);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (4 * quad + i >= live) continue;
@@ -546,21 +559,20 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
       else
         *reinterpret_cast<f32x2_t *>(p.stats + 2 * (slot + lane)) = f32x2_t{top, total};
     }
-    const float inv = total == 0.f ? 0.f : 1.f / total;  // zero for a head without a weight
     constexpr int W = KS == 3 ? 32 : KS == 6 ? 64 : 8 * KS;  // threads of a head
     const int c = 4 * (threadIdx.x % W);
     for (int h0 = 0; h0 < live; h0 += kThreads / W) {
       const int h = h0 + threadIdx.x / W;
-      const float scale = __shfl(inv, h & 15, 64);
       if (h >= live || c >= d) continue;
       f32x4_t o = *reinterpret_cast<const f32x4_t *>(&red[0][h][c]);
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) o += *reinterpret_cast<const f32x4_t *>(&red[w][h][c]);
+      if (none >> h & 1) o = f32x4_t{0, 0, 0, 0};
       if (whole) {
         typedef E out_t __attribute__((ext_vector_type(4)));
         out_t r;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = (E)(scale == 0.f ? 0.f : o[e] * scale);
+        for (int e = 0; e < 4; ++e) r[e] = (E)o[e];
         *reinterpret_cast<out_t *>(a.out.p + s * a.out.row + (head0 + h) * a.out.head + c * es) = r;
       } else {
         *reinterpret_cast<f32x4_t *>(p.partial + (slot + h) * d + c) = o;
@@ -632,6 +644,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttendArgs a, Plan p, bo
   if (pieces <= 1) return;
   const int head0 = kh * a.group + tile * 16 + in_tile;
   // `sides` threads share four columns of a head, each takes every sides-th piece
+  const float down = down_of(units * kWaves * kStep<E>);
   const int items = live * d / 4, sides = kThreads / items, side = tid / items, item = tid - side * items;
   const int h = 4 * item / d, c = 4 * item - h * d;
   if (side < sides) {
@@ -660,9 +673,9 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttendArgs a, Plan p, bo
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         if (i0 + k * sides >= pieces) continue;
-        const float f = exp2_of(t[k].m - base);
-        all.l += t[k].l * f;
-        o += u[k] * f;
+        const float f = t[k].l * exp2_of(t[k].m - base);
+        all.l += f;
+        o += u[k] * (f * down);
       }
     }
     *reinterpret_cast<f32x4_t *>(red + 4 * tid) = o;
@@ -681,7 +694,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttendArgs a, Plan p, bo
   if (c == 0) finish_row(a, p, (int64_t)s * a.q.n + head0 + h, top, total);
   E *const out = reinterpret_cast<E *>(a.out.p + s * a.out.row + (head0 + h) * a.out.head) + c;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) out[k] = (E)(total == 0.f ? 0.f : v[k] / total);
+  for (int k = 0; k < 4; ++k) out[k] = (E)(total == 0.f ? 0.f : v[k] / (total * down));
 }
 
 constexpr int kMassSlots = 256;  // of a strip

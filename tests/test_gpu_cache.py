@@ -440,7 +440,7 @@ def test_attend_more_sequences_than_a_wavefront_counts(window):
     assert not bool((off & ~torch.isnan(before)).any()) and torch.equal(torch.isnan(before), torch.isnan(c.mass))
 
 
-def check_against_plain(c, table, lengths, q, what):
+def check_against_plain(c, table, lengths, q, what, least=1e-30):
     """Held to plain_attend; n / 16 + 64 additions of a chain at most, as in check_attend."""
     d = c.d
     ref, lse, _, size, big = (t.cpu().numpy() for t in plain_attend(c, table, lengths, q, d**-0.5))
@@ -448,7 +448,7 @@ def check_against_plain(c, table, lengths, q, what):
     delta = (d + 8) * 2.0**-24 * big + (2 * big + 8) * 2.0**-23
     chain = (max(int(lengths.max()), 1) / 16 + 64) * 2.0**-23
     rel = 2 * delta + 2.0**-16 + chain
-    within(out, ref, half(c.dtype) * np.abs(ref) * 1.001 + size * rel[:, :, None] * 1.01 + 1e-30, what)
+    within(out, ref, half(c.dtype) * np.abs(ref) * 1.001 + size * rel[:, :, None] * 1.01 + least, what)
     within(l, lse, delta + chain + 2.0**-22 + 2.0**-22 * np.abs(np.where(np.isfinite(lse), lse, 0.0)), what + " lse")
 
 
@@ -624,6 +624,24 @@ def test_attend_infinite_values(q_size, dtype):
     out, l = gsi.gsi_cache_attend(c, table, lengths, q)
     assert np.array_equal(f64(out), want, equal_nan=True)
     assert torch.equal(bits(l), bits(lse))
+
+
+@DTYPES
+@pytest.mark.parametrize("d", [24, 64, 128, 256])
+def test_attend_values_near_the_largest(d, dtype):
+    """Values up to 2^128 times 0.97: sums of values that are not yet divided by the
+    weights' sum would pass the largest number, in some wavefronts and shares and not
+    in others; and values of 2^-100, results of which have no fewer digits."""
+    g = gen(62 + d)
+    lens = [1, 2, 3, 40, 700, 2500, 3000, 0] + torch.randint(1, 120, (100,), generator=g, device=DEV).tolist()
+    lengths = torch.tensor(lens, device=DEV, dtype=torch.int32)
+    c, table = make_pool(g, len(lens), lens, 4, 16, d, dtype, age=False)
+    V = torch.nan_to_num(c.V).clamp(-3.875, 3.875)
+    q = torch.randn(len(lens), 8, d, generator=g, device=DEV).to(dtype)
+    for values in (V, V.abs()):  # signs that cancel, and sums of n values
+        for k in (0, 126, 121, -100):
+            c.V.copy_(values.double() * 2.0**k)
+            check_against_plain(c, table, lengths, q, f"values of 2^{k}", least=0.0 if k else 1e-30)
 
 
 @DTYPES
