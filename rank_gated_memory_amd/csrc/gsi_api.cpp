@@ -17,6 +17,7 @@
 #include "gsi_batched.h"
 #include "gsi_calib.h"
 #include "gsi_internal.h"
+#include "gsi_layout.h"
 
 namespace gsi {
 hipError_t launch_prepare(int dtype, const void *W, const void *V, void *M, int d, int d_out,
@@ -74,27 +75,6 @@ int cu_count() {
 #ifndef GSI_APPLY_BLOCKS_PER_CU
 #define GSI_APPLY_BLOCKS_PER_CU 32
 #endif
-
-struct WsLayout {
-  uint64_t gate_off, need_off, pref_off, float_off, ctl_off, gcnt_off, total;
-};
-
-// The group counters of two-level partial sums follow the control words.
-uint64_t gcnt_offset(uint64_t ctl_off, int64_t ctl) { return align_up(ctl_off + (uint64_t)ctl * 4, 256); }
-
-// ctl: control words of the single-launch stack kernel (0 for gsi_linear);
-// units_a: projection units (at most one group counter each)
-WsLayout ws_layout(int64_t n, int64_t floats, int64_t ctl, int64_t units_a) {
-  WsLayout w;
-  w.gate_off = align_up((uint64_t)(n + 1) * 4, 256);
-  w.need_off = align_up(w.gate_off + (uint64_t)n * 16, 256);
-  w.pref_off = align_up(w.need_off + (uint64_t)n * 4, 256);
-  w.float_off = align_up(w.pref_off + (uint64_t)(n + 1) * 4, 256);
-  w.ctl_off = align_up(w.float_off + (uint64_t)floats * 4, 256);
-  w.gcnt_off = gcnt_offset(w.ctl_off, ctl);
-  w.total = align_up(w.gcnt_off + (uint64_t)units_a * 4, 256);
-  return w;
-}
 
 void set_ws(KArgs &a, void *ws, uint64_t gate_off, uint64_t need_off, uint64_t pref_off,
             uint64_t float_off, uint64_t gcnt_off) {
@@ -156,65 +136,6 @@ gsi_status gsi_prepare(const gsi_map *map, void *stream) {
   return e == hipSuccess ? GSI_OK : GSI_E_HIP;
 }
 
-// Bytes of V_k per projection unit of a stack plan: small enough that the
-// gates of a step open progressively (output work overlaps projection in
-// the single launch), large enough to amortise a unit's partial hand-off.
-#ifndef GSI_PLAN_PROJ_UNIT_KB
-#define GSI_PLAN_PROJ_UNIT_KB 384
-#endif
-static int64_t plan_proj_target(int64_t total_v_bytes) {
-  int64_t t = total_v_bytes / (256 * 4);
-  if (t < 16 * 1024) t = 16 * 1024;
-  if (t > GSI_PLAN_PROJ_UNIT_KB * 1024) t = GSI_PLAN_PROJ_UNIT_KB * 1024;
-  return t;
-}
-
-// Unit shapes of every call of a (validated) plan, chosen wave by wave.
-// A wave's projection units aim at (its V_k bytes) / 1024, clamped to
-// [16 KiB, GSI_PLAN_PROJ_UNIT_KB], and at most kMaxPartials per call (the
-// final sum of a call's partials is then one round of loads).  A wave whose fast
-// outputs make fewer than kFineUnits ordinary units is latency-bound (the
-// waves of a dependency-chained stack): it takes the smallest output units.
-constexpr int64_t kFineUnits = 1024;
-#ifndef GSI_PLAN_MAX_PARTIALS
-#define GSI_PLAN_MAX_PARTIALS 64
-#endif
-constexpr int64_t kMaxPartials = GSI_PLAN_MAX_PARTIALS;
-constexpr int64_t kTwoLevelUnitBytes = 64 * 1024;
-constexpr int64_t kMaxPartials2 = 256;
-
-// Unit shape of one call in a wave whose projection bytes total `wave_vbytes`
-// and whose fast outputs make `wave_fast_units` ordinary units (the rule
-// above).
-static UnitShape shape_in_wave(int32_t d, int32_t d_out, int32_t k, int es, int64_t wave_vbytes,
-                               int64_t wave_fast_units) {
-  const int64_t t = plan_proj_target(wave_vbytes);
-  const bool fine = wave_fast_units < kFineUnits;
-  const int64_t vi = (int64_t)d * k * es;
-  int64_t ti = std::max<int64_t>(t, (vi + kMaxPartials - 1) / kMaxPartials);
-  // Where the cap of kMaxPartials one-level partials would make the units
-  // larger than the wave's target and than kTwoLevelUnitBytes (a wide V_k in
-  // a latency-bound wave), up to kMaxPartials2 smaller units are summed in
-  // two levels instead.
-  if (ti > t && ti > kTwoLevelUnitBytes)
-    ti = std::max<int64_t>({t, kTwoLevelUnitBytes, (vi + kMaxPartials2 - 1) / kMaxPartials2});
-  return unit_shape(d, d_out, k, es, ti, fine);
-}
-
-// Unit shape of the n tokens of one map in the batch-1 kernels: the n tokens
-// are n calls of one wave, shaped as a stack plan would shape them (a few
-// tokens are latency-bound and take the small units).
-static UnitShape linear_shape(const gsi_map *map, int64_t n) {
-  const int es = esize_of(map->dtype);
-  const int64_t coarse = unit_shape(map->d, map->d_out, map->k, es, 1 << 20).fast_units;
-  return shape_in_wave(map->d, map->d_out, map->k, es, (int64_t)map->d * map->k * es * n, coarse * n);
-}
-
-static uint64_t linear_ws_bytes(const gsi_map *map, int64_t n) {
-  const UnitShape us = linear_shape(map, n);
-  return ws_layout(n, n * (us.g_floats + us.part_floats), 0, n * us.a_units).total;
-}
-
 // bf16 maps with two or more tokens take the batched MFMA path; fp32 maps
 // and single tokens take the batch-1 kernels.
 static bool use_batched(const gsi_map *map, int32_t T) { return map->dtype == GSI_BF16 && T >= 2; }
@@ -231,13 +152,7 @@ size_t gsi_linear_workspace(const gsi_map *map, int32_t T) {
     }
     return (size_t)need;
   }
-  // launches of kMaxCalls tokens, then one with the remainder
-  if (T >= kMaxCalls) need = linear_ws_bytes(map, kMaxCalls);
-  if (T % kMaxCalls) {
-    const uint64_t r = linear_ws_bytes(map, T % kMaxCalls);
-    if (r > need) need = r;
-  }
-  return (size_t)need;
+  return (size_t)linear_layout(map->d, map->d_out, map->k, esize_of(map->dtype), T).ws.total;
 }
 
 static gsi_status linear_batched(const gsi_map *map, const void *x, void *y, int32_t T, float eps,
@@ -295,10 +210,11 @@ gsi_status gsi_linear(const gsi_map *map, const void *x, void *y, int32_t T, flo
   if (use_batched(map, T)) return linear_batched(map, x, y, T, eps, mode, rho, slow, ws, st);
   // Tokens are processed in launches of at most kMaxCalls tokens; each
   // launch reuses the same workspace (stream order separates them).
+  const LinearLayout layout = linear_layout(map->d, map->d_out, map->k, es, T);
+  const WsLayout &wl = layout.ws;
   for (int32_t t0 = 0; t0 < T; t0 += kMaxCalls) {
     const int32_t n = (T - t0) < kMaxCalls ? (T - t0) : kMaxCalls;
-    const UnitShape us = linear_shape(map, n);
-    const WsLayout wl = ws_layout(n, n * (us.g_floats + us.part_floats), 0, n * us.a_units);
+    const UnitShape &us = layout.of(n);
     KArgs a{};
     a.table = nullptr;
     a.unit_call = nullptr;

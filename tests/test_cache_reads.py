@@ -16,7 +16,7 @@ HEAD = r"""
 #include <cstdio>
 #include <cstdlib>
 #include <vector>
-#include "gsi_attend_at.h"
+#include "@HEADER@"
 using namespace gsi;
 #define HOLD(what, ...)                                  \
   do {                                                   \
@@ -30,9 +30,10 @@ using namespace gsi;
 """
 
 
-def run(tmp_path, body):
+def run(tmp_path, body, header="gsi_attend_at.h"):
+    """The body of a main() over the functions of a header of the library."""
     source, program = tmp_path / "check.cpp", tmp_path / "check"
-    source.write_text(HEAD + "int main() {\n" + body + '\n  std::printf("held\\n");\n}\n')
+    source.write_text(HEAD.replace("@HEADER@", header) + "int main() {\n" + body + '\n  std::printf("held\\n");\n}\n')
     subprocess.run([COMPILER, "-std=c++17", "-O1", "-Wall", "-Wextra", "-Werror", "-I", CSRC, str(source), "-o",
                     str(program)], check=True, timeout=120)
     r = subprocess.run([str(program)], capture_output=True, text=True, timeout=120)
