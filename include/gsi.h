@@ -132,10 +132,20 @@ size_t gsi_linear_workspace(const gsi_map *map, int32_t T);
  *   ws  : device workspace of at least gsi_linear_workspace(map, T) bytes.
  *         It must be zero-filled before its first use; every call leaves
  *         its counters at zero again, so the same buffer can be reused by
- *         later calls on the same stream.  Calls that share a workspace
- *         must not run concurrently.
+ *         later calls of the same layout (below) on the same stream.  Calls
+ *         that share a workspace must not run concurrently.
  * T == 0 is a no-op returning GSI_OK.  Tokens are independent: the result
- * of a token does not depend on the other tokens of the batch. */
+ * of a token does not depend on the other tokens of the batch.
+ *
+ * A workspace serves one layout.  Where its counters lie goes by the sizes of
+ * the work: for gsi_linear by T and the map's d, d_out, k and dtype (not by its
+ * addresses, eps or mode), for a stack by these sizes, the waves and the shared
+ * projections of all its calls in their order.  Where one layout counts another
+ * keeps sums, and a kernel that counts on from sums gives wrong results or
+ * reads and writes outside its buffers.  So calls of different layouts (two
+ * maps of different sizes, a prompt and a token, two stacks) have a workspace
+ * each, or all of the buffer is zero-filled, in stream order, between a call of
+ * one layout and the next of another. */
 gsi_status gsi_linear(const gsi_map *map, const void *x, void *y, int32_t T, float eps,
                       int32_t mode, float *rho, uint8_t *slow, void *ws, size_t ws_bytes,
                       void *stream);
@@ -204,7 +214,8 @@ size_t gsi_stack_workspace(const void *plan_host);
 
 /* Run every call of a plan: plan_host is the host buffer gsi_stack_plan
  * filled, plan_dev a byte-identical device copy of it.  Same workspace
- * rules as gsi_linear.  Equivalent to gsi_linear(T = 1) on each call, in
+ * rules as gsi_linear: zero-filled before the first use, one layout, no two
+ * runs at once.  Equivalent to gsi_linear(T = 1) on each call, in
  * array order; the results are bitwise identical to the two-phase form
  * below for the same plan.  One persistent launch: the output work of a
  * call starts as soon as its own gate is decided, while other calls are

@@ -236,13 +236,18 @@ def gsi_linear_workspace(m: Map, T: int) -> int:
 
 
 def workspace(nbytes: int, device) -> torch.Tensor:
-    """A zero-filled workspace buffer (zero before first use, as gsi.h requires)."""
+    """A zero-filled workspace buffer (zero before first use, as gsi.h requires),
+    for calls of one layout: gsi_linear of one T and one size of map, or stacks of
+    the same sizes and waves.  For calls of another layout take another one, or
+    zero_() this one in between: where one layout counts, another keeps sums."""
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
 def gsi_linear(m: Map, x: torch.Tensor, eps: float, mode: int = GATED, y=None, rho=None,
                slow=None, ws=None, stream=None):
-    """Gated map on x [T][d]; returns (y [T][d_out], rho [T], slow [T] uint8)."""
+    """Gated map on x [T][d]; returns (y [T][d_out], rho [T], slow [T] uint8).
+    ws: a workspace() of gsi_linear_workspace(m, T) bytes, used before only by
+    calls of the same T and sizes of map, or zeroed since."""
     if x.dim() == 1:
         x = x[None]
     T = x.shape[0]
@@ -347,7 +352,9 @@ class StackIncomplete(RuntimeError):
 
 
 def gsi_stack(plan: Stack, mode: int, ws: torch.Tensor, stream=None, check: bool = False):
-    """Run a plan (one launch).  gsi_stack returns GSI_OK once the launch is
+    """Run a plan (one launch).  ws: a workspace() of plan.ws_bytes, used before
+    only by plans of the same sizes and waves, or zeroed since.  gsi_stack returns
+    GSI_OK once the launch is
     enqueued; whether every device-side wait finished is only known from the
     workspace's status word after the stream has run, which check=True
     reads (synchronising the stream) and turns into StackIncomplete."""
