@@ -513,8 +513,9 @@ size_t gsi_cache_attend_workspace(const gsi_cache *cache, const gsi_table *table
  *                weights over the query heads of its key head; no page is then
  *                named twice for slots in use, by one sequence or two
  * A sequence without slots (or with no page that there is, or whose scores all
- * are -inf) gives zeros, and lse -inf.  What lies behind the n slots is never
- * part of a result, whatever it holds.  Finite values overflow only where the
+ * are -inf) gives zeros, and lse -inf.  What lies before slot first and behind
+ * the n slots is never part of a result, whatever it holds, and pages without a
+ * slot in [first, n) are not read.  Finite values overflow only where the
  * result does; in turn a weight below 2^-80 of its head's largest may count as 0
  * (0 times an infinite value is NaN), and results of values below 2^-80 may
  * lose digits.  Needs `ws` of at least

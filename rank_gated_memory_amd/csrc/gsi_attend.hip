@@ -320,13 +320,14 @@ __global__ void __launch_bounds__(kThreads, KS <= 2 ? 3 : KS <= 4 ? 2 : 1) atten
 
   // The page numbers of this lane's keys and values, as the table has them: they
   // are checked where they are used, a step later, so that nothing waits for
-  // them here.  Slots behind the last read the last one's and are masked.
+  // them here.  Slots before the first and behind the last read those ones' and are
+  // masked.
   struct Where {
     uint32_t k, v;
   };
   const auto pages_of = [&](const Segment &g, int st) {
     const int32_t *const table = a.c.table + g.s * a.c.ld;
-    const auto page = [&](int t) { return (uint32_t)table[min(t, g.sp.n - 1) >> a.c.shift]; };
+    const auto page = [&](int t) { return (uint32_t)table[slot_in_use(t, g.sp.first, g.sp.n) >> a.c.shift]; };
     return Where{page(st * step + 8 * kblock), page(st * step + 8 * vblock)};
   };
   const auto start_of = [&](const Segment &g, uint32_t page, int t) {
@@ -722,7 +723,7 @@ __global__ void __launch_bounds__(kThreads) mass_kernel(AttendArgs a, Plan p, in
     const int kh = (int)over(in, of), strip = in - kh * of;
     const int i = (first / kMassSlots + strip) * kMassSlots + 4 * lane;
     const int64_t row0 = (int64_t)s * a.q.n + kh * a.group;
-    const int page = page_of(a.c, s, min(i, n - 1));
+    const int page = page_of(a.c, s, slot_in_use(i, first, n));
     float *const number = a.c.mass + number_at(a.c, max(page, 0), kh, i);
     f32x4_t mass = {0, 0, 0, 0}, add = {0, 0, 0, 0};
     if (own == 0) __builtin_memcpy(&mass, number, 16);

@@ -44,4 +44,11 @@ constexpr int value_slots(int es) { return es == 4 ? 4 : 8; }
 constexpr int value_block(int es, int quad) { return es == 4 ? quad >> 1 : quad; }
 constexpr int value_slot(int es, int quad) { return es == 4 ? 4 * (quad & 1) : 0; }
 
+// The slot whose page number is read for slot t, of the slots [first, n) in use: no
+// other's, and what is read there for a slot outside counts as nothing.
+constexpr int slot_in_use(int t, int first, int n) {
+  const int at = t > first ? t : first;
+  return at < n ? at : n - 1;
+}
+
 }  // namespace gsi

@@ -94,3 +94,19 @@ def test_a_step_reads_each_slot_once(tmp_path, es):
       ++values.at(8 * value_block(es, quad) + value_slot(es, quad) + e);
     }
   for (int t = 0; t < attend_step(es); ++t) HOLD(keys[t] == 1 && values[t] == 1, "slot %d", t);""")
+
+
+def test_page_numbers_are_read_of_slots_in_use_alone(tmp_path):
+    """Steps (of attention) and strips of 256 slots (of the mass) begin before a
+    window and end behind a sequence: what they look up lies within."""
+    run(tmp_path, r"""
+  for (int n = 1; n < 700; n += n < 40 ? 1 : 37)
+    for (int window = 0; window < n + 2; window += window < 40 ? 1 : 41) {
+      const int first = window > 0 && n > window ? n - window : 0;
+      for (const int unit : {attend_step(2), attend_step(4), 256})
+        for (int t = first / unit * unit; t < n + 3 * unit; ++t) {
+          const int at = slot_in_use(t, first, n);
+          HOLD(first <= at && at < n, "slot %d for slot %d of %d to %d", at, t, first, n);
+          HOLD(t < first || t >= n || at == t, "slot %d for slot %d of %d to %d", at, t, first, n);
+        }
+    }""")
