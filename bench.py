@@ -660,9 +660,12 @@ def bench_cache(args):
     over its 2049 entries with the weights kept (gsi_cache_attend), the cache
     cut back to 2048, the newest 512 of them for certain (gsi_cache_evict), and
     the gated out and fc_out maps, out from attention's output (one gsi_stack
-    launch).  All layers are one HIP graph, replayed; positions and the tables
-    stay as they are, the caches go on from step to step.  Beside it the same
-    graph without the cache's calls, and the cache's calls alone.
+    launch).  All layers are one HIP graph, replayed; the position goes up by one
+    at every step and with it the new entries' ages, the tables stay as they are,
+    the caches go on from step to step.  So the new entry is always the newest, and
+    every key head moves it into the place of the one that is given up: the moves
+    of the last step are counted.  Beside it the same graph without the cache's
+    calls, and the cache's calls alone.
     """
     import torch
 
@@ -698,6 +701,7 @@ def bench_cache(args):
     ws_first, ws_second = (gsi.workspace(work[0][k].ws_bytes, dev) for k in range(2))
 
     def step(with_maps, with_cache):
+        sources = []
         for first, second, cache, y, att in work:
             if with_maps:
                 gsi.gsi_stack(first, gsi.GATED, ws_first)
@@ -706,17 +710,21 @@ def bench_cache(args):
                 q = gsi.gsi_cache_append(cache, table, slots, qkv[:, heads:2 * heads], qkv[:, 2 * heads:], rotary=rotary,
                                          positions=positions, q=qkv[:, :heads])
                 gsi.gsi_cache_attend(cache, table, lengths, q, accumulate=True, out=att.view(1, heads, d))
-                gsi.gsi_cache_evict(cache, table, lengths, budget, recent=recent)
+                sources.append(gsi.gsi_cache_evict(cache, table, lengths, budget, recent=recent)[1])
             if with_maps:
                 gsi.gsi_stack(second, gsi.GATED, ws_second)
+        if with_cache:
+            positions.add_(1)
+        return sources
 
-    times = {}
+    times, moves = {}, {}
+    stays = torch.arange(budget, dtype=torch.int32, device=dev)
     for name, what in (("step", (True, True)), ("maps alone", (True, False)), ("cache alone", (False, True))):
         step(*what)
         torch.cuda.synchronize()
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
-            step(*what)
+            sources = step(*what)
         for _ in range(args.warmup):
             graph.replay()
         torch.cuda.synchronize()
@@ -726,7 +734,9 @@ def bench_cache(args):
         torch.cuda.synchronize()
         times[name] = (time.perf_counter() - t0) * 1e6 / args.steps
         log(f"{name}: {times[name]:.1f} us per step of {layers} layers")
-        del graph
+        if sources:
+            moves[name] = sum(int((s != stays).sum()) for s in sources)
+        del graph, sources
     status = max(work[0][0].status(ws_first), work[0][1].status(ws_second))
     finite = all(bool(torch.isfinite(t).all()) for w in work for t in (*w[3], w[4]))
     read = layers * (budget + 1) * heads * (2 * d * 2 + 8)
@@ -736,11 +746,12 @@ def bench_cache(args):
         "unit": "tokens/s", "n_gpus": 1, "steps": args.steps, "warmup": args.warmup, "ms_per_step": times["step"] / 1e3,
         "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
         "config": {"workload": f"gptj6b-28L-cache: {layers} layers, 16 heads of 256, 64 elements turned in pairs, pages of "
-                               f"{page}, 2049 entries cut to 2048 at every step and layer", "us_per_step": times},
+                               f"{page}, 2049 entries cut to 2048 at every step and layer", "us_per_step": times,
+                   "entries_moved": moves},
         "roofline": {"bound": "hbm", "kernel": "attend_kernel and the calls around it", "achieved": gbps,
                      "peak": PEAK_HBM_GBPS, "unit": "GB/s", "frac": gbps / PEAK_HBM_GBPS, "traffic": None},
         "status": status, "finite": finite}), flush=True)
-    if status or not finite:
+    if status or not finite or any(n != layers * heads for n in moves.values()):
         sys.exit(3)
 
 
