@@ -799,9 +799,6 @@ Plan plan_of(const Pool &c, int q_heads, bool accumulate, uint8_t *ws, size_t *b
 template <typename E>
 gsi_status launch_as(const AttendArgs &a, hipStream_t st) {
   const Plan p = plan_of<E>(a.c, a.q.n, a.accumulate, a.ws, nullptr);
-  // units of 64 slots or more, one of a sequence at least, cost two, and a row one:
-  // that of a key head is counted in 32 bits
-  if ((((int64_t)a.c.most << a.c.shift) / 32 + 3) * a.c.S > INT32_MAX) return GSI_E_SHAPE;
   const unsigned grid = (p.shares + 7) / 8 * 8 * p.tiles;
   const auto go = [&](auto ks) {
     attend_kernel<E, decltype(ks)::value><<<grid, kThreads, 0, st>>>(a, p);
@@ -846,6 +843,10 @@ gsi_status launch_as(const AttendArgs &a, hipStream_t st) {
 }
 
 }  // namespace
+
+// Units of 64 slots or more, one of a sequence at least, cost two, and a row one: that
+// of a key head is counted in 32 bits.
+bool attend_counts(const Pool &c) { return (((int64_t)c.most << c.shift) / 32 + 3) * c.S <= INT32_MAX; }
 
 size_t attend_workspace(const Pool &c, int dtype, int q_heads, bool accumulate) {
   size_t bytes = 0;

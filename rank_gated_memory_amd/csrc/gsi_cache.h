@@ -65,6 +65,7 @@ struct EvictArgs {
 };
 
 gsi_status launch_rotate(const RotateArgs &a, int dtype, int layout, hipStream_t st);
+bool attend_counts(const Pool &c);  // whether there are no more slots than are counted
 size_t attend_workspace(const Pool &c, int dtype, int q_heads, bool accumulate);
 gsi_status launch_attend(const AttendArgs &a, int dtype, hipStream_t st);
 gsi_status launch_evict(const EvictArgs &a, int dtype, hipStream_t st);

@@ -172,7 +172,8 @@ size_t gsi_cache_attend_workspace(const gsi_cache *cache, const gsi_table *table
                                   int32_t accumulate) {
   if (check_cache(cache) != GSI_OK || check_table(table, cache->page) != GSI_OK) return 0;
   if (q_heads < 1 || q_heads > 4096 || q_heads % cache->heads) return 0;
-  return attend_workspace(pool_of(cache, table), cache->dtype, q_heads, accumulate != 0);
+  const Pool pool = pool_of(cache, table);
+  return attend_counts(pool) ? attend_workspace(pool, cache->dtype, q_heads, accumulate != 0) : 0;
 }
 
 gsi_status gsi_cache_attend(const gsi_cache *cache, const gsi_table *table, const int32_t *lengths,
@@ -191,6 +192,7 @@ gsi_status gsi_cache_attend(const gsi_cache *cache, const gsi_table *table, cons
   if (!lengths) return GSI_E_NULL;
   AttendArgs a{};
   a.c = pool_of(cache, table);
+  if (!attend_counts(a.c)) return GSI_E_SHAPE;
   const size_t need = attend_workspace(a.c, cache->dtype, q->n, accumulate != 0);
   if (need > 0 && !ws) return GSI_E_NULL;
   if (ws_bytes < need) return GSI_E_WORKSPACE;

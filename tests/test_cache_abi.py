@@ -170,6 +170,21 @@ def test_attend_refuses_more_slots_than_it_counts():
     assert attend(t=table(S=1 << 20, most=1 << 13, ld=1 << 13), ws_bytes=2**63) == E_SHAPE
 
 
+@pytest.mark.parametrize("S,most,page", [((1 << 24) - 1, 1 << 10, 16), (1 << 20, 1 << 13, 16), ((1 << 24) - 1, 1 << 18, 4096)])
+def test_no_workspace_for_more_slots_than_it_counts(S, most, page):
+    """Sizes that the call refuses, whatever workspace it is given, and whose scores
+    would be 2^64 bytes and more."""
+    c, t = cache(page=page, ps=page * 128), table(S=S, most=most, ld=most)
+    q = heads(row=4096 * 64, n=4096)
+    assert gsi.lib().gsi_cache_attend_workspace(REF(c), REF(t), 4096, 1) == 0
+    for size in (0, 1 << 40, 2**63):
+        assert attend(c=c, t=t, q=q, out=q, accumulate=1, ws_bytes=size) == E_SHAPE
+    most = ((2**31 - 1) // S - 3) * 32 // page  # the most that is counted
+    t = table(S=S, most=most, ld=most)
+    need = gsi.lib().gsi_cache_attend_workspace(REF(c), REF(t), 4096, 1)
+    assert need >= S * 4096 * most * page * 4 and attend(c=c, t=t, q=q, out=q, accumulate=1, ws_bytes=need - 1) == E_WS
+
+
 def test_evict_refuses():
     assert evict(c=None) == E_NULL and evict(t=None) == E_NULL and evict(lengths=None) == E_NULL
     assert evict(source=None) == E_NULL and evict(c=cache(mass=None)) == E_NULL
