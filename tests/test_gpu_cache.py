@@ -644,6 +644,67 @@ def test_attend_values_near_the_largest(d, dtype):
             check_against_plain(c, table, lengths, q, f"values of 2^{k}", least=0.0 if k else 1e-30)
 
 
+def single_weights(g, dtype, lens, d=256):
+    """A pool whose slot i has the value e_i, and queries with one element each: out
+    is the weights themselves, and a score a single product.  (cache, table, lengths,
+    q, weights in 64 bits)"""
+    c, table = make_pool(g, len(lens), lens, 1, 32, d, dtype, most=d // 32)
+    q = torch.zeros(len(lens), 3, d, device=DEV, dtype=dtype)
+    q[:, :, 5] = torch.tensor([0.3, -0.7, 1.0], device=DEV, dtype=dtype)
+    weights = np.zeros((len(lens), 3, d))
+    for s, n in enumerate(lens):
+        i = torch.arange(n, device=DEV)
+        at, off = table[s].long()[i // 32], i % 32
+        k = (6 * torch.rand(n, generator=g, device=DEV) - 3).to(dtype)  # scores of at most 3
+        c.K[at, 0, off] = torch.randn(n, d, generator=g, device=DEV).to(dtype)
+        c.K[at, 0, off, 5] = k
+        c.V[at, 0, off] = torch.eye(d, device=DEV, dtype=dtype)[:n]
+        e = np.exp(f64(q[s, :, 5])[:, None] * f64(k)[None])
+        weights[s, :, :n] = e / e.sum(1, keepdims=True)
+    c.mass.zero_()
+    return c, table, torch.tensor(lens, device=DEV, dtype=torch.int32), q, weights
+
+
+# A score is one product (2^-24 of it), times log2 e (rounded itself) rounded: off by 3
+# x 2^-24 |s|, |s| <= 3, and by 2^-24 |s - top| <= 6 x 2^-24 where the maximum is taken
+# off: 15 x 2^-24; the exponential by 2^-23 more: 17 in all, of a weight and of each in
+# the weights' sum.  That sum of n <= 256 takes a term through 4 additions a step of
+# one to four steps, 2 across lanes and 4 across wavefronts: 22.  Times a power of two,
+# the other wavefronts' factor (2^-23 and 17 as above), the quotient (three roundings) and
+# the sum with zeros: 24.  17 + 17 + 22 + 24 = 80.
+WEIGHT = 80 * 2.0**-24
+
+
+def test_attend_fp32_weights_have_all_their_digits():
+    """Weights of which no more than a handful of roundings are lost: that they are
+    not held in the 16 digits of two bf16 numbers, which the sums' bounds allow."""
+    g = gen(71)
+    lens = [1, 2, 3, 17, 64, 65, 200, 256]
+    c, table, lengths, q, p = single_weights(g, F32, lens)
+    out, _ = gsi.gsi_cache_attend(c, table, lengths, q, scale=1.0)
+    within(out, p, WEIGHT * p, "weights")
+    # the bound sees what it is there for: the same weights with 16 digits
+    cut = (p * 2.0**16 / 2.0**np.floor(np.log2(p, where=p > 0, out=np.zeros_like(p)))).round() / 2.0**16 \
+        * 2.0**np.floor(np.log2(p, where=p > 0, out=np.zeros_like(p)))
+    assert (np.abs(cut - p) > WEIGHT * p).any()
+
+
+@DTYPES
+def test_attend_mass_has_all_its_digits(dtype):
+    """What is added to the mass, in both types: three heads' weights, each from its
+    score and the softmax's level (their sizes at most 3 + log 256 = 8.6, times log2 e
+    13, each rounded where it is written and taken off: 40 x 2^-24 more), added up."""
+    g = gen(72)
+    lens = [1, 2, 3, 17, 64, 65, 200, 256]
+    c, table, lengths, q, p = single_weights(g, dtype, lens)
+    gsi.gsi_cache_attend(c, table, lengths, q, scale=1.0, accumulate=True)
+    for s, n in enumerate(lens):
+        i = torch.arange(n, device=DEV)
+        got = c.mass[table[s].long()[i // 32], 0, i % 32]
+        want = p[s, :, :n].sum(0)
+        within(got, want, (WEIGHT + 44 * 2.0**-24) * want, f"mass of {n}")
+
+
 @DTYPES
 def test_attend_strides_and_what_is_left(dtype):
     g = gen(14)
