@@ -407,6 +407,12 @@ gsi_status gsi_group_combine(const void *y, int64_t ldy, int32_t R, const int32_
  * table[s * ld + i / page].  A page number outside [0, pages) holds nothing:
  * nothing is read from it or written to it, attention leaves its slots out.
  * Table entries of slots that a call does not use are not read.
+ * The lengths are on the device, and the host goes by the table's width: the
+ * scores that gsi_cache_attend keeps to accumulate take S * query heads * most *
+ * page * 4 bytes of workspace, and gsi_cache_evict takes the form for most * page
+ * slots, in which few entries of a wide table take longer.  A program that knows a
+ * bound on the lengths gives the table with the `most` that holds it, and the ld
+ * that it has.
  * 0 <= S < 2^24, 0 <= most, most * page <= 2^30, ld >= most.
  *
  * Conventions beside those at the top

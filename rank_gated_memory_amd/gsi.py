@@ -813,7 +813,9 @@ def gsi_cache_attend(c: Cache, table: torch.Tensor, lengths: torch.Tensor, q: to
     lengths[s] slots of its pages, or the last `window` of them: (out like q,
     lse [S][q heads] fp32).  scale None is d^-0.5.  accumulate adds each slot's
     weights to the cache's mass.  ws: device memory of
-    gsi_cache_attend_workspace() bytes with any contents."""
+    gsi_cache_attend_workspace() bytes with any contents; with accumulate it goes
+    by the table's width: table[:, :m], of the pages that the longest sequence
+    needs, asks for less."""
     dtype, dev, d = c.dtype, c.device, c.d
     hq = _heads(q, "q", dtype, dev, d)
     S, n = q.shape[0], hq.n
@@ -856,7 +858,9 @@ def gsi_cache_evict(c: Cache, table: torch.Tensor, lengths: torch.Tensor, budget
     """Cut every sequence of more than `budget` entries to it: each key head keeps
     its `recent` newest entries and those of the largest mass, in place or, with
     `to` [S][most'], copied into other pages of the pool.  Returns (lengths_out
-    [S], moved [S][heads][budget]: the slot each slot's entry came from, or -1)."""
+    [S], moved [S][heads][budget]: the slot each slot's entry came from, or -1).
+    The call goes by the table's width: table[:, :m], of the pages that the longest
+    sequence needs, is faster than a wide one."""
     dev = c.device
     pages = _table(table, "table", dev)
     S = pages.S

@@ -899,6 +899,26 @@ def test_evict_of_sequences_beyond_a_wavefront():
     check_evict(c, table, torch.tensor(lens, device=DEV, dtype=torch.int32), 33, 10, what="many sequences")
 
 
+def test_a_narrower_view_of_a_wide_table():
+    """The pages that the longest sequence needs, as a view: the same choice of an
+    eviction, attention within its bounds, and a workspace by the view's width."""
+    g = gen(81)
+    lens = [300, 17, 0, 130]
+    lengths = torch.tensor(lens, device=DEV, dtype=torch.int32)
+    c, table = make_pool(g, 4, lens, 2, 16, 64, BF16, most=2500)
+    narrow = table[:, :19]
+    assert narrow.stride(0) == 2500
+    wide_bytes, narrow_bytes = (gsi.gsi_cache_attend_workspace(c, t, 4, True) for t in (table, narrow))
+    assert wide_bytes > 100 * 4 * 4 * 19 * 16 * 4 and narrow_bytes < wide_bytes / 10
+    q = torch.randn(4, 4, 64, generator=g, device=DEV).to(BF16)
+    check_attend(c, narrow, lengths, q, accumulate=True, what="narrow")
+    copies = [gsi.Cache(*(t.clone() for t in (c.K, c.V, c.mass, c.age))) for _ in range(2)]
+    check_evict(copies[0], narrow, lengths, 100, 20, what="narrow")
+    check_evict(copies[1], table, lengths, 100, 20, what="wide")
+    for name in ("K", "V", "mass"):
+        assert torch.equal(bits(getattr(copies[0], name)), bits(getattr(copies[1], name))), name
+
+
 # ---- the operators together ----
 
 
