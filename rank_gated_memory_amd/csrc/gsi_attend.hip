@@ -31,13 +31,13 @@
 // at 16 B a clock and CU from HBM the matrix cores are at 5 % (bf16) or 30 %
 // (fp32) of their rate even then.  The workgroups of a share's tiles run on one
 // XCD at one time, so that one of them reads from HBM and all from its L2: 64
-// sequences of 2000 slots, 8 key heads for 256, 524 MB, 115 us (16 query heads for
-// each key head: 98; with the tiles one after the other 190).  Two tiles in one
+// sequences of 2000 slots, 8 key heads for 256, 524 MB, 121 us (16 query heads for
+// each key head: 103; with the tiles one after the other 190).  Two tiles in one
 // workgroup's registers: 64 sequences of 2000 slots, one key head for 32, 39 us, in
-// two workgroups 28.
+// two workgroups 28 then and 25 now.
 //
 // Bound by HBM where the lengths fill the chip: two sequences of 131071 slots, 8
-// heads of 128, 537 MB in 98 us, 5.5 TB/s; 64 of 1 to 4096 slots, 40 heads of 128,
+// heads of 128, 537 MB in 95 us, 5.7 TB/s; 64 of 1 to 4096 slots, 40 heads of 128,
 // 700 MB in 143 us with the scores kept, 4.9.  One sequence of 1777 slots of 16
 // heads of 256, 29 MB, takes 12 us and 4 for the join: a launch's latency, a
 // length's, a page number's, and the keys' and values' own.
