@@ -440,7 +440,7 @@ def test_attend_more_sequences_than_a_wavefront_counts(window):
     assert not bool((off & ~torch.isnan(before)).any()) and torch.equal(torch.isnan(before), torch.isnan(c.mass))
 
 
-def check_against_plain(c, table, lengths, q, what, least=1e-30):
+def check_against_plain(c, table, lengths, q, what):
     """Held to plain_attend; n / 16 + 64 additions of a chain at most, as in check_attend."""
     d = c.d
     ref, lse, _, size, big = (t.cpu().numpy() for t in plain_attend(c, table, lengths, q, d**-0.5))
@@ -448,7 +448,7 @@ def check_against_plain(c, table, lengths, q, what, least=1e-30):
     delta = (d + 8) * 2.0**-24 * big + (2 * big + 8) * 2.0**-23
     chain = (max(int(lengths.max()), 1) / 16 + 64) * 2.0**-23
     rel = 2 * delta + 2.0**-16 + chain
-    within(out, ref, half(c.dtype) * np.abs(ref) * 1.001 + size * rel[:, :, None] * 1.01 + least, what)
+    within(out, ref, half(c.dtype) * np.abs(ref) * 1.001 + size * rel[:, :, None] * 1.01 + 1e-30, what)
     within(l, lse, delta + chain + 2.0**-22 + 2.0**-22 * np.abs(np.where(np.isfinite(lse), lse, 0.0)), what + " lse")
 
 
@@ -641,7 +641,14 @@ def test_attend_values_near_the_largest(d, dtype):
     for values in (V, V.abs()):  # signs that cancel, and sums of n values
         for k in (0, 126, 121, -100):
             c.V.copy_(values.double() * 2.0**k)
-            check_against_plain(c, table, lengths, q, f"values of 2^{k}", least=0.0 if k else 1e-30)
+            ref, lse, _, size, big = (t.cpu().numpy() for t in plain_attend(c, table, lengths, q, d**-0.5))
+            out, l = gsi.gsi_cache_attend(c, table, lengths, q)
+            # as in check_attend, but for its 1e-30
+            delta = (d + 8) * 2.0**-24 * big + (2 * big + 8) * 2.0**-23
+            chain = (max(lens) / 16 + 64) * 2.0**-23
+            rel = 2 * delta + 2.0**-16 + chain
+            within(out, ref, half(dtype) * np.abs(ref) * 1.001 + size * rel[:, :, None] * 1.01, f"values of 2^{k}")
+            within(l, lse, delta + chain + 2.0**-22 + 2.0**-22 * np.abs(np.where(np.isfinite(lse), lse, 0.0)), "lse")
 
 
 def single_weights(g, dtype, lens, d=256):
